@@ -21,10 +21,13 @@ LIB_PATH = os.path.join(_HERE, "libep_mi355x.so")
 EP_OK = 0
 EP_DTYPE_BF16 = 0
 EP_DTYPE_FP8_E4M3 = 1
+EP_DTYPE_FP32 = 2
+SCORES = {"softmax": 0, "sigmoid": 1}
 MAX_EXPERTS = 1024
 MAX_TOPK = 64
 LL_MAX_SLOTS = 8192
 MAX_EXPERT_ALIGNMENT = 1024
+MAX_ROUTE_GROUPS = 64
 
 
 class EpError(RuntimeError):
@@ -38,6 +41,7 @@ _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
 _sz = ctypes.c_size_t
+_f32 = ctypes.c_float
 
 SIGNATURES = {
     "ep_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32]),
@@ -65,6 +69,15 @@ SIGNATURES = {
                                          _vp, _vp, _sz, _vp]),
     "ep_low_latency_dispatch": (ctypes.c_int, [_vp, _i32, _i32, _vp, _i32, _i32, _i32,
                                                ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "ep_combine_backward": (ctypes.c_int, [_vp, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _vp, _vp,
+                                           _vp]),
+    "ep_dispatch_backward": (ctypes.c_int, [_vp, _i64, _vp, _i32, _i32, _i32, _vp, _vp]),
+    "ep_route": (ctypes.c_int, [_vp, ctypes.c_int, _vp, _i32, _i32, _i32, ctypes.c_int, _i32,
+                                _i32, _i32, _f32, _vp, _vp, _vp]),
+    "ep_route_backward": (ctypes.c_int, [_vp, ctypes.c_int, _vp, _vp, _i32, _i32, _i32,
+                                         ctypes.c_int, _i32, _f32, _vp, _vp]),
+    "ep_expert_linear_w4": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _i64, _vp, _vp, _i32, _i32,
+                                           _i32, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _vp]),
     "ep_get_device_error": (ctypes.c_int, [_vp, _sz, ctypes.POINTER(_i64), _vp]),
     "ep_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "ep_convert_e4m3": (ctypes.c_int, [_vp, _vp, _i64, _i32, _vp]),
@@ -550,6 +563,206 @@ def combine(y: torch.Tensor, dst_row: torch.Tensor, topk_weights: torch.Tensor,
     _need(out, torch.bfloat16, "out", (T, H), device=dev)
     _check(lib().ep_combine_cu(_ptr(y), y.shape[0], _ptr(dst_row), _ptr(topk_weights), T, K, H,
                                _ptr(out), int(num_cus), _stream(y)), "ep_combine_cu")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# gradients of dispatch and combine
+# ---------------------------------------------------------------------------
+
+def _launch(name: str, t: torch.Tensor, *args):
+    """Call ``name`` with ``args`` and torch's current stream on t's device,
+    with that device current."""
+    fn = getattr(lib(), name)
+    if t.device.index == torch.cuda.current_device():
+        status = fn(*args, _stream(t))
+    else:
+        with torch.cuda.device(t.device):
+            status = fn(*args, _stream(t))
+    _check(status, name)
+
+
+def combine_backward(grad_out: torch.Tensor, y: torch.Tensor | None, dst_row: torch.Tensor,
+                     topk_weights: torch.Tensor | None, out=None, num_rows: int | None = None):
+    """ep_combine_backward: from grad_out [T, H] bf16 the gradients of
+    combine(y, dst_row, topk_weights): (grad_y [R, H] bf16, grad_weights
+    [T, K] float32), or the ones given in ``out``.  Rows of grad_y that no slot
+    names are left as they are (a grad_y not given is allocated
+    uninitialised).  Without ``topk_weights`` only grad_weights is computed,
+    without ``y`` only grad_y (with ``num_rows`` rows if it is allocated here);
+    the other one is None."""
+    if grad_out.dim() != 2 or dst_row.dim() != 2 or (y is not None and y.dim() != 2):
+        raise ValueError("grad_out must be [T, H], y [R, H] and dst_row [T, K]")
+    T, K = dst_row.shape
+    H = grad_out.shape[1]
+    dev = grad_out.device
+    _need(grad_out, torch.bfloat16, "grad_out", (T, H), device=dev)
+    _need(dst_row, torch.int32, "dst_row", device=dev)
+    grad_y, grad_weights = (None, None) if out is None else out
+    if y is None and topk_weights is None:
+        raise ValueError("combine_backward needs y or topk_weights")
+    if y is not None:
+        num_rows = y.shape[0]
+    elif grad_y is not None:
+        num_rows = grad_y.shape[0]
+    elif num_rows is None:
+        raise ValueError("combine_backward without y needs num_rows or a grad_y in out")
+    R = int(num_rows)
+    if y is not None:
+        _need(y, torch.bfloat16, "y", (R, H), device=dev)
+        if grad_weights is None:
+            grad_weights = torch.empty((T, K), dtype=torch.float32, device=dev)
+        _need(grad_weights, torch.float32, "grad_weights", (T, K), device=dev)
+    elif grad_weights is not None:
+        raise ValueError("grad_weights needs y")
+    if topk_weights is not None:
+        _need(topk_weights, torch.float32, "topk_weights", (T, K), device=dev)
+        if grad_y is None:
+            grad_y = torch.empty((R, H), dtype=torch.bfloat16, device=dev)
+        _need(grad_y, torch.bfloat16, "grad_y", (R, H), device=dev)
+    elif grad_y is not None:
+        raise ValueError("grad_y needs topk_weights")
+    _launch("ep_combine_backward", grad_out, _ptr(grad_out), _ptr(y), R, _ptr(dst_row),
+            _ptr(topk_weights), T, K, H, _ptr(grad_y), _ptr(grad_weights))
+    return grad_y, grad_weights
+
+
+def dispatch_backward(grad_recv_x: torch.Tensor, dst_row: torch.Tensor,
+                      out: torch.Tensor | None = None) -> torch.Tensor:
+    """ep_dispatch_backward: from grad_recv_x [R, H] bf16, laid out like the
+    receive rows, the gradient of dispatch's x: grad_x [T, H] bf16."""
+    if grad_recv_x.dim() != 2 or dst_row.dim() != 2:
+        raise ValueError("grad_recv_x must be [R, H] and dst_row [T, K]")
+    T, K = dst_row.shape
+    R, H = grad_recv_x.shape
+    dev = grad_recv_x.device
+    _need(grad_recv_x, torch.bfloat16, "grad_recv_x", device=dev)
+    _need(dst_row, torch.int32, "dst_row", device=dev)
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    _need(out, torch.bfloat16, "out", (T, H), device=dev)
+    _launch("ep_dispatch_backward", grad_recv_x, _ptr(grad_recv_x), R, _ptr(dst_row), T, K, H,
+            _ptr(out))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# router
+# ---------------------------------------------------------------------------
+
+def _logits_dtype(logits: torch.Tensor) -> int:
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("logits must be float32 or bfloat16, got %s" % logits.dtype)
+    _need(logits, logits.dtype, "logits", device=logits.device)
+    return EP_DTYPE_FP32 if logits.dtype == torch.float32 else EP_DTYPE_BF16
+
+
+def _score(score: str) -> int:
+    if score not in SCORES:
+        raise ValueError("score must be one of %s, got %r" % (sorted(SCORES), score))
+    return SCORES[score]
+
+
+def route(logits: torch.Tensor, num_topk: int, expert_bias: torch.Tensor | None = None,
+          score: str = "softmax", num_groups: int = 1, topk_groups: int = 1,
+          normalize: bool = False, scale: float = 1.0, out=None):
+    """ep_route: logits [T, E] float32 or bf16 -> (topk_idx [T, K] int64,
+    topk_weights [T, K] float32), the arguments of the dispatch calls and of
+    combine.  ``out`` = (topk_idx, topk_weights) may be given."""
+    dt = _logits_dtype(logits)
+    T, E = logits.shape
+    K = int(num_topk)
+    dev = logits.device
+    if expert_bias is not None:
+        _need(expert_bias, torch.float32, "expert_bias", (E,), device=dev)
+    if out is None:
+        out = (torch.empty((T, K), dtype=torch.int64, device=dev),
+               torch.empty((T, K), dtype=torch.float32, device=dev))
+    idx, w = out
+    _need(idx, torch.int64, "topk_idx", (T, K), device=dev)
+    _need(w, torch.float32, "topk_weights", (T, K), device=dev)
+    _launch("ep_route", logits, _ptr(logits), dt, _ptr(expert_bias), T, E, K, _score(score),
+            int(num_groups), int(topk_groups), int(bool(normalize)), float(scale), _ptr(idx),
+            _ptr(w))
+    return idx, w
+
+
+def route_backward(logits: torch.Tensor, topk_idx: torch.Tensor, grad_weights: torch.Tensor,
+                   score: str = "softmax", normalize: bool = False, scale: float = 1.0,
+                   out: torch.Tensor | None = None) -> torch.Tensor:
+    """ep_route_backward: the gradient of route's topk_weights with respect to
+    its logits, [T, E] in their type."""
+    dt = _logits_dtype(logits)
+    T, E = logits.shape
+    dev = logits.device
+    if topk_idx.dim() != 2:
+        raise ValueError("topk_idx must be [T, K]")
+    K = topk_idx.shape[1]
+    _need(topk_idx, torch.int64, "topk_idx", (T, K), device=dev)
+    _need(grad_weights, torch.float32, "grad_weights", (T, K), device=dev)
+    if out is None:
+        out = torch.empty_like(logits)
+    _need(out, logits.dtype, "out", (T, E), device=dev)
+    _launch("ep_route_backward", logits, _ptr(logits), dt, _ptr(topk_idx), _ptr(grad_weights), T,
+            E, K, _score(score), int(bool(normalize)), float(scale), _ptr(out))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# experts
+# ---------------------------------------------------------------------------
+
+def expert_linear_w4(x: torch.Tensor, weight: torch.Tensor, scales: torch.Tensor,
+                     num_tokens_per_expert: torch.Tensor,
+                     expert_offsets: torch.Tensor | None = None, capacity: int = 0,
+                     x_scales: torch.Tensor | None = None, zeros: torch.Tensor | None = None,
+                     swiglu: bool = False, out: torch.Tensor | None = None) -> torch.Tensor:
+    """ep_expert_linear_w4: the experts' products over the rows of a dispatch.
+
+    x is [R, I] bf16, or uint8 E4M3 codes with x_scales [R, I/128]; weight
+    uint8 [E, W, I/2], scales bf16 [E, I/G, W], zeros uint8 [E, I/G, W] or
+    None, W = N, or 2N with swiglu.  The rows are those of a dispatch with
+    offsets (expert_offsets [E+1] and the counts of its Layout) or of a
+    low_latency_dispatch (its counts and ``capacity``).  Returns y [R, N]
+    bf16; rows that hold no token are left as they are (an ``out`` not given
+    is allocated uninitialised)."""
+    if x.dim() != 2 or weight.dim() != 3 or scales.dim() != 3:
+        raise ValueError("x must be [R, I], weight [E, W, I/2] and scales [E, I/G, W]")
+    R, I = x.shape
+    E, W = weight.shape[0], weight.shape[1]
+    NG = scales.shape[1]
+    dev = x.device
+    if swiglu and W % 2 != 0:
+        raise ValueError("swiglu needs an even number of weight channels, got %d" % W)
+    N = W // 2 if swiglu else W
+    if I % 2 != 0 or NG == 0 or I % NG != 0:
+        raise ValueError("scales must hold I/G groups: I = %d, groups = %d" % (I, NG))
+    fp8 = x.dtype == torch.uint8
+    _need(x, torch.uint8 if fp8 else torch.bfloat16, "x", device=dev)
+    if fp8:
+        if x_scales is None:
+            raise ValueError("E4M3 codes need x_scales")
+        _need(x_scales, torch.float32, "x_scales", (R, I // 128), device=dev)
+    elif x_scales is not None:
+        raise ValueError("x_scales belong to E4M3 codes (uint8 x)")
+    _need(weight, torch.uint8, "weight", (E, W, I // 2), device=dev)
+    _need(scales, torch.bfloat16, "scales", (E, NG, W), device=dev)
+    if zeros is not None:
+        _need(zeros, torch.uint8, "zeros", (E, NG, W), device=dev)
+    _need(num_tokens_per_expert, torch.int32, "num_tokens_per_expert", (E,), device=dev)
+    if expert_offsets is not None:
+        if capacity:
+            raise ValueError("give expert_offsets or capacity, not both")
+        _need(expert_offsets, torch.int32, "expert_offsets", (E + 1,), device=dev)
+    if out is None:
+        out = torch.empty((R, N), dtype=torch.bfloat16, device=dev)
+    _need(out, torch.bfloat16, "out", (R, N), device=dev)
+    _launch("ep_expert_linear_w4", x, _ptr(x), _ptr(x_scales),
+            EP_DTYPE_FP8_E4M3 if fp8 else EP_DTYPE_BF16, R, _ptr(expert_offsets),
+            _ptr(num_tokens_per_expert), int(capacity), E, I, N, I // NG, _ptr(weight),
+            _ptr(scales), _ptr(zeros), int(bool(swiglu)), _ptr(out))
     return out
 
 

@@ -356,6 +356,140 @@ ep_status_t ep_combine(const void* y, int64_t num_rows, const int32_t* dst_row,
                          stream);
 }
 
+ep_status_t ep_combine_backward(const void* grad_out, const void* y, int64_t num_rows,
+                                const int32_t* dst_row, const float* topk_weights,
+                                int32_t num_tokens, int32_t num_topk, int32_t hidden,
+                                void* grad_y, float* grad_weights, void* stream) {
+    const int32_t T = num_tokens, K = num_topk, H = hidden;
+    if (T < 0 || K <= 0 || H <= 0 || H % 8 != 0 || num_rows < 0) return EP_ERR_INVALID_ARG;
+    if ((int64_t)T * K >= kMaxRows) return EP_ERR_INVALID_ARG;
+    if (K > EP_MAX_TOPK) return EP_ERR_UNSUPPORTED;
+    if (T > 0) {
+        // without rows every slot is skipped: grad_y and y may then be empty
+        if (!grad_out || !dst_row || (!grad_weights && !grad_y)) return EP_ERR_INVALID_ARG;
+        if (grad_y && !topk_weights) return EP_ERR_INVALID_ARG;
+        if (grad_weights && num_rows > 0 && !y) return EP_ERR_INVALID_ARG;
+        if (!aligned16(grad_out) || (y && !aligned16(y)) || (grad_y && !aligned16(grad_y)))
+            return EP_ERR_INVALID_ARG;
+    }
+    return from_hip(ep::launch_combine_backward(
+        static_cast<const uint16_t*>(grad_out),
+        grad_weights ? static_cast<const uint16_t*>(y) : nullptr, num_rows, dst_row, topk_weights,
+        T, K, H, static_cast<uint16_t*>(grad_y), grad_weights,
+        static_cast<hipStream_t>(stream)));
+}
+
+ep_status_t ep_dispatch_backward(const void* grad_recv_x, int64_t num_rows,
+                                 const int32_t* dst_row, int32_t num_tokens, int32_t num_topk,
+                                 int32_t hidden, void* grad_x, void* stream) {
+    const int32_t T = num_tokens, K = num_topk, H = hidden;
+    if (T < 0 || K <= 0 || H <= 0 || H % 8 != 0 || num_rows < 0) return EP_ERR_INVALID_ARG;
+    if ((int64_t)T * K >= kMaxRows) return EP_ERR_INVALID_ARG;
+    if (K > EP_MAX_TOPK) return EP_ERR_UNSUPPORTED;
+    if (T > 0) {
+        if (!dst_row || !grad_x || (num_rows > 0 && !grad_recv_x)) return EP_ERR_INVALID_ARG;
+        if ((grad_recv_x && !aligned16(grad_recv_x)) || !aligned16(grad_x))
+            return EP_ERR_INVALID_ARG;
+    }
+    return from_hip(ep::launch_combine(static_cast<const uint16_t*>(grad_recv_x), num_rows,
+                                       dst_row, nullptr, T, K, H,
+                                       static_cast<uint16_t*>(grad_x), 0,
+                                       static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// Shape and type checks shared by the router and its gradient.
+ep_status_t check_route(ep_dtype_t dtype, int32_t T, int32_t E, int32_t K, ep_score_t score,
+                        float scale) {
+    if (T < 0 || E <= 0 || K <= 0 || K > E) return EP_ERR_INVALID_ARG;
+    if (dtype != EP_DTYPE_BF16 && dtype != EP_DTYPE_FP32) return EP_ERR_INVALID_ARG;
+    if (score != EP_SCORE_SOFTMAX && score != EP_SCORE_SIGMOID) return EP_ERR_INVALID_ARG;
+    if (!(scale - scale == 0.0f)) return EP_ERR_INVALID_ARG;   // infinite or NaN
+    if ((int64_t)T * K >= kMaxRows) return EP_ERR_INVALID_ARG;
+    if (E > EP_MAX_EXPERTS || K > EP_MAX_TOPK) return EP_ERR_UNSUPPORTED;
+    return EP_OK;
+}
+
+bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+}  // namespace
+
+extern "C" {
+
+ep_status_t ep_route(const void* logits, ep_dtype_t logits_dtype, const float* expert_bias,
+                     int32_t num_tokens, int32_t num_experts, int32_t num_topk, ep_score_t score,
+                     int32_t num_groups, int32_t topk_groups, int32_t normalize, float scale,
+                     int64_t* topk_idx, float* topk_weights, void* stream) {
+    const int32_t T = num_tokens, E = num_experts, K = num_topk;
+    ep_status_t st = check_route(logits_dtype, T, E, K, score, scale);
+    if (st != EP_OK) return st;
+    if (num_groups < 1 || E % num_groups != 0 || topk_groups < 1 || topk_groups > num_groups ||
+        (int64_t)K > (int64_t)topk_groups * (E / num_groups))
+        return EP_ERR_INVALID_ARG;
+    if (num_groups > EP_MAX_ROUTE_GROUPS) return EP_ERR_UNSUPPORTED;
+    const bool bf16 = logits_dtype == EP_DTYPE_BF16;
+    if (T > 0) {
+        if (!logits || !topk_idx || !topk_weights) return EP_ERR_INVALID_ARG;
+        if (!aligned_to(logits, bf16 ? 2 : 4)) return EP_ERR_INVALID_ARG;
+    }
+    return from_hip(ep::launch_route(logits, bf16, expert_bias, T, E, K,
+                                     score == EP_SCORE_SOFTMAX, num_groups, topk_groups,
+                                     normalize != 0, scale, topk_idx, topk_weights,
+                                     static_cast<hipStream_t>(stream)));
+}
+
+ep_status_t ep_route_backward(const void* logits, ep_dtype_t logits_dtype,
+                              const int64_t* topk_idx, const float* grad_weights,
+                              int32_t num_tokens, int32_t num_experts, int32_t num_topk,
+                              ep_score_t score, int32_t normalize, float scale,
+                              void* grad_logits, void* stream) {
+    const int32_t T = num_tokens, E = num_experts, K = num_topk;
+    ep_status_t st = check_route(logits_dtype, T, E, K, score, scale);
+    if (st != EP_OK) return st;
+    const bool bf16 = logits_dtype == EP_DTYPE_BF16;
+    if (T > 0) {
+        if (!logits || !topk_idx || !grad_weights || !grad_logits) return EP_ERR_INVALID_ARG;
+        if (!aligned_to(logits, bf16 ? 2 : 4) || !aligned_to(grad_logits, bf16 ? 2 : 4))
+            return EP_ERR_INVALID_ARG;
+    }
+    return from_hip(ep::launch_route_backward(logits, bf16, topk_idx, grad_weights, T, E, K,
+                                              score == EP_SCORE_SOFTMAX, normalize != 0, scale,
+                                              grad_logits, static_cast<hipStream_t>(stream)));
+}
+
+ep_status_t ep_expert_linear_w4(const void* x, const float* x_scales, ep_dtype_t x_dtype,
+                                int64_t num_rows, const int32_t* expert_offsets,
+                                const int32_t* num_tokens_per_expert, int32_t capacity,
+                                int32_t num_experts, int32_t in_features, int32_t out_features,
+                                int32_t group_size, const uint8_t* weight, const void* scales,
+                                const uint8_t* zeros, int32_t swiglu, void* y, void* stream) {
+    const int32_t E = num_experts, I = in_features, N = out_features, G = group_size;
+    if (E <= 0 || I <= 0 || N <= 0 || N % 8 != 0 || num_rows < 0 || num_rows >= kMaxRows)
+        return EP_ERR_INVALID_ARG;
+    if ((G != 32 && G != 64 && G != 128) || I % G != 0) return EP_ERR_INVALID_ARG;
+    if (x_dtype != EP_DTYPE_BF16 && x_dtype != EP_DTYPE_FP8_E4M3) return EP_ERR_INVALID_ARG;
+    const bool fp8 = x_dtype == EP_DTYPE_FP8_E4M3;
+    if (fp8 && I % 128 != 0) return EP_ERR_INVALID_ARG;
+    if (!expert_offsets && (capacity < 1 || (int64_t)E * capacity > num_rows))
+        return EP_ERR_INVALID_ARG;
+    if (num_rows > 0) {
+        if (!x || !num_tokens_per_expert || !weight || !scales || !y || (fp8 && !x_scales))
+            return EP_ERR_INVALID_ARG;
+        if (!aligned16(x) || !aligned16(weight) || !aligned16(y) || !aligned_to(scales, 8) ||
+            !aligned_to(zeros, 4))
+            return EP_ERR_INVALID_ARG;
+    }
+    const int64_t W = (int64_t)N * (swiglu ? 2 : 1);
+    if (E > EP_MAX_EXPERTS || W * (I / 2) >= kMaxRows) return EP_ERR_UNSUPPORTED;
+    return from_hip(ep::launch_expert_linear_w4(
+        x, x_scales, fp8, num_rows, expert_offsets, num_tokens_per_expert, capacity, E, I, N, G,
+        weight, static_cast<const uint16_t*>(scales), zeros, swiglu != 0,
+        static_cast<uint16_t*>(y), static_cast<hipStream_t>(stream)));
+}
+
 ep_status_t ep_get_device_error(const void* workspace, size_t workspace_bytes,
                                 int64_t* num_invalid, void* stream) {
     if (!workspace || !num_invalid || workspace_bytes < ep::kWsHeaderBytes)

@@ -29,6 +29,9 @@
 // 90.4 / 87.0 at top-4, 62.9 / 61.6 at top-2 and 52.0 / 51.8 at top-1: with
 // fewer slots the burst is a larger share of a tile's traffic, and the CU
 // waits for it before its next tile starts.
+//
+// With w null every weight is 1, and the chain fma(1, y, acc) = acc + y is the
+// gradient of dispatch: the sum of the gradients of a token's receive rows.
 #include "ep_internal.h"
 #include "ep_device.h"
 
@@ -86,7 +89,7 @@ __device__ __forceinline__ void combine_task(const uint16_t* __restrict__ y, int
     float wl = 0.0f;
     if (lane < kk) {
         drow = dst_row[(int64_t)t * kk + lane];
-        wl = w[(int64_t)t * kk + lane];
+        wl = w ? w[(int64_t)t * kk + lane] : 1.0f;
         if (drow >= nrows) drow = -1;   // outside y: skipped like a masked slot
     }
     float acc[8];
@@ -139,7 +142,7 @@ __global__ __launch_bounds__(kCombineTileThreads) void combine_tile_kernel(
     float wl = 0.0f;
     if (lane < nt * KT) {
         drow = dst_row[(int64_t)t0 * KT + lane];
-        wl = w[(int64_t)t0 * KT + lane];
+        wl = w ? w[(int64_t)t0 * KT + lane] : 1.0f;
         if (drow >= nrows) drow = -1;   // outside y: skipped like a masked slot
     }
     const int ntask = nt * nchunk;

@@ -229,9 +229,38 @@ constexpr int kCombineTileMinBlocks = 512;
 
 // num_cus > 0: the CU-budget form (at most num_cus workgroups of
 // kBudgetThreads striding over the tasks); otherwise the ordinary launch.
+// w null: unit weights (the gradient of dispatch).
 hipError_t launch_combine(const uint16_t* y, int64_t nrows, const int32_t* dst_row,
                           const float* w, int T, int K, int H, uint16_t* out, int num_cus,
                           hipStream_t s);
+
+// --------------------------------------------------------------- backward ---
+constexpr int kBackwardMaxThreads = 1024;
+
+// Gradient of combine.  gy null: no row gradients (w is then unused); gw null:
+// no weight gradients (y is then unused).
+hipError_t launch_combine_backward(const uint16_t* gout, const uint16_t* y, int64_t nrows,
+                                   const int32_t* dst_row, const float* w, int T, int K, int H,
+                                   uint16_t* gy, float* gw, hipStream_t s);
+
+// ----------------------------------------------------------------- router ---
+constexpr int kRouteThreads = 256;
+
+// bias null: the logits decide (unless NG > 1).  logits bf16 or fp32.
+hipError_t launch_route(const void* logits, bool bf16, const float* bias, int T, int E, int K,
+                        bool softmax, int NG, int TG, bool normalize, float scale,
+                        int64_t* topk_idx, float* topk_weights, hipStream_t s);
+hipError_t launch_route_backward(const void* logits, bool bf16, const int64_t* topk_idx,
+                                 const float* gw, int T, int E, int K, bool softmax,
+                                 bool normalize, float scale, void* grad_logits, hipStream_t s);
+
+// ---------------------------------------------------------------- experts ---
+// offsets null: expert e's rows start at e * capacity.  zeros null: 8.
+hipError_t launch_expert_linear_w4(const void* x, const float* xs, bool fp8, int64_t num_rows,
+                                   const int32_t* offsets, const int32_t* counts, int capacity,
+                                   int E, int I, int N, int G, const uint8_t* w,
+                                   const uint16_t* scales, const uint8_t* zeros, bool swiglu,
+                                   uint16_t* y, hipStream_t s);
 
 // ------------------------------------------------------------ diagnostics ---
 hipError_t launch_convert_e4m3(const float* in, uint8_t* out, int64_t n, int mode, hipStream_t s);

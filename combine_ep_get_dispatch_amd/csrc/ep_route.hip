@@ -1,0 +1,538 @@
+// The router on gfx950: from a token's logits over the experts to its K slots
+// (topk_idx, topk_weights), and the gradient of the weights with respect to
+// the logits.
+//
+// Mathematics.  s_e = sigmoid(l_e) or softmax over the experts; the order is
+// that of choice_e = s_e + bias_e (of l_e itself without a bias: both scores
+// grow with the logit).  With groups only the experts of the best groups stay,
+// a group's score being the sum of its two largest choices.  The K largest
+// remain, equal ones by lowest index, and
+//   w_k = scale * s_k   or   scale * s_k / sum over the slots of s.
+// An expert whose logit is -inf or NaN is not available.
+//
+// Precision.  Where a bias or groups decide, choices are compared in fp64: two
+// experts whose fp32 scores fall on the same value or swap under its rounding
+// would otherwise be picked by the rounding, not by the definition.  Where the
+// logits decide they are compared as they are.
+//
+// Layout.  A token belongs to a segment of L lanes of a wave and a lane holds
+// VPL consecutive experts, so that lower lanes hold lower ids: the lowest lane
+// among equals, and the lowest value in it, is the lowest id, and the maximum
+// needs no index beside it.  Maxima over a segment of up to 16 lanes stay
+// inside a DPP row.
+#include "ep_internal.h"
+#include "ep_device.h"
+
+#include <type_traits>
+
+namespace ep {
+namespace {
+
+constexpr float kFltMax = 3.4028234663852886e38f;
+
+// Maximum and sum over aligned segments of L lanes, the same for every lane of
+// a segment; all lanes active.
+__device__ __forceinline__ uint32_t dpp_move(uint32_t v, int step) {
+    switch (step) {
+        case 0: return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xf, 0xf, false);
+        case 1: return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xf, 0xf, false);
+        case 2: return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, false);
+        case 3: return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xf, 0xf, false);
+        case 4: return (uint32_t)__shfl_xor((int)v, 16);
+        default: return (uint32_t)__shfl_xor((int)v, 32);
+    }
+}
+template <typename V>
+__device__ __forceinline__ V seg_move(V v, int step) {
+    if constexpr (sizeof(V) == 4) {
+        return __builtin_bit_cast(V, dpp_move(__builtin_bit_cast(uint32_t, v), step));
+    } else {
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);
+        const uint32_t lo = dpp_move((uint32_t)u, step), hi = dpp_move((uint32_t)(u >> 32), step);
+        return __builtin_bit_cast(V, (uint64_t)hi << 32 | lo);
+    }
+}
+template <int L, typename V>
+__device__ __forceinline__ V seg_max(V v) {
+#pragma unroll
+    for (int i = 0; (1 << i) < L; ++i) {
+        const V o = seg_move(v, i);
+        v = o > v ? o : v;
+    }
+    return v;
+}
+template <int L, typename V>
+__device__ __forceinline__ V seg_sum(V v) {
+#pragma unroll
+    for (int i = 0; (1 << i) < L; ++i) v += seg_move(v, i);
+    return v;
+}
+
+// Unsigned keys in the order of the values, 0 below all of them (an expert
+// that is not available).  Adding 0 makes -0 and +0 the same key.
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t u = __float_as_uint(v + 0.0f);
+    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ uint64_t order_key(double v) {
+    const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
+    return u ^ ((u >> 63) ? ~0ull : 1ull << 63);
+}
+
+__device__ __forceinline__ float load_logit(const float* p) { return *p; }
+__device__ __forceinline__ float load_logit(const uint16_t* p) {
+    return __uint_as_float((uint32_t)*p << 16);
+}
+// -inf where the expert is not available; +inf counts as fp32's largest value.
+__device__ __forceinline__ float clean_logit(float v) {
+    return v > -INFINITY ? fminf(v, kFltMax) : -INFINITY;
+}
+
+// A lane's VPL logits: experts [e0, e0 + VPL), -inf past E.  vec: rows start
+// at 16-byte boundaries and E is a multiple of the 16-byte vector.
+template <int VPL>
+__device__ __forceinline__ void load_row(float (&l)[VPL], const float* row, int e0, int E,
+                                         bool vec) {
+    if (VPL % 4 == 0 && vec) {
+#pragma unroll
+        for (int j = 0; j + 3 < VPL; j += 4) {
+            float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            if (e0 + j < E) v = *reinterpret_cast<const float4*>(row + e0 + j);
+            l[j] = v.x;
+            l[j + 1] = v.y;
+            l[j + 2] = v.z;
+            l[j + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) l[j] = e0 + j < E ? row[e0 + j] : -INFINITY;
+    }
+}
+template <int VPL>
+__device__ __forceinline__ void load_row(float (&l)[VPL], const uint16_t* row, int e0, int E,
+                                         bool vec) {
+    if (VPL % 8 == 0 && vec) {
+#pragma unroll
+        for (int j = 0; j + 7 < VPL; j += 8) {
+            uint4 v = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+            if (e0 + j < E) v = *reinterpret_cast<const uint4*>(row + e0 + j);
+            l[j] = bf16_lo(v.x);
+            l[j + 1] = bf16_hi(v.x);
+            l[j + 2] = bf16_lo(v.y);
+            l[j + 3] = bf16_hi(v.y);
+            l[j + 4] = bf16_lo(v.z);
+            l[j + 5] = bf16_hi(v.z);
+            l[j + 6] = bf16_lo(v.w);
+            l[j + 7] = bf16_hi(v.w);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) l[j] = e0 + j < E ? load_logit(row + e0 + j) : -INFINITY;
+    }
+}
+
+template <int VPL>
+__device__ __forceinline__ void store_row(const float (&o)[VPL], float* row, int e0, int E,
+                                          bool vec) {
+    if (VPL % 4 == 0 && vec) {
+#pragma unroll
+        for (int j = 0; j + 3 < VPL; j += 4)
+            if (e0 + j < E)
+                *reinterpret_cast<float4*>(row + e0 + j) =
+                    make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j)
+            if (e0 + j < E) row[e0 + j] = o[j];
+    }
+}
+template <int VPL>
+__device__ __forceinline__ void store_row(const float (&o)[VPL], uint16_t* row, int e0, int E,
+                                          bool vec) {
+    if (VPL % 8 == 0 && vec) {
+#pragma unroll
+        for (int j = 0; j + 7 < VPL; j += 8)
+            if (e0 + j < E)
+                *reinterpret_cast<uint4*>(row + e0 + j) = make_uint4(
+                    pack_bf16x2(o[j], o[j + 1]), pack_bf16x2(o[j + 2], o[j + 3]),
+                    pack_bf16x2(o[j + 4], o[j + 5]), pack_bf16x2(o[j + 6], o[j + 7]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j)
+            if (e0 + j < E) row[e0 + j] = (uint16_t)pack_bf16x2(o[j], 0.0f);
+    }
+}
+
+__device__ __forceinline__ double sigmoid64(double l) { return 1.0 / (1.0 + exp(-l)); }
+
+// FULL: choices in fp64 (a bias or groups); otherwise the logits decide.
+// Dynamic LDS, per token of the workgroup: K slots (int), then with groups
+// E choices (double, at an 8-byte boundary), NG group scores (double) and NG
+// flags (int).
+template <typename LT, int VPL, int L, bool FULL>
+__global__ __launch_bounds__(kRouteThreads) void route_kernel(
+    const LT* __restrict__ logits, const float* __restrict__ bias, int T, int E, int K,
+    bool softmax, int NG, int TG, bool normalize, float scale, int64_t* __restrict__ topk_idx,
+    float* __restrict__ topk_weights, bool vec) {
+    using Key = typename std::conditional<FULL, uint64_t, uint32_t>::type;
+    constexpr int kTokens = kRouteThreads / L;
+    extern __shared__ EP_LDS_ALIGN unsigned char s_raw[];
+    const int lane = threadIdx.x & 63;
+    const int sl = lane & (L - 1);
+    const int tok = threadIdx.x / L;                 // token of the workgroup
+    const int64_t t = (int64_t)blockIdx.x * kTokens + tok;
+    const bool live = t < T;
+    int* s_idx = reinterpret_cast<int*>(s_raw) + tok * K;
+
+    const int e0 = sl * VPL;
+    float l[VPL];
+    const LT* row = logits + t * E;
+    if (live) {
+        load_row<VPL>(l, row, e0, E, vec);
+    } else {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) l[j] = -INFINITY;
+    }
+    float lmax = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+        l[j] = clean_logit(l[j]);
+        lmax = fmaxf(lmax, l[j]);
+    }
+    for (int k = sl; k < K; k += L) s_idx[k] = -1;
+
+    // the softmax over all experts: its maximum and sum
+    float m = 0.0f;
+    double total = 1.0;
+    const bool need_total = softmax && (FULL || !normalize);
+    if (need_total) {
+        m = fmaxf(seg_max<L>(lmax), -kFltMax);
+        if constexpr (FULL) {
+            double a = 0.0;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) a += exp((double)l[j] - (double)m);
+            total = seg_sum<L>(a);
+        } else {
+            float a = 0.0f;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) a += expf(l[j] - m);
+            total = (double)seg_sum<L>(a);
+        }
+    }
+
+    Key key[VPL];
+    if constexpr (FULL) {
+        double ch[VPL];
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            const double s = softmax ? exp((double)l[j] - (double)m) / total
+                                     : sigmoid64((double)l[j]);
+            double c = s;
+            if (bias && e0 + j < E) c += (double)bias[e0 + j];
+            // not available: the logit, or a bias of -inf or NaN
+            ch[j] = (l[j] > -INFINITY && c > -INFINITY) ? c : -INFINITY;
+            key[j] = ch[j] > -INFINITY ? order_key(bias ? c : (double)l[j]) : 0;
+        }
+        if (NG > 1) {
+            const size_t idx_bytes = ((size_t)kTokens * K * 4 + 15) & ~(size_t)15;
+            double* s_ch = reinterpret_cast<double*>(s_raw + idx_bytes) + tok * (E + 2 * NG);
+            double* s_gs = s_ch + E;
+            int* s_flag = reinterpret_cast<int*>(s_gs + NG);
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (e0 + j < E) s_ch[e0 + j] = ch[j];
+            __syncthreads();
+            const int gsz = E / NG;
+            for (int g = sl; g < NG; g += L) {
+                double a = -INFINITY, b = -INFINITY;   // the two largest of the group
+                int i = g < gsz ? g : 0;               // lanes start at different banks
+                for (int n = 0; n < gsz; ++n) {
+                    const double v = s_ch[g * gsz + i];
+                    if (v > a) {
+                        b = a;
+                        a = v;
+                    } else if (v > b) {
+                        b = v;
+                    }
+                    if (++i == gsz) i = 0;
+                }
+                s_gs[g] = b > -INFINITY ? a + b : a;
+            }
+            __syncthreads();
+            for (int g = sl; g < NG; g += L) {
+                const double v = s_gs[g];
+                int better = 0;
+                for (int i = 0; i < NG; ++i) {
+                    const double o = s_gs[i];
+                    better += (o > v || (o == v && i < g)) ? 1 : 0;
+                }
+                s_flag[g] = better < TG ? 1 : 0;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (e0 + j < E && !s_flag[(e0 + j) / gsz]) key[j] = 0;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) key[j] = l[j] > -INFINITY ? order_key(l[j]) : 0;
+    }
+
+    const uint64_t segmask = (L == 64 ? ~0ull : ((1ull << (L & 63)) - 1)) << (lane - sl);
+    for (int k = 0; k < K; ++k) {
+        Key best = 0;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) best = key[j] > best ? key[j] : best;
+        const Key top = seg_max<L>(best);
+        const uint64_t eq = __ballot(best == top && top != 0) & segmask;
+        if (eq != 0 && __builtin_ctzll(eq) == (unsigned)lane) {
+            int at = 0;
+#pragma unroll
+            for (int j = VPL - 1; j >= 0; --j)
+                if (key[j] == top) at = j;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (j == at) key[j] = 0;
+            s_idx[k] = e0 + at;
+        }
+    }
+    __syncthreads();
+
+    // slot k of the token: lanes k, k + L, ... of its segment
+    if (normalize && softmax) {
+        // over the selected experts alone, from their own maximum
+        m = -kFltMax;
+        for (int k = sl; k < K; k += L)
+            if (s_idx[k] >= 0) m = fmaxf(m, clean_logit(load_logit(row + s_idx[k])));
+        m = seg_max<L>(m);
+    }
+    double sum = 0.0;
+    if (normalize) {
+        for (int k = sl; k < K; k += L)
+            if (s_idx[k] >= 0) {
+                const double v = (double)clean_logit(load_logit(row + s_idx[k]));
+                sum += softmax ? exp(v - (double)m) : sigmoid64(v);
+            }
+        sum = seg_sum<L>(sum);
+    } else {
+        sum = softmax ? total : 1.0;
+    }
+    for (int k = sl; k < K; k += L) {
+        const int e = s_idx[k];
+        double w = 0.0;
+        if (e >= 0 && sum > 0.0) {
+            const double v = (double)clean_logit(load_logit(row + e));
+            w = (softmax ? exp(v - (double)m) : sigmoid64(v)) / sum * (double)scale;
+        }
+        if (live) {
+            topk_idx[t * K + k] = e;
+            topk_weights[t * K + k] = (float)w;
+        }
+    }
+}
+
+// Gradient.  With c_k = scale * grad_weights[k] over the token's valid slots:
+//   softmax, not normalised:  d_i = p_i (c_i - sum_k c_k p_k), every expert;
+//   softmax, normalised:      d_k = q_k (c_k - sum_j c_j q_j), q the softmax
+//                             over the slots;
+//   sigmoid, not normalised:  d_k = c_k s_k (1 - s_k);
+//   sigmoid, normalised:      d_k = q_k (c_k - sum_j c_j q_j) (1 - s_k),
+//                             q_k = s_k / sum_j s_j;
+// 0 for every other expert.  Slots of one token that name the same expert add
+// up in slot order.  Dynamic LDS: per token K expert ids (int), K values.
+template <typename LT, int VPL, int L>
+__global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(
+    const LT* __restrict__ logits, const int64_t* __restrict__ topk_idx,
+    const float* __restrict__ grad_weights, int T, int E, int K, bool softmax, bool normalize,
+    float scale, LT* __restrict__ grad_logits, bool vec) {
+    constexpr int kTokens = kRouteThreads / L;
+    extern __shared__ EP_LDS_ALIGN unsigned char s_raw[];
+    const int sl = threadIdx.x & (L - 1);
+    const int tok = threadIdx.x / L;
+    const int64_t t = (int64_t)blockIdx.x * kTokens + tok;
+    const bool live = t < T;
+    int* s_idx = reinterpret_cast<int*>(s_raw) + tok * K;
+    float* s_val = reinterpret_cast<float*>(s_raw) + kTokens * K + tok * K;
+
+    const int e0 = sl * VPL;
+    const LT* row = logits + t * E;
+    const bool dense = softmax && !normalize;
+    float p[VPL];
+    float m = -kFltMax;
+    float inv = 0.0f;
+    if (dense) {
+        if (live) {
+            load_row<VPL>(p, row, e0, E, vec);
+        } else {
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) p[j] = -INFINITY;
+        }
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            p[j] = clean_logit(p[j]);
+            m = fmaxf(m, p[j]);
+        }
+        m = seg_max<L>(m);
+        float a = 0.0f;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            p[j] = expf(p[j] - m);
+            a += p[j];
+        }
+        a = seg_sum<L>(a);
+        inv = a > 0.0f ? 1.0f / a : 0.0f;
+    }
+
+    if (normalize && softmax) {
+        for (int k = sl; k < K; k += L) {
+            const int64_t e = live ? topk_idx[t * K + k] : -1;
+            if (e >= 0 && e < E) m = fmaxf(m, clean_logit(load_logit(row + e)));
+        }
+        m = seg_max<L>(m);
+    }
+    // sums over the slots: of the unnormalised shares v, and of c * v
+    double sv = 0.0, scv = 0.0;
+    for (int k = sl; k < K; k += L) {
+        const int64_t e64 = live ? topk_idx[t * K + k] : -1;
+        const int e = e64 >= 0 && e64 < E ? (int)e64 : -1;
+        s_idx[k] = e;
+        if (e >= 0 && (dense || normalize)) {
+            const double v = (double)clean_logit(load_logit(row + e));
+            const double u = softmax ? exp(v - (double)m) : sigmoid64(v);
+            sv += u;
+            scv += u * (double)grad_weights[t * K + k];
+        }
+    }
+    sv = seg_sum<L>(sv);
+    scv = seg_sum<L>(scv) * (double)scale;
+    const double norm = dense ? (double)inv : (sv > 0.0 ? 1.0 / sv : 0.0);
+    const double mean = scv * norm;                 // sum_k c_k times the share of k
+    for (int k = sl; k < K; k += L) {
+        const int e = s_idx[k];
+        double d = 0.0;
+        if (e >= 0) {
+            const double c = (double)scale * (double)grad_weights[t * K + k];
+            if (dense) {
+                d = c;
+            } else {
+                const double v = (double)clean_logit(load_logit(row + e));
+                if (softmax) {
+                    d = exp(v - (double)m) * norm * (c - mean);
+                } else {
+                    const double s = sigmoid64(v);
+                    d = normalize ? s * norm * (c - mean) : c * s;
+                    d *= sigmoid64(-v);
+                }
+            }
+        }
+        s_val[k] = (float)d;
+    }
+    __syncthreads();
+    float o[VPL];
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) o[j] = 0.0f;
+    for (int k = 0; k < K; ++k) {
+        const int at = s_idx[k] - e0;
+        const float d = s_val[k];
+        if (at >= 0 && at < VPL) {
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (j == at) o[j] += d;
+        }
+    }
+    if (dense) {
+        const float mf = (float)mean;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) o[j] = p[j] * inv * (o[j] - mf);
+    }
+    if (live) store_row<VPL>(o, grad_logits + t * E, e0, E, vec);
+}
+
+bool rows_vectorised(const void* p, size_t elem, int E) {
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (E * elem) % 16 == 0;
+}
+
+template <typename LT, int VPL, int L>
+hipError_t launch_route_l(const LT* logits, const float* bias, int T, int E, int K, bool softmax,
+                          int NG, int TG, bool normalize, float scale, int64_t* topk_idx,
+                          float* topk_weights, hipStream_t s) {
+    constexpr int kTokens = kRouteThreads / L;
+    const dim3 grid((unsigned)((T + kTokens - 1) / kTokens)), block(kRouteThreads);
+    const bool vec = rows_vectorised(logits, sizeof(LT), E);
+    size_t lds = ((size_t)kTokens * K * 4 + 15) & ~(size_t)15;
+    if (NG > 1) lds += (size_t)kTokens * (E + 2 * NG) * 8;
+    if (bias || NG > 1)
+        hipLaunchKernelGGL((route_kernel<LT, VPL, L, true>), grid, block, lds, s, logits, bias, T,
+                           E, K, softmax, NG, TG, normalize, scale, topk_idx, topk_weights, vec);
+    else
+        hipLaunchKernelGGL((route_kernel<LT, VPL, L, false>), grid, block, lds, s, logits, bias,
+                           T, E, K, softmax, NG, TG, normalize, scale, topk_idx, topk_weights,
+                           vec);
+    return hipGetLastError();
+}
+
+template <typename LT, int VPL, int L>
+hipError_t launch_route_backward_l(const LT* logits, const int64_t* topk_idx, const float* gw,
+                                   int T, int E, int K, bool softmax, bool normalize, float scale,
+                                   LT* grad_logits, hipStream_t s) {
+    constexpr int kTokens = kRouteThreads / L;
+    const dim3 grid((unsigned)((T + kTokens - 1) / kTokens)), block(kRouteThreads);
+    const bool vec = rows_vectorised(logits, sizeof(LT), E) &&
+                     rows_vectorised(grad_logits, sizeof(LT), E);
+    const size_t lds = (size_t)kTokens * K * 8;
+    hipLaunchKernelGGL((route_backward_kernel<LT, VPL, L>), grid, block, lds, s, logits, topk_idx,
+                       gw, T, E, K, softmax, normalize, scale, grad_logits, vec);
+    return hipGetLastError();
+}
+
+// The lanes per token and experts per lane: the fewest lanes that hold the
+// experts at 16 a lane.
+#define EP_ROUTE_DISPATCH(FN, LT, ...)                             \
+    do {                                                           \
+        if (E <= 8) return FN<LT, 1, 8>(__VA_ARGS__);              \
+        if (E <= 64) return FN<LT, 4, 16>(__VA_ARGS__);            \
+        if (E <= 128) return FN<LT, 8, 16>(__VA_ARGS__);           \
+        if (E <= 256) return FN<LT, 16, 16>(__VA_ARGS__);          \
+        if (E <= 512) return FN<LT, 16, 32>(__VA_ARGS__);          \
+        return FN<LT, 16, 64>(__VA_ARGS__);                        \
+    } while (0)
+
+template <typename LT>
+hipError_t route_any(const void* logits, const float* bias, int T, int E, int K, bool softmax,
+                     int NG, int TG, bool normalize, float scale, int64_t* topk_idx,
+                     float* topk_weights, hipStream_t s) {
+    EP_ROUTE_DISPATCH(launch_route_l, LT, static_cast<const LT*>(logits), bias, T, E, K, softmax,
+                      NG, TG, normalize, scale, topk_idx, topk_weights, s);
+}
+
+template <typename LT>
+hipError_t route_backward_any(const void* logits, const int64_t* topk_idx, const float* gw, int T,
+                              int E, int K, bool softmax, bool normalize, float scale,
+                              void* grad_logits, hipStream_t s) {
+    EP_ROUTE_DISPATCH(launch_route_backward_l, LT, static_cast<const LT*>(logits), topk_idx, gw, T,
+                      E, K, softmax, normalize, scale, static_cast<LT*>(grad_logits), s);
+}
+
+}  // namespace
+
+hipError_t launch_route(const void* logits, bool bf16, const float* bias, int T, int E, int K,
+                        bool softmax, int NG, int TG, bool normalize, float scale,
+                        int64_t* topk_idx, float* topk_weights, hipStream_t s) {
+    if (T == 0) return hipSuccess;
+    return bf16 ? route_any<uint16_t>(logits, bias, T, E, K, softmax, NG, TG, normalize, scale,
+                                      topk_idx, topk_weights, s)
+                : route_any<float>(logits, bias, T, E, K, softmax, NG, TG, normalize, scale,
+                                   topk_idx, topk_weights, s);
+}
+
+hipError_t launch_route_backward(const void* logits, bool bf16, const int64_t* topk_idx,
+                                 const float* gw, int T, int E, int K, bool softmax,
+                                 bool normalize, float scale, void* grad_logits, hipStream_t s) {
+    if (T == 0) return hipSuccess;
+    return bf16 ? route_backward_any<uint16_t>(logits, topk_idx, gw, T, E, K, softmax, normalize,
+                                               scale, grad_logits, s)
+                : route_backward_any<float>(logits, topk_idx, gw, T, E, K, softmax, normalize,
+                                            scale, grad_logits, s);
+}
+
+}  // namespace ep

@@ -67,8 +67,14 @@ typedef enum EP_ENUM_BASE {
 
 typedef enum EP_ENUM_BASE {
     EP_DTYPE_BF16 = 0,       /* receive rows are bf16 copies of the tokens  */
-    EP_DTYPE_FP8_E4M3 = 1    /* receive rows are OCP E4M3 codes + scales    */
+    EP_DTYPE_FP8_E4M3 = 1,   /* receive rows are OCP E4M3 codes + scales    */
+    EP_DTYPE_FP32 = 2        /* router logits only                          */
 } ep_dtype_t;
+
+typedef enum EP_ENUM_BASE {
+    EP_SCORE_SOFTMAX = 0,    /* scores: softmax over the experts            */
+    EP_SCORE_SIGMOID = 1     /* scores: sigmoid of each logit               */
+} ep_score_t;
 
 /* Limits of the library (EP_ERR_UNSUPPORTED beyond them). */
 #define EP_MAX_EXPERTS 1024
@@ -76,6 +82,7 @@ typedef enum EP_ENUM_BASE {
 #define EP_LL_MAX_SLOTS 8192   /* T*K of one ep_low_latency_dispatch call */
 #define EP_MAX_EXPERT_ALIGNMENT 1024   /* of ep_layout_dispatch_aligned */
 #define EP_STATIC_SCRATCH_BYTES (8u << 20)   /* per GPU, of ep_layout_dispatch_static */
+#define EP_MAX_ROUTE_GROUPS 64   /* expert groups of ep_route */
 
 /*
  * Bytes of device workspace that ep_get_dispatch_layout and ep_dispatch need
@@ -380,6 +387,141 @@ ep_status_t ep_layout_dispatch_cu(const void *x, int32_t num_tokens, int32_t hid
 ep_status_t ep_combine_cu(const void *y, int64_t num_rows, const int32_t *dst_row,
                           const float *topk_weights, int32_t num_tokens, int32_t num_topk,
                           int32_t hidden, void *out, int32_t num_cus, void *stream);
+
+/*
+ * Gradient of combine, for training (the throughput kernels of the family
+ * serve training: "DeepSeek releases DeepEP, an efficient communication
+ * library for MoE models", section "Technical Details"; the formulas are
+ * those of ep_combine differentiated).  With r = dst_row[t*K+k]:
+ *   grad_y[r*H + h]       = bf16(topk_weights[t*K+k] * grad_out[t*H + h])
+ *   grad_weights[t*K + k] = sum over h of grad_out[t*H + h] * y[r*H + h]
+ * the product taken in fp32, the sum in fp32 in an order fixed by the shape
+ * (equal inputs give equal bits).  A slot whose r lies outside [0, num_rows)
+ * is skipped as ep_combine skips it: its grad_weights is 0 and no row is
+ * written.  Rows of grad_y that no slot names are left untouched.  A row must
+ * be named by at most one slot, as every dispatch form numbers them (if two
+ * slots name it, which one's gradient it holds is unspecified).
+ *   grad_y NULL: only grad_weights (topk_weights may then be NULL).
+ *   grad_weights NULL: only grad_y (y may then be NULL).
+ * Both NULL is EP_ERR_INVALID_ARG.  Types, shapes, limits and errors as
+ * ep_combine: grad_out bf16 [T*H], y and grad_y bf16 [num_rows*H],
+ * topk_weights and grad_weights fp32 [T*K]; grad_out, y and grad_y 16-byte
+ * aligned.  T may be 0.
+ */
+ep_status_t ep_combine_backward(const void *grad_out, const void *y, int64_t num_rows,
+                                const int32_t *dst_row, const float *topk_weights,
+                                int32_t num_tokens, int32_t num_topk, int32_t hidden,
+                                void *grad_y, float *grad_weights, void *stream);
+
+/*
+ * Gradient of dispatch: a token's gradient is the sum of those of its receive
+ * rows,
+ *   acc = +0.0f;  for k = 0..K-1 with 0 <= dst_row[t*K+k] < num_rows:
+ *       acc = acc + grad_recv_x[dst_row[t*K+k]*H + h]
+ *   grad_x[t*H + h] = bf16(acc), rounded to nearest even;
+ * 0 for a token without a row.  grad_recv_x is bf16 [num_rows*H], laid out
+ * like the receive rows (of any dispatch form; for the de-duplicated one like
+ * the expert-major rows that dst_row names), the gradient with respect to the
+ * values the rows stand for: an FP8 dispatch passes it straight through its
+ * quantiser.  Types, shapes, limits and errors as ep_combine without weights.
+ */
+ep_status_t ep_dispatch_backward(const void *grad_recv_x, int64_t num_rows,
+                                 const int32_t *dst_row, int32_t num_tokens, int32_t num_topk,
+                                 int32_t hidden, void *grad_x, void *stream);
+
+/*
+ * Router: each token's K experts and gate weights from its logits, in the
+ * form the dispatch calls take.  Group-limited gating is what the library
+ * family is aligned with ("DeepSeek releases DeepEP, an efficient
+ * communication library for MoE models", section "DeepEP: Optimizing MoE
+ * Communication"); the pages give no formula, this library's is:
+ *   score[e]  = sigmoid(l[e]), or the softmax of l over the E experts;
+ *   choice[e] = score[e] + expert_bias[e]   (expert_bias NULL: score[e]);
+ *   with num_groups > 1 the experts form that many groups of consecutive ids,
+ *   a group's score is the sum of its two largest choices (its only one if it
+ *   has one), and the experts outside the topk_groups best groups drop out;
+ *   the K remaining experts of largest choice (without a bias: of largest
+ *   logit) are the slots, in descending order; ties go to the lowest id, of
+ *   experts and of groups.  Choices are compared in fp64.
+ *   topk_weights[k] = scale * score[e_k], or with normalize
+ *                     scale * score[e_k] / sum over the slots of score
+ *                     (0 if that sum is 0): the bias decides, it does not weigh.
+ * An expert whose logit is -inf or NaN, or whose bias is, is not available.
+ * If fewer than K experts are left the last slots get topk_idx = -1 and
+ * weight 0, a masked slot everywhere in this library; so a padded token whose
+ * logits are all -inf takes no part.  A logit of +inf counts as fp32's largest
+ * value.
+ * logits [T*E] fp32 (EP_DTYPE_FP32) or bf16 (EP_DTYPE_BF16), aligned to their
+ * element; expert_bias fp32 [E] or NULL; topk_idx int64 [T*K]; topk_weights
+ * fp32 [T*K].  E % num_groups == 0, 1 <= topk_groups <= num_groups,
+ * K <= topk_groups * (E / num_groups); scale finite.  EP_ERR_UNSUPPORTED for
+ * E > EP_MAX_EXPERTS, K > EP_MAX_TOPK or num_groups > EP_MAX_ROUTE_GROUPS.
+ * One launch, no workspace.  T may be 0.
+ */
+ep_status_t ep_route(const void *logits, ep_dtype_t logits_dtype, const float *expert_bias,
+                     int32_t num_tokens, int32_t num_experts, int32_t num_topk,
+                     ep_score_t score, int32_t num_groups, int32_t topk_groups,
+                     int32_t normalize, float scale, int64_t *topk_idx, float *topk_weights,
+                     void *stream);
+
+/*
+ * Gradient of ep_route's weights with respect to the logits, the choice of
+ * experts held fixed: with c_k = scale * grad_weights[k] over a token's slots
+ * whose topk_idx lies in [0, E) (the others are skipped) and e the slot's
+ * expert,
+ *   softmax:             d l_i = p_i * (sum of the c of i's slots - sum_k c_k p_k)
+ *   softmax, normalize:  d l_e = q_k * (c_k - sum_j c_j q_j), q = p / sum of the slots' p
+ *   sigmoid:             d l_e = c_k * s_k * (1 - s_k)
+ *   sigmoid, normalize:  d l_e = q_k * (c_k - sum_j c_j q_j) * (1 - s_k), q = s / sum of the slots' s
+ * and 0 for every other expert; every element of grad_logits is written, in
+ * logits' type, rounded once.  Slots of one token that name the same expert
+ * add up.  The arguments are those of the ep_route call; topk_idx is its
+ * output, grad_weights fp32 [T*K].  No gradient reaches the bias.
+ */
+ep_status_t ep_route_backward(const void *logits, ep_dtype_t logits_dtype,
+                              const int64_t *topk_idx, const float *grad_weights,
+                              int32_t num_tokens, int32_t num_experts, int32_t num_topk,
+                              ep_score_t score, int32_t normalize, float scale,
+                              void *grad_logits, void *stream);
+
+/*
+ * The experts' linear layer with 4-bit weights, over the rows that a dispatch
+ * wrote, with an optional gated activation: what runs between dispatch and
+ * combine in decode, where an expert has few rows and its weights are read
+ * once.  For every row r of expert e, and channel n:
+ *   a[n]    = sum over i of x[r,i] * (q[e,n,i] - z[e,i/G,n]) * s[e,i/G,n]
+ *   y[r,n]  = bf16(a[n]),                          n < N        (swiglu == 0)
+ *   y[r,n]  = bf16(silu(a[n]) * a[N + n]),         n < N        (swiglu != 0)
+ * accumulated in fp32, silu(v) = v / (1 + exp(-v)), rounded once.
+ *   Rows of expert e: with expert_offsets (the offsets layouts) rows
+ *   expert_offsets[e] .. expert_offsets[e] + num_tokens_per_expert[e] - 1; with
+ *   expert_offsets NULL (the fixed-capacity layout) rows e*capacity ..
+ *   e*capacity + min(num_tokens_per_expert[e], capacity) - 1.  Rows outside
+ *   [0, num_rows) are neither read nor written; rows of no expert are left
+ *   untouched in y.
+ *   x: x_dtype EP_DTYPE_BF16, bf16 [num_rows*I], x_scales ignored; or
+ *   EP_DTYPE_FP8_E4M3, codes [num_rows*I] and x_scales fp32 [num_rows*I/128],
+ *   as dispatch writes them (I % 128 == 0).
+ *   weight: uint8 [E, W, I/2], W = N, or 2N with swiglu (gate channels first);
+ *   byte j of a row holds q of channel 2j in its low and of 2j+1 in its high
+ *   four bits.  scales: bf16 [E, I/G, W].  zeros: uint8 [E, I/G, W], values
+ *   0..15 (the low four bits count), or NULL for z = 8.
+ *   group_size G: 32, 64 or 128, dividing I.
+ * I > 0, N > 0, N % 8 == 0; x, weight, y 16-byte aligned, scales 8-byte,
+ * zeros 4-byte.  capacity is ignored with expert_offsets, else >= 1 with
+ * E*capacity <= num_rows; num_rows < 2^31.  EP_ERR_UNSUPPORTED for
+ * E > EP_MAX_EXPERTS or W * I/2 >= 2^31.  x and the scales are expected
+ * finite, |x| < 2^119.  No workspace; the order of the sums is fixed by the
+ * arguments' shapes.  (No page describes the experts themselves; format and
+ * definition are this library's.)
+ */
+ep_status_t ep_expert_linear_w4(const void *x, const float *x_scales, ep_dtype_t x_dtype,
+                                int64_t num_rows, const int32_t *expert_offsets,
+                                const int32_t *num_tokens_per_expert, int32_t capacity,
+                                int32_t num_experts, int32_t in_features,
+                                int32_t out_features, int32_t group_size,
+                                const uint8_t *weight, const void *scales,
+                                const uint8_t *zeros, int32_t swiglu, void *y, void *stream);
 
 /*
  * Waits for `stream`, then stores in *num_invalid the number of invalid

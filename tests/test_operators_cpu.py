@@ -1,0 +1,236 @@
+"""The router, the gradients of dispatch and combine, and the experts' 4-bit
+products without a GPU: every refusal of their C entry points and of the
+binding, and the references that the GPU tests compare with.
+
+No call here reaches a kernel.  Pointers are placeholders that the host checks
+look at and never follow (real buffers where a GPU is present).
+"""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import operator_refs as ref
+from combine_ep_get_dispatch_amd import binding as b
+from combine_ep_get_dispatch_amd import workloads as wl
+from test_abi_cpu import Bufs, INVALID, UNSUPPORTED, _NoLaunch
+
+BAD16 = ctypes.c_void_p(0x100008)
+
+
+@pytest.fixture
+def buf():
+    return Bufs()
+
+
+def test_combine_backward_rejects_bad_arguments(buf):
+    L = b.lib()
+    go, y, dst, w, gy, gw = (buf() for _ in range(6))
+
+    def call(go=go, y=y, rows=8, dst=dst, w=w, T=4, K=2, H=256, gy=gy, gw=gw):
+        return L.ep_combine_backward(go, y, rows, dst, w, T, K, H, gy, gw, None)
+
+    for kw in [dict(go=None), dict(y=None), dict(dst=None), dict(w=None), dict(gy=None, gw=None),
+               dict(rows=-1), dict(T=-1), dict(K=0), dict(H=0), dict(H=12), dict(T=1 << 28, K=8),
+               dict(go=BAD16), dict(y=BAD16), dict(gy=BAD16)]:
+        assert call(**kw) == INVALID, kw
+    assert call(K=65) == UNSUPPORTED
+
+
+def test_dispatch_backward_rejects_bad_arguments(buf):
+    L = b.lib()
+    g, dst, gx = (buf() for _ in range(3))
+
+    def call(g=g, rows=8, dst=dst, T=4, K=2, H=256, gx=gx):
+        return L.ep_dispatch_backward(g, rows, dst, T, K, H, gx, None)
+
+    for kw in [dict(g=None), dict(dst=None), dict(gx=None), dict(rows=-1), dict(T=-1), dict(K=0),
+               dict(H=0), dict(H=20), dict(T=1 << 28, K=8), dict(g=BAD16), dict(gx=BAD16)]:
+        assert call(**kw) == INVALID, kw
+    assert call(K=65) == UNSUPPORTED
+
+
+def test_route_rejects_bad_arguments(buf):
+    L = b.lib()
+    lg, bias, idx, w = (buf() for _ in range(4))
+
+    def call(lg=lg, dt=2, bias=bias, T=4, E=16, K=2, sc=1, ng=4, tg=2, nm=1, scale=1.0, idx=idx,
+             w=w):
+        return L.ep_route(lg, dt, bias, T, E, K, sc, ng, tg, nm, scale, idx, w, None)
+
+    for kw in [dict(lg=None), dict(idx=None), dict(w=None), dict(dt=1), dict(dt=3), dict(dt=-1),
+               dict(T=-1), dict(E=0), dict(K=0), dict(K=17), dict(sc=2), dict(sc=-1), dict(ng=0),
+               dict(ng=3), dict(tg=0), dict(tg=5), dict(K=9, tg=2), dict(ng=-4),
+               dict(scale=math.inf), dict(scale=math.nan), dict(T=1 << 28, K=8),
+               dict(lg=ctypes.c_void_p(0x100002)), dict(lg=ctypes.c_void_p(0x100001), dt=0)]:
+        assert call(**kw) == INVALID, kw
+    assert call(E=2048, ng=1, tg=1) == UNSUPPORTED
+    assert call(E=128, K=65, ng=1, tg=1) == UNSUPPORTED
+    assert call(E=130, ng=65, tg=65) == UNSUPPORTED
+    assert b.MAX_ROUTE_GROUPS == 64
+
+
+def test_route_backward_rejects_bad_arguments(buf):
+    L = b.lib()
+    lg, idx, gw, gl = (buf() for _ in range(4))
+
+    def call(lg=lg, dt=2, idx=idx, gw=gw, T=4, E=16, K=2, sc=0, nm=0, scale=1.0, gl=gl):
+        return L.ep_route_backward(lg, dt, idx, gw, T, E, K, sc, nm, scale, gl, None)
+
+    for kw in [dict(lg=None), dict(idx=None), dict(gw=None), dict(gl=None), dict(dt=1),
+               dict(T=-1), dict(E=0), dict(K=0), dict(K=17), dict(sc=2), dict(scale=-math.inf),
+               dict(lg=ctypes.c_void_p(0x100002)), dict(gl=ctypes.c_void_p(0x100001), dt=0)]:
+        assert call(**kw) == INVALID, kw
+    assert call(E=2048) == UNSUPPORTED
+    assert call(E=128, K=65) == UNSUPPORTED
+
+
+def test_expert_linear_rejects_bad_arguments(buf):
+    L = b.lib()
+    x, xs, off, cnt, w, s, z, y = (buf() for _ in range(8))
+
+    def call(x=x, xs=xs, dt=1, rows=64, off=None, cnt=cnt, C=16, E=4, I=256, N=64, G=128, w=w,
+             s=s, z=None, act=0, y=y):
+        return L.ep_expert_linear_w4(x, xs, dt, rows, off, cnt, C, E, I, N, G, w, s, z, act, y,
+                                     None)
+
+    for kw in [dict(x=None), dict(xs=None), dict(cnt=None), dict(w=None), dict(s=None),
+               dict(y=None), dict(dt=2), dict(dt=-1), dict(rows=-1), dict(rows=1 << 31),
+               dict(C=0), dict(C=17), dict(C=-1), dict(E=0), dict(I=0), dict(I=200),
+               dict(I=160, G=32), dict(N=0), dict(N=12), dict(G=16), dict(G=0), dict(G=256),
+               dict(x=BAD16), dict(w=BAD16), dict(y=BAD16), dict(s=ctypes.c_void_p(0x100004)),
+               dict(z=ctypes.c_void_p(0x100002))]:
+        assert call(**kw) == INVALID, kw
+    assert call(E=2048, C=1, rows=4096) == UNSUPPORTED
+    assert call(I=1 << 20, N=1 << 12) == UNSUPPORTED
+    assert call(I=1 << 20, N=1 << 11, act=1) == UNSUPPORTED
+
+
+@pytest.fixture
+def stand_in(monkeypatch):
+    """CPU tensors stand in for GPU ones; a call into the library fails."""
+    monkeypatch.setattr(b, "_is_gpu", lambda t: True)
+    monkeypatch.setattr(b, "lib", lambda: _NoLaunch())
+
+
+def test_binding_checks_the_gradients_tensors(stand_in):
+    T, K, H, R = 4, 2, 16, 8
+    bf = torch.bfloat16
+    go, y = torch.zeros((T, H), dtype=bf), torch.zeros((R, H), dtype=bf)
+    dst, w = torch.zeros((T, K), dtype=torch.int32), torch.zeros((T, K))
+    gy, gw = torch.zeros((R, H), dtype=bf), torch.zeros((T, K))
+    for args, kw in [((go[:2], y, dst, w), {}), ((go.float(), y, dst, w), {}),
+                     ((go, y[:, :8], dst, w), {}), ((go, y, dst.long(), w), {}),
+                     ((go, y, dst, w.double()), {}), ((go, y, dst, w[:2]), {}),
+                     ((go, y, dst, w), dict(out=(gy[:4], gw))),
+                     ((go, y, dst, w), dict(out=(gy, gw[:2]))),
+                     ((go, y, dst, w), dict(out=(gy.t().contiguous().t(), gw))),
+                     ((go, None, dst, None), {}), ((go, None, dst, w), {}),
+                     ((go, None, dst, w), dict(out=(gy, gw))),
+                     ((go, y, dst, None), dict(out=(gy, gw))),
+                     ((go, y.to("meta"), dst, w), {})]:
+        with pytest.raises((ValueError, TypeError)):
+            b.combine_backward(*args, **kw)
+    for args, kw in [((y, dst.long()), {}), ((y.float(), dst), {}), ((y[:, 0], dst), {}),
+                     ((y, dst), dict(out=go[:2])), ((y.t(), dst), {})]:
+        with pytest.raises((ValueError, TypeError)):
+            b.dispatch_backward(*args, **kw)
+
+
+def test_binding_checks_the_routers_tensors(stand_in):
+    T, E, K = 4, 16, 2
+    lg = torch.zeros((T, E))
+    idx, w = torch.zeros((T, K), dtype=torch.int64), torch.zeros((T, K))
+    for args, kw in [((lg.double(), K), {}), ((lg.half(), K), {}), ((lg[0], K), {}),
+                     ((lg.t(), K), {}), ((lg[:, ::2], K), {}),
+                     ((lg, K), dict(expert_bias=torch.zeros(E - 1))),
+                     ((lg, K), dict(expert_bias=torch.zeros(E, dtype=torch.float64))),
+                     ((lg, K), dict(score="relu")), ((lg, K), dict(out=(idx.int(), w))),
+                     ((lg, K), dict(out=(idx, w[:, :1])))]:
+        with pytest.raises((ValueError, TypeError, AssertionError)) as e:
+            b.route(*args, **kw)
+        assert not isinstance(e.value, AssertionError), (args, kw)
+    for args, kw in [((lg, idx.int(), w), {}), ((lg, idx, w[:2]), {}), ((lg, idx[:, 0], w), {}),
+                     ((lg, idx, w), dict(score="max")),
+                     ((lg, idx, w), dict(out=lg.bfloat16())), ((lg, idx[:3], w[:3]), {})]:
+        with pytest.raises((ValueError, TypeError)):
+            b.route_backward(*args, **kw)
+
+
+def test_binding_checks_the_experts_tensors(stand_in):
+    E, C, I, N, G = 3, 4, 256, 16, 64
+    x = torch.zeros((E * C, I), dtype=torch.bfloat16)
+    q = torch.zeros((E * C, I), dtype=torch.uint8)
+    xs = torch.zeros((E * C, I // 128))
+    w = torch.zeros((E, N, I // 2), dtype=torch.uint8)
+    s = torch.zeros((E, I // G, N), dtype=torch.bfloat16)
+    z = torch.zeros((E, I // G, N), dtype=torch.uint8)
+    cnt = torch.zeros(E, dtype=torch.int32)
+    off = torch.zeros(E + 1, dtype=torch.int32)
+    for args, kw in [((x.float(), w, s, cnt), dict(capacity=C)),
+                     ((q, w, s, cnt), dict(capacity=C)),
+                     ((q, w, s, cnt), dict(capacity=C, x_scales=xs[:, :1])),
+                     ((x, w, s, cnt), dict(capacity=C, x_scales=xs)),
+                     ((x, w[:, :, :64], s, cnt), dict(capacity=C)),
+                     ((x, w, s[:, :3], cnt), dict(capacity=C)),
+                     ((x, w, s.float(), cnt), dict(capacity=C)),
+                     ((x, w, s, cnt.long()), dict(capacity=C)),
+                     ((x, w, s, cnt[:2]), dict(capacity=C)),
+                     ((x, w, s, cnt), dict(capacity=C, zeros=z.int())),
+                     ((x, w, s, cnt), dict(capacity=C, expert_offsets=off)),
+                     ((x, w, s, cnt), dict(expert_offsets=off[:E])),
+                     ((x, w, s, cnt), dict(capacity=C, out=x)),
+                     ((x, w[0], s, cnt), dict(capacity=C)),
+                     ((x, w[:, :15].contiguous(), s[:, :, :15].contiguous(), cnt),
+                      dict(capacity=C, swiglu=True))]:
+        with pytest.raises((ValueError, TypeError)):
+            b.expert_linear_w4(*args, **kw)
+
+
+@pytest.mark.parametrize("name", ["tiny", "decode", "prefill"])
+def test_router_reference_agrees_with_the_workloads_gating(name):
+    """The seeded workloads draw their routing with a gating of their own
+    (numpy); on the same logits the router's reference gives the same."""
+    cfg = wl.CONFIGS[name]
+    T = 48
+    idx, w, _ = wl.route(cfg, T)
+    lg = torch.from_numpy(wl._rng(100 + cfg["c"]).standard_normal((T, cfg["E"])))
+    ri, rw = ref.route(lg, cfg["K"], score="softmax" if cfg["gating"] == "softmax" else "sigmoid",
+                       num_groups=cfg.get("n_groups", 1), topk_groups=cfg.get("topk_groups", 1),
+                       normalize=True)
+    assert np.array_equal(ri.numpy(), idx)
+    assert np.allclose(rw.numpy(), w, rtol=1e-6)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("normalize", [False, True])
+def test_router_gradient_reference_against_differences(score, normalize):
+    """The reference gradient against central differences of the reference
+    router's weights, the selected experts held fixed."""
+    g = torch.Generator().manual_seed(5)
+    T, E, K, h = 3, 7, 3, 1e-5
+    lg = torch.randn((T, E), generator=g, dtype=torch.float64)
+    gw = torch.randn((T, K), generator=g, dtype=torch.float64)
+    idx, _ = ref.route(lg, K, score=score, normalize=normalize, scale=1.5)
+
+    def loss(l):
+        v = ref.scores(l, score).gather(1, idx)
+        if normalize:
+            v = v / v.sum(1, keepdim=True)
+        return float((v * 1.5 * gw).sum())
+
+    grad, _ = ref.route_backward(lg, idx, gw, score, normalize, 1.5)
+    for t in range(T):
+        for e in range(E):
+            up, dn = lg.clone(), lg.clone()
+            up[t, e] += h
+            dn[t, e] -= h
+            assert abs((loss(up) - loss(dn)) / (2 * h) - float(grad[t, e])) < 1e-8
+
+
+def test_e4m3_values_are_the_formats():
+    v = ref.e4m3_values()
+    t = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
+    assert torch.equal(torch.nan_to_num(v, nan=1e9), torch.nan_to_num(t, nan=1e9))
