@@ -255,6 +255,12 @@ hipError_t launch_route_backward(const void* logits, bool bf16, const int64_t* t
                                  bool normalize, float scale, void* grad_logits, hipStream_t s);
 
 // ---------------------------------------------------------------- experts ---
+// A workgroup's waves, its channel tiles of 16 (gate and up halves with the
+// activation) and the row tiles of 16 it takes at once.
+constexpr int kExpertWaves = 8;
+constexpr int kExpertTiles = 4;
+constexpr int kExpertRowTiles = 2;
+
 // offsets null: expert e's rows start at e * capacity.  zeros null: 8.
 hipError_t launch_expert_linear_w4(const void* x, const float* xs, bool fp8, int64_t num_rows,
                                    const int32_t* offsets, const int32_t* counts, int capacity,
