@@ -38,6 +38,8 @@
 #include "ep_internal.h"
 #include "ep_device.h"
 
+#include <type_traits>
+
 namespace ep {
 namespace {
 
@@ -53,7 +55,7 @@ struct ExpertArgs {
     const int32_t* offsets;
     const int32_t* counts;
     int capacity;
-    int I, N;
+    int E, I, N;
     const uint8_t* w;
     const uint16_t* scales;
     const uint8_t* zeros;
@@ -118,258 +120,548 @@ __device__ __forceinline__ f32x4 mfma32_e4m3(const int (&a)[2], const int (&b)[2
     return __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(la, lb, c, 0, 0, 0);
 }
 
-// RT row tiles of 16 rows from row r0 of the expert (n rows from `begin`), the
-// channel tile at channel n0 (of each half, with SWIGLU).
-template <bool FP8, int G, bool ZP, bool SWIGLU, int RT>
-__device__ __forceinline__ void expert_tile(const ExpertArgs& p, int e, int n0, int64_t begin,
-                                            int n, int r0, f32x4* s_part) {
-    constexpr int CT = kExpertTiles;
-    constexpr bool kWide = FP8 && G == 128;     // one instruction per 128 codes
+// What a wave reads for 128 input channels (block b) of its channel and row
+// tiles.  All of a block's loads are issued together, one block ahead of the
+// arithmetic on it: the wave waits once per block, and while it works on one
+// block the next is on its way.
+template <bool FP8, int G, bool ZP, int RT, int CT>
+struct Block {
+    static constexpr int kX = FP8 && G == 128 ? 2 : 4;      // loads per row tile
+    using XV = typename std::conditional<FP8 && G != 128, uint2, i32x4>::type;
+    i32x4 w[CT];
+    XV x[RT][kX];
+    float xs[RT];
+};
+
+// Bases that are the same for the wave and 32-bit offsets of this lane.
+template <int RT, int CT>
+struct Lane {
+    const uint8_t* w;
+    const uint8_t* x;
+    const uint8_t* xs;
+    uint32_t woff[CT];     // bytes, of the channels that the lane loads
+    uint32_t xrow[RT];
+    uint32_t I, lg;
+};
+
+template <bool FP8, int G, bool ZP, int RT, int CT>
+__device__ __forceinline__ void load_weights(Block<FP8, G, ZP, RT, CT>& k,
+                                             const Lane<RT, CT>& a, int ct, int b) {
+    k.w[ct] = i32x4{0, 0, 0, 0};
+    if (G == 128 || b * 128 + a.lg * 32 < a.I)              // the last block may be short
+        k.w[ct] = *reinterpret_cast<const i32x4*>(a.w + (a.woff[ct] + b * 64));
+}
+
+template <bool FP8, int G, bool ZP, int RT, int CT>
+__device__ __forceinline__ void load_rows(Block<FP8, G, ZP, RT, CT>& k, const Lane<RT, CT>& a,
+                                          int b) {
+    const uint32_t kb = b * 128, I = a.I;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        if constexpr (FP8 && G == 128) {
+            const i32x4* xp =
+                reinterpret_cast<const i32x4*>(a.x + (a.xrow[rt] * I + kb + a.lg * 32));
+            k.x[rt][0] = xp[0];
+            k.x[rt][1] = xp[1];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                // the 8 channels of step j that this lane holds codes of
+                const uint32_t c = kb + (G < 128 ? j * 32 + a.lg * 8 : a.lg * 32 + j * 8);
+                k.x[rt][j] = {};
+                if (G == 128 || kb + j * 32 < I) {
+                    using XV = typename Block<FP8, G, ZP, RT, CT>::XV;
+                    k.x[rt][j] = *reinterpret_cast<const XV*>(
+                        a.x + (a.xrow[rt] * I + c) * (FP8 ? 1 : 2));
+                }
+            }
+        }
+        k.xs[rt] = 1.0f;
+        if constexpr (FP8)
+            k.xs[rt] = *reinterpret_cast<const float*>(a.xs + (a.xrow[rt] * (I / 128) + b) * 4);
+    }
+}
+
+// What a group's sums start from: -z sum x for each of the lane's channels
+// (in units of 2^-9 where the codes count as q * 2^-9; with the 128 that bf16
+// codes carry).
+template <bool FP8, int G, bool ZP>
+__device__ __forceinline__ f32x4 group_start(float sx, unsigned zv) {
+    const float unit = FP8 && G != 128 ? 0.001953125f : 1.0f;
+    const float more = FP8 ? 0.0f : 128.0f;
+    f32x4 c;
+    if constexpr (ZP) {
+        const unsigned m = zv & 0x0f0f0f0fu;
+        const float u = -unit * sx;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = ((float)((m >> (8 * i)) & 255u) + more) * u;
+    } else {
+        const float u = -unit * (8.0f + more) * sx;
+        c = f32x4{u, u, u, u};
+    }
+    return c;
+}
+
+// A group's sums, scaled into acc.
+__device__ __forceinline__ void add_group(f32x4& acc, const f32x4& t, uint2 sv, float xs) {
+    acc[0] = __builtin_fmaf(bf16_lo(sv.x) * xs, t[0], acc[0]);
+    acc[1] = __builtin_fmaf(bf16_hi(sv.x) * xs, t[1], acc[1]);
+    acc[2] = __builtin_fmaf(bf16_lo(sv.y) * xs, t[2], acc[2]);
+    acc[3] = __builtin_fmaf(bf16_hi(sv.y) * xs, t[3], acc[3]);
+}
+
+template <bool FP8, int G, bool ZP, int RT, int CT>
+__device__ __forceinline__ void use_block(f32x4 (&acc)[CT][RT],
+                                          Block<FP8, G, ZP, RT, CT>& k, int b, int I,
+                                          const uint2* s_sc, const unsigned* s_z) {
+    // the scales and zero points of the lane's channels of tile ct, group i of the block
+    auto scale = [&](int ct, int i) { return s_sc[i * (CT * 4) + ct * 4]; };
+    auto zero_point = [&](int ct, int i) { return ZP ? s_z[i * (CT * 4) + ct * 4] : 0u; };
+    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (FP8 && G == 128) {
+        i32x8 xv[RT], ones;
+        float sx[RT];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ones[i] = 0x38383838;   // 1.0, taken back 2^-9 below
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                int u = k.x[rt][i / 4][i % 4], v = k.x[rt][i / 4][i % 4 + 1];
+                order_e4m3(u, v);
+                xv[rt][i] = u;
+                xv[rt][i + 1] = v;
+            }
+            sx[rt] = mfma128(ones, xv[rt], zero)[0] * 0.001953125f;
+        }
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            i32x8 a;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                int o[2];
+                codes_e4m3(o, k.w[ct][i]);
+                a[2 * i] = o[0];
+                a[2 * i + 1] = o[1];
+            }
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+                add_group(acc[ct][rt],
+                          mfma128(a, xv[rt], group_start<FP8, G, ZP>(sx[rt], zero_point(ct, 0))),
+                          scale(ct, 0), k.xs[rt]);
+        }
+    } else {
+        if constexpr (G < 128) {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) transpose_groups(k.w[ct]);
+        }
+        constexpr int kSteps = G / 32;     // matrix instructions per group of scales
+        const i32x4 ones = {0x3f803f80, 0x3f803f80, 0x3f803f80, 0x3f803f80};
+        const int ones8[2] = {0x38383838, 0x38383838};
+#pragma unroll
+        for (int j0 = 0; j0 < 4; j0 += kSteps) {
+            if (G < 128 && b * 128 + j0 * 32 >= I) break;
+            f32x4 d[CT][RT];
+            if constexpr (FP8) {
+                int xv[RT][kSteps][2];
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    f32x4 sx = zero;
+#pragma unroll
+                    for (int j = 0; j < kSteps; ++j) {
+                        xv[rt][j][0] = (int)k.x[rt][j0 + j].x;
+                        xv[rt][j][1] = (int)k.x[rt][j0 + j].y;
+                        order_e4m3(xv[rt][j][0], xv[rt][j][1]);
+                        sx = mfma32_e4m3(ones8, xv[rt][j], sx);
+                    }
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+                        d[ct][rt] = group_start<FP8, G, ZP>(sx[0], zero_point(ct, j0 / kSteps));
+                }
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                    for (int j = 0; j < kSteps; ++j) {
+                        int a[2];
+                        codes_e4m3(a, k.w[ct][j0 + j]);
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt)
+                            d[ct][rt] = mfma32_e4m3(a, xv[rt][j], d[ct][rt]);
+                    }
+            } else {
+                i32x4 xv[RT][kSteps];
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    f32x4 sx = zero;
+#pragma unroll
+                    for (int j = 0; j < kSteps; ++j) {
+                        xv[rt][j] = order_bf16(k.x[rt][j0 + j]);
+                        sx = mfma32(ones, xv[rt][j], sx);
+                    }
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+                        d[ct][rt] = group_start<FP8, G, ZP>(sx[0], zero_point(ct, j0 / kSteps));
+                }
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                    for (int j = 0; j < kSteps; ++j) {
+                        const i32x4 a = codes_bf16(k.w[ct][j0 + j]);
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt)
+                            d[ct][rt] = mfma32(a, xv[rt][j], d[ct][rt]);
+                    }
+            }
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+                    add_group(acc[ct][rt], d[ct][rt], scale(ct, j0 / kSteps),
+                              FP8 ? k.xs[rt] * 512.0f : 1.0f);
+        }
+    }
+}
+
+// The same value, unknown to the compiler, which would otherwise compute what
+// follows from it once, ahead of the loop over tasks, and hold it in registers
+// that the loop over blocks needs.
+__device__ __forceinline__ int opaque(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// Rows of expert e: the first one, and how many (0 or less: none).
+__device__ __forceinline__ int64_t expert_rows(const ExpertArgs& p, int e, int64_t& begin) {
+    begin = p.offsets ? (int64_t)p.offsets[e] : (int64_t)e * p.capacity;
+    int64_t end = begin + (p.offsets ? p.counts[e] : min(p.counts[e], p.capacity));
+    if (begin < 0) begin = 0;
+    if (end > p.num_rows) end = p.num_rows;
+    return end - begin;
+}
+
+// A workgroup's task: rows [r0, n) (at most RT * 16 of them) of expert e, whose
+// rows start at `begin`; its channel tile starts at channel n0 (of each half,
+// with SWIGLU).
+struct Task {
+    int e, n0, n, r0;
+    int64_t begin;
+};
+
+// The experts' row blocks: the first 64 experts' (which a workgroup counts
+// once) in LDS, the others' counted again for every task.
+struct RowBlocks {
+    int first[64], rows[64], upto[64];   // first row, rows, row blocks of experts 0..i
+};
+
+// The task at place `task` of the order: the (row block, channel tile) pairs of
+// the experts that have rows, the row blocks of a tile next to each other (they
+// share its weights) and the tiles of an expert next to each other (they share
+// its rows, and lines of its scales).  False if there is none.
+template <int RT>
+__device__ __forceinline__ bool find_task(Task& t, const ExpertArgs& p, const RowBlocks& rbs,
+                                          int64_t task, int ntile, int channels) {
+    const int lane = threadIdx.x & 63;
+    int before = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 64) {
+        int first, rows, upto;
+        if (e0 == 0) {
+            first = rbs.first[lane];
+            rows = rbs.rows[lane];
+            upto = rbs.upto[lane];
+        } else {
+            int64_t b = 0, m = 0;
+            if (e0 + lane < p.E) m = expert_rows(p, e0 + lane, b);
+            first = (int)b;
+            rows = m > 0 ? (int)m : 0;
+            upto = (rows + RT * 16 - 1) / (RT * 16);
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int o = __shfl_up(upto, d);
+                if (lane >= d) upto += o;
+            }
+            upto += before;
+        }
+        const uint64_t hit = __ballot((int64_t)upto * ntile > task);
+        if (hit) {
+            const int at = __builtin_ctzll(hit);
+            t.e = e0 + at;
+            t.n = __builtin_amdgcn_readlane(rows, at);
+            t.begin = __builtin_amdgcn_readlane(first, at);
+            const int nb = (t.n + RT * 16 - 1) / (RT * 16);
+            const int64_t local =
+                task - (int64_t)(__builtin_amdgcn_readlane(upto, at) - nb) * ntile;
+            const int tile = (int)(local / nb), rb = (int)(local - (int64_t)tile * nb);
+            t.n0 = tile * channels;
+            t.r0 = rb * RT * 16;
+            // (false only for counts whose sum overflows)
+            return tile < ntile && t.r0 < t.n;
+        }
+        before = __builtin_amdgcn_readlane(upto, 63);
+    }
+    return false;
+}
+
+// The scales and zero points of a workgroup's channels for a chunk of input
+// channels, [group][channel / 4], and the waves' sums.
+template <int G, bool ZP, int RT, int CT>
+struct ExpertLds {
+    static constexpr int kChunk = G == 32 ? 32 : 64;       // blocks of 128 channels
+    static constexpr int kEntries = kChunk * (128 / G) * CT * 4;
+    uint2 sc[kEntries];
+    unsigned z[ZP ? kEntries : 1];
+    f32x4 part[kExpertWaves * CT * RT * 64];
+    RowBlocks rbs;
+};
+
+// Every XCD (workgroups i, i + 8, ...) gets one run of the tasks, which its
+// workgroups stride over.  Experts without rows have no tasks.  The first loads
+// of a workgroup's next task are issued before it finishes the one at hand.
+template <bool FP8, int G, bool ZP, bool SWIGLU, int RT, int CT, int NB, int WPS>
+__global__ __launch_bounds__(kExpertWaves * 64, WPS) void expert_linear_kernel(const ExpertArgs p) {
+    using Lds = ExpertLds<G, ZP, RT, CT>;
+    using Blk = Block<FP8, G, ZP, RT, CT>;
+    __shared__ Lds lds;
+    constexpr int kChannels = CT * 16 / (SWIGLU ? 2 : 1);
+    constexpr int kThreads = kExpertWaves * 64;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lg = lane >> 4, lr = lane & 15;
     const int I = p.I, N = p.N;
     const int W = SWIGLU ? 2 * N : N;
-    const int NG = I / G;
     const int nblk = (I + 127) / 128;
+    const int ntile = (N + kChannels - 1) / kChannels;
 
-    // first channel of tile ct, and the channels this lane loads and scales
-    const uint8_t* wrow[CT];
-    int sch[CT];
+    // Row blocks of the experts; every wave writes the same numbers, and reads
+    // its own.
+    int total = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 64) {
+        int64_t b = 0, m = 0;
+        if (e0 + lane < p.E) m = expert_rows(p, e0 + lane, b);
+        const int rows = m > 0 ? (int)m : 0;
+        int upto = (rows + RT * 16 - 1) / (RT * 16);
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-        const int half = SWIGLU ? ct / (CT / 2) : 0;
-        const int c0 = n0 + (SWIGLU ? ct % (CT / 2) : ct) * 16;
-        // past the last channel: any channel, its sums are not stored
-        wrow[ct] = p.w + ((int64_t)e * W + half * N + min(c0 + lr, N - 1)) * (I / 2) + lg * 16;
-        sch[ct] = half * N + min(c0 + lg * 4, N - 4);
-    }
-    const uint16_t* sc = p.scales + (int64_t)e * NG * W;
-    const uint8_t* zr = ZP ? p.zeros + (int64_t)e * NG * W : nullptr;
-    int64_t xrow[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) xrow[rt] = begin + min(r0 + rt * 16 + lr, n - 1);
-
-    f32x4 acc[CT][RT];
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) acc[ct][rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-    // scale a group's sums (d, and sx of the ones) into acc
-    auto apply = [&](int ct, int rt, int g, const f32x4& d, float sx, float xsc) {
-        const uint2 sv = *reinterpret_cast<const uint2*>(sc + (int64_t)g * W + sch[ct]);
-        float z[4] = {8.0f, 8.0f, 8.0f, 8.0f};
-        if constexpr (ZP) {
-            const unsigned zv = *reinterpret_cast<const unsigned*>(zr + (int64_t)g * W + sch[ct]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) z[i] = (float)((zv >> (8 * i)) & 15u);
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(upto, d);
+            if (lane >= d) upto += o;
         }
-        const float s[4] = {bf16_lo(sv.x), bf16_hi(sv.x), bf16_lo(sv.y), bf16_hi(sv.y)};
+        if (e0 == 0) {
+            lds.rbs.first[lane] = (int)b;
+            lds.rbs.rows[lane] = rows;
+            lds.rbs.upto[lane] = upto;
+        }
+        total += __builtin_amdgcn_readlane(upto, 63);
+    }
+    const int64_t tasks = (int64_t)total * ntile;
+    const int64_t per = (tasks + kXcds - 1) / kXcds;
+    const int64_t end = min(tasks, (blockIdx.x % kXcds + 1) * per);
+    int64_t task = blockIdx.x % kXcds * per + blockIdx.x / kXcds;
+    const int stride = gridDim.x / kXcds;
+
+    Task t;
+    Lane<RT, CT> a;
+    a.I = I;
+    a.lg = lg;
+    const uint16_t* sc;
+    const uint8_t* zr;
+    auto aim = [&]() {
+        const int lg = opaque(lane) >> 4, lr = opaque(lane) & 15;
+        a.w = p.w + (int64_t)t.e * W * (I / 2);
+        a.x = p.x + (t.begin + t.r0) * I * (FP8 ? 1 : 2);
+        a.xs = FP8 ? reinterpret_cast<const uint8_t*>(p.xs + (t.begin + t.r0) * (I / 128))
+                   : nullptr;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float t;
-            if constexpr (kWide)
-                t = __builtin_fmaf(-z[i], sx, d[i]);
-            else if constexpr (FP8)
-                t = __builtin_fmaf(512.0f, d[i], -z[i] * sx);
-            else
-                t = __builtin_fmaf(-(z[i] + 128.0f), sx, d[i]);
-            acc[ct][rt][i] = __builtin_fmaf(FP8 ? s[i] * xsc : s[i], t, acc[ct][rt][i]);
+        for (int ct = 0; ct < CT; ++ct) {
+            const int half = SWIGLU ? ct / (CT / 2) : 0;
+            const int c0 = t.n0 + (SWIGLU ? ct % (CT / 2) : ct) * 16;
+            // past the last channel: any channel, its sums are not stored
+            a.woff[ct] = (uint32_t)(half * N + min(c0 + lr, N - 1)) * (uint32_t)(I / 2) + lg * 16;
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) a.xrow[rt] = min(rt * 16 + lr, t.n - 1 - t.r0);
+        sc = p.scales + (int64_t)t.e * (I / G) * W;
+        zr = ZP ? p.zeros + (int64_t)t.e * (I / G) * W : nullptr;
+    };
+
+    // Scales of the chunk of blocks from c0, in rounds of kBatch entries a
+    // thread: fetched, then kept in LDS.
+    constexpr int kBatch = 4, kRound = kBatch * kThreads;
+    uint2 bs[kBatch];
+    unsigned bz[kBatch];
+    auto entries = [&](int c0) {
+        return (min((c0 + Lds::kChunk) * 128, I) / G - c0 * (128 / G)) * (CT * 4);
+    };
+    auto fetch = [&](int c0, int first) {
+        const int tid = opaque(threadIdx.x);
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            // past the last entry: that one again
+            const int i = min(first + q * kThreads + tid, entries(c0) - 1);
+            const int u = i % (CT * 4), ct = u / 4;
+            const int half = SWIGLU ? ct / (CT / 2) : 0;
+            const int ch = t.n0 + (SWIGLU ? ct % (CT / 2) : ct) * 16 + u % 4 * 4;
+            const uint32_t at = (uint32_t)(c0 * (128 / G) + i / (CT * 4)) * W + half * N +
+                                min(ch, N - 4);
+            bs[q] = *reinterpret_cast<const uint2*>(sc + at);
+            if constexpr (ZP) bz[q] = *reinterpret_cast<const unsigned*>(zr + at);
+        }
+    };
+    auto keep = [&](int c0, int first) {
+        const int tid = opaque(threadIdx.x);
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            const int i = first + q * kThreads + tid;
+            if (i < entries(c0)) {
+                lds.sc[i] = bs[q];
+                if constexpr (ZP) lds.z[i] = bz[q];
+            }
         }
     };
 
-    for (int b = wave; b < nblk; b += kExpertWaves) {
-        const int kb = b * 128;
-        i32x4 wv[CT];
-        const bool whole = G == 128 || kb + lg * 32 < I;    // the last block may be short
+    // A wave takes steps of NB neighbouring blocks, every kExpertWaves-th step
+    // of a chunk.  The load after its last step takes that step again, and a
+    // step's second block past the end the last one, so that the number of
+    // loads under way is the same on every path.
+    Blk k0[NB], k1[NB];
+    f32x4 acc[CT][RT];
+    auto load = [&](Blk (&k)[NB], int c0, int st) {
+        const int c1 = min(c0 + Lds::kChunk, nblk);
+        // the 64 bytes of a row that neighbouring blocks read share a line
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-            wv[ct] = i32x4{0, 0, 0, 0};
-            if (whole) wv[ct] = *reinterpret_cast<const i32x4*>(wrow[ct] + b * 64);
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+                load_weights<FP8, G, ZP, RT, CT>(k[i], a, ct, min(c0 + st * NB + i, c1 - 1));
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+            load_rows<FP8, G, ZP, RT, CT>(k[i], a, min(c0 + st * NB + i, c1 - 1));
+        __builtin_amdgcn_sched_barrier(0);      // loads stay ahead of the arithmetic
+    };
+    auto use = [&](Blk (&k)[NB], int c0, int st) {
+        const int c1 = min(c0 + Lds::kChunk, nblk);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const int b = st * NB + i;          // of the chunk
+            if (NB == 1 || c0 + b < c1) {
+                const int at = b * (128 / G) * (CT * 4) + lg;
+                use_block<FP8, G, ZP, RT, CT>(acc, k[i], c0 + b, I, lds.sc + at,
+                                              lds.z + (ZP ? at : 0));
+            }
         }
-        float xsc[RT];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) xsc[rt] = FP8 ? p.xs[xrow[rt] * (I / 128) + b] : 1.0f;
-        const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // A chunk's first loads: the scales ahead of the weights, which then travel
+    // while the scales are put in place.
+    auto start = [&](int c0) {
+        fetch(c0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        if (wave * NB < min(Lds::kChunk, nblk - c0)) load(k0, c0, wave);
+    };
 
-        if constexpr (kWide) {
-            i32x8 xv[RT];
-            float sx[RT];
-            i32x8 ones;
+    bool more = task < end && find_task<RT>(t, p, lds.rbs, task, ntile, kChannels);
+    if (more) {
+        aim();
+        start(0);
+    }
+    while (more) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ones[i] = 0x38383838;    // 1.0, and 2^-9 undoes the scale
+        for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                const i32x4* xp =
-                    reinterpret_cast<const i32x4*>(p.x + xrow[rt] * I + kb + lg * 32);
-                const i32x4 a = xp[0], c = xp[1];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    xv[rt][i] = a[i];
-                    xv[rt][4 + i] = c[i];
-                }
-#pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    int u = xv[rt][i], v = xv[rt][i + 1];
-                    order_e4m3(u, v);
-                    xv[rt][i] = u;
-                    xv[rt][i + 1] = v;
-                }
-                sx[rt] = mfma128(ones, xv[rt], zero)[0] * 0.001953125f;
+            for (int rt = 0; rt < RT; ++rt) acc[ct][rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int c0 = 0; c0 < nblk; c0 += Lds::kChunk) {
+            if (c0 > 0) {
+                start(c0);
+                __syncthreads();                // the last chunk's scales are done with
             }
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                i32x8 a;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    int o[2];
-                    codes_e4m3(o, wv[ct][i]);
-                    a[2 * i] = o[0];
-                    a[2 * i + 1] = o[1];
-                }
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-                    apply(ct, rt, b, mfma128(a, xv[rt], zero), sx[rt], xsc[rt]);
+            keep(c0, 0);
+            for (int first = kRound; first < entries(c0); first += kRound) {
+                fetch(c0, first);
+                keep(c0, first);
             }
-        } else {
-            if constexpr (G < 128) {
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) transpose_groups(wv[ct]);
+            __syncthreads();
+            const int nstep = (min(Lds::kChunk, nblk - c0) + NB - 1) / NB;
+            if (wave < nstep) {
+                const int last = wave + (nstep - 1 - wave) / kExpertWaves * kExpertWaves;
+                int st = wave;
+                for (; st < last; st += 2 * kExpertWaves) {
+                    load(k1, c0, st + kExpertWaves);
+                    use(k0, c0, st);
+                    load(k0, c0, min(st + 2 * kExpertWaves, last));
+                    use(k1, c0, st + kExpertWaves);
+                }
+                if (st == last) use(k0, c0, st);
             }
-            constexpr int kSteps = G / 32;     // matrix instructions per group of scales
-            const i32x4 ones = {0x3f803f80, 0x3f803f80, 0x3f803f80, 0x3f803f80};
-            const int ones8[2] = {0x38383838, 0x38383838};
+        }
+        const Task done = t;
+        task += stride;
+        more = task < end && find_task<RT>(t, p, lds.rbs, task, ntile, kChannels);
+        if (more) {
+            aim();
+            start(0);
+        }
+
+        // the waves' sums, in wave order; wave i finishes tiles i, i + kExpertWaves, ...
+        constexpr int kTiles = CT * RT;
 #pragma unroll
-            for (int j0 = 0; j0 < 4; j0 += kSteps) {
-                if (G < 128 && kb + j0 * 32 >= I) break;
-                f32x4 d[CT][RT], sx[RT];
+        for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    sx[rt] = zero;
+            for (int rt = 0; rt < RT; ++rt)
+                lds.part[(wave * kTiles + ct * RT + rt) * 64 + lane] = acc[ct][rt];
+        __syncthreads();
+        constexpr int kOut = SWIGLU ? kTiles / 2 : kTiles;
+        for (int o = wave; o < kOut; o += kExpertWaves) {
+            const int ct = o / RT, rt = o % RT;
+            f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f}, u = v;
+            for (int i = 0; i < kExpertWaves; ++i) v += lds.part[(i * kTiles + o) * 64 + lane];
+            if constexpr (SWIGLU) {
+                for (int i = 0; i < kExpertWaves; ++i)
+                    u += lds.part[(i * kTiles + kOut + o) * 64 + lane];
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) d[ct][rt] = zero;
-                }
-#pragma unroll
-                for (int j = j0; j < j0 + kSteps; ++j) {
-                    // codes of step j in this lane: 8 from here
-                    const int k = kb + (G < 128 ? j * 32 + lg * 8 : lg * 32 + j * 8);
-                    if constexpr (FP8) {
-                        int xv[RT][2];
-#pragma unroll
-                        for (int rt = 0; rt < RT; ++rt) {
-                            const uint2 v =
-                                *reinterpret_cast<const uint2*>(p.x + xrow[rt] * I + k);
-                            xv[rt][0] = (int)v.x;
-                            xv[rt][1] = (int)v.y;
-                            order_e4m3(xv[rt][0], xv[rt][1]);
-                            sx[rt] = mfma32_e4m3(ones8, xv[rt], sx[rt]);
-                        }
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) {
-                            int a[2];
-                            codes_e4m3(a, wv[ct][j]);
-#pragma unroll
-                            for (int rt = 0; rt < RT; ++rt)
-                                d[ct][rt] = mfma32_e4m3(a, xv[rt], d[ct][rt]);
-                        }
-                    } else {
-                        i32x4 xv[RT];
-#pragma unroll
-                        for (int rt = 0; rt < RT; ++rt) {
-                            xv[rt] = order_bf16(*reinterpret_cast<const i32x4*>(
-                                p.x + (xrow[rt] * I + k) * 2));
-                            sx[rt] = mfma32(ones, xv[rt], sx[rt]);
-                        }
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) {
-                            const i32x4 a = codes_bf16(wv[ct][j]);
-#pragma unroll
-                            for (int rt = 0; rt < RT; ++rt)
-                                d[ct][rt] = mfma32(a, xv[rt], d[ct][rt]);
-                        }
-                    }
-                }
-                const int g = (kb + j0 * 32) / G;
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
-                        apply(ct, rt, g, d[ct][rt], sx[rt][0], xsc[rt]);
+                for (int i = 0; i < 4; ++i) v[i] = v[i] / (1.0f + expf(-v[i])) * u[i];
+            }
+            const int row = done.r0 + rt * 16 + lr, c = done.n0 + ct * 16 + lg * 4;
+            if (row < done.n && c < N) {
+                const uint2 o2 = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+                *reinterpret_cast<uint2*>(p.y + (done.begin + row) * N + c) = o2;
             }
         }
     }
-
-    // the waves' sums, in wave order; wave i finishes tiles i, i + kExpertWaves, ...
-    constexpr int kTiles = CT * RT;
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-            s_part[(wave * kTiles + ct * RT + rt) * 64 + lane] = acc[ct][rt];
-    __syncthreads();
-    constexpr int kOut = SWIGLU ? kTiles / 2 : kTiles;
-    for (int o = wave; o < kOut; o += kExpertWaves) {
-        const int ct = o / RT, rt = o % RT;
-        f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f}, u = a;
-        for (int v = 0; v < kExpertWaves; ++v) a += s_part[(v * kTiles + o) * 64 + lane];
-        if constexpr (SWIGLU) {
-            for (int v = 0; v < kExpertWaves; ++v)
-                u += s_part[(v * kTiles + kOut + o) * 64 + lane];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = a[i] / (1.0f + expf(-a[i])) * u[i];
-        }
-        const int row = r0 + rt * 16 + lr, c = n0 + ct * 16 + lg * 4;
-        if (row < n && c < N) {
-            const uint2 v = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
-            *reinterpret_cast<uint2*>(p.y + (begin + row) * N + c) = v;
-        }
-    }
-    __syncthreads();
 }
 
 template <bool FP8, int G, bool ZP, bool SWIGLU>
-__global__ __launch_bounds__(kExpertWaves * 64) void expert_linear_kernel(const ExpertArgs p) {
-    __shared__ f32x4 s_part[kExpertWaves * kExpertTiles * kExpertRowTiles * 64];
-    const int e = blockIdx.y;
-    int64_t begin = p.offsets ? (int64_t)p.offsets[e] : (int64_t)e * p.capacity;
-    int64_t end = begin + (p.offsets ? p.counts[e] : min(p.counts[e], p.capacity));
-    if (begin < 0) begin = 0;
-    if (end > p.num_rows) end = p.num_rows;
-    if (end <= begin) return;
-    const int n = (int)(end - begin);
-    const int n0 = blockIdx.x * (kExpertTiles * 16 / (SWIGLU ? 2 : 1));
-    for (int r0 = blockIdx.z * kExpertRowTiles * 16; r0 < n;
-         r0 += gridDim.z * kExpertRowTiles * 16) {
-        if (n - r0 <= 16)
-            expert_tile<FP8, G, ZP, SWIGLU, 1>(p, e, n0, begin, n, r0, s_part);
-        else
-            expert_tile<FP8, G, ZP, SWIGLU, kExpertRowTiles>(p, e, n0, begin, n, r0, s_part);
-    }
+void launch_r(dim3 grid, hipStream_t s, const ExpertArgs& p, int rt) {
+    const dim3 block(kExpertWaves * 64);
+    if (rt == 1)
+        hipLaunchKernelGGL(
+            (expert_linear_kernel<FP8, G, ZP, SWIGLU, 1, kExpertTiles,
+                                  few_blocks(FP8), few_waves(FP8)>), grid,
+            block, 0, s, p);
+    else
+        hipLaunchKernelGGL(
+            (expert_linear_kernel<FP8, G, ZP, SWIGLU, kExpertRowTiles, kExpertTiles, 1, 2>), grid,
+            block, 0, s, p);
 }
 
 template <bool FP8, int G>
-void launch_g(dim3 grid, hipStream_t s, const ExpertArgs& p, bool swiglu) {
-    const dim3 block(kExpertWaves * 64);
+void launch_g(dim3 grid, hipStream_t s, const ExpertArgs& p, bool swiglu, int rt) {
     if (p.zeros) {
         if (swiglu)
-            hipLaunchKernelGGL((expert_linear_kernel<FP8, G, true, true>), grid, block, 0, s, p);
+            launch_r<FP8, G, true, true>(grid, s, p, rt);
         else
-            hipLaunchKernelGGL((expert_linear_kernel<FP8, G, true, false>), grid, block, 0, s, p);
+            launch_r<FP8, G, true, false>(grid, s, p, rt);
     } else {
         if (swiglu)
-            hipLaunchKernelGGL((expert_linear_kernel<FP8, G, false, true>), grid, block, 0, s, p);
+            launch_r<FP8, G, false, true>(grid, s, p, rt);
         else
-            hipLaunchKernelGGL((expert_linear_kernel<FP8, G, false, false>), grid, block, 0, s, p);
+            launch_r<FP8, G, false, false>(grid, s, p, rt);
     }
 }
 
 template <bool FP8>
-void launch_t(int G, dim3 grid, hipStream_t s, const ExpertArgs& p, bool swiglu) {
+void launch_t(int G, dim3 grid, hipStream_t s, const ExpertArgs& p, bool swiglu, int rt) {
     switch (G) {
-        case 32: launch_g<FP8, 32>(grid, s, p, swiglu); break;
-        case 64: launch_g<FP8, 64>(grid, s, p, swiglu); break;
-        default: launch_g<FP8, 128>(grid, s, p, swiglu); break;
+        case 32: launch_g<FP8, 32>(grid, s, p, swiglu, rt); break;
+        case 64: launch_g<FP8, 64>(grid, s, p, swiglu, rt); break;
+        default: launch_g<FP8, 128>(grid, s, p, swiglu, rt); break;
     }
 }
 
@@ -382,17 +674,20 @@ hipError_t launch_expert_linear_w4(const void* x, const float* xs, bool fp8, int
                                    uint16_t* y, hipStream_t s) {
     if (num_rows == 0) return hipSuccess;
     const ExpertArgs p = {static_cast<const uint8_t*>(x), xs, num_rows, offsets, counts, capacity,
-                          I, N, w, scales, zeros, y};
-    const int tile = kExpertTiles * 16 / (swiglu ? 2 : 1);
-    // row blocks side by side where an expert has many rows on average
+                          E, I, N, w, scales, zeros, y};
     const int64_t avg = offsets ? num_rows / E : capacity;
-    int z = (int)((avg + kExpertRowTiles * 16 - 1) / (kExpertRowTiles * 16));
-    z = z < 1 ? 1 : z > 8 ? 8 : z;
-    const dim3 grid((unsigned)((N + tile - 1) / tile), (unsigned)E, (unsigned)z);
+    const int rt = avg <= kExpertFewRows ? 1 : kExpertRowTiles;
+    const int tile = kExpertTiles * 16 / (swiglu ? 2 : 1);
+    // at most one workgroup per task, and no more than the GPU holds at once
+    const int64_t blocks = offsets ? E + num_rows / (rt * 16)
+                                   : (int64_t)E * ((capacity + rt * 16 - 1) / (rt * 16));
+    const int64_t tasks = blocks * ((N + tile - 1) / tile);
+    const int64_t held = (rt == 1 ? few_waves(fp8) : 2) * 4 / kExpertWaves * kCus;
+    const dim3 grid((unsigned)(((tasks < held ? tasks : held) + kXcds - 1) / kXcds * kXcds));
     if (fp8)
-        launch_t<true>(G, grid, s, p, swiglu);
+        launch_t<true>(G, grid, s, p, swiglu, rt);
     else
-        launch_t<false>(G, grid, s, p, swiglu);
+        launch_t<false>(G, grid, s, p, swiglu, rt);
     return hipGetLastError();
 }
 
