@@ -31,52 +31,81 @@ namespace {
 constexpr float kFltMax = 3.4028234663852886e38f;
 
 // Maximum and sum over aligned segments of L lanes, the same for every lane of
-// a segment; all lanes active.
-__device__ __forceinline__ uint32_t dpp_move(uint32_t v, int step) {
-    switch (step) {
-        case 0: return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xf, 0xf, false);
-        case 1: return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xf, 0xf, false);
-        case 2: return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, false);
-        case 3: return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xf, 0xf, false);
-        case 4: return (uint32_t)__shfl_xor((int)v, 16);
-        default: return (uint32_t)__shfl_xor((int)v, 32);
-    }
-}
-template <typename V>
-__device__ __forceinline__ V seg_move(V v, int step) {
-    if constexpr (sizeof(V) == 4) {
-        return __builtin_bit_cast(V, dpp_move(__builtin_bit_cast(uint32_t, v), step));
+// a segment; all lanes active.  Inside a row of 16 lanes a step is one DPP move
+// (neighbours, pairs, half rows and rows mirrored), across rows one swap of
+// rows or halves, after which both partners stand in one lane.
+template <int STEP>
+__device__ __forceinline__ void partners(uint32_t& a, uint32_t& b) {
+    constexpr int kDpp[4] = {0xB1, 0x4E, 0x141, 0x140};
+    if constexpr (STEP < 4) {
+        b = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a, kDpp[STEP], 0xf, 0xf, false);
+    } else if constexpr (STEP == 4) {
+        const auto r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+        a = r[0];
+        b = r[1];
     } else {
-        const uint64_t u = __builtin_bit_cast(uint64_t, v);
-        const uint32_t lo = dpp_move((uint32_t)u, step), hi = dpp_move((uint32_t)(u >> 32), step);
-        return __builtin_bit_cast(V, (uint64_t)hi << 32 | lo);
+        const auto r = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+        a = r[0];
+        b = r[1];
     }
 }
-template <int L, typename V>
+template <int STEP>
+__device__ __forceinline__ void partners(float& a, float& b) {
+    uint32_t x = __float_as_uint(a), y;
+    partners<STEP>(x, y);
+    a = __uint_as_float(x);
+    b = __uint_as_float(y);
+}
+template <int STEP>
+__device__ __forceinline__ void partners(double& a, double& b) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, a);
+    uint32_t x0 = (uint32_t)u, x1 = (uint32_t)(u >> 32), y0, y1;
+    partners<STEP>(x0, y0);
+    partners<STEP>(x1, y1);
+    a = __builtin_bit_cast(double, (uint64_t)x1 << 32 | x0);
+    b = __builtin_bit_cast(double, (uint64_t)y1 << 32 | y0);
+}
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
+template <int L, int STEP = 0, typename V>
 __device__ __forceinline__ V seg_max(V v) {
-#pragma unroll
-    for (int i = 0; (1 << i) < L; ++i) {
-        const V o = seg_move(v, i);
-        v = o > v ? o : v;
+    if constexpr ((1 << STEP) < L) {
+        V o;
+        partners<STEP>(v, o);
+        return seg_max<L, STEP + 1>(larger(v, o));
     }
     return v;
 }
-template <int L, typename V>
+template <int L, int STEP = 0, typename V>
 __device__ __forceinline__ V seg_sum(V v) {
-#pragma unroll
-    for (int i = 0; (1 << i) < L; ++i) v += seg_move(v, i);
+    if constexpr ((1 << STEP) < L) {
+        V o;
+        partners<STEP>(v, o);
+        return seg_sum<L, STEP + 1>(v + o);
+    }
     return v;
+}
+// The two largest values of a segment of `lanes` lanes (a power of two, at
+// most L), from the two largest of each lane.
+template <int L, int STEP = 0>
+__device__ __forceinline__ void seg_top2(double& a, double& b, int lanes) {
+    if constexpr ((1 << STEP) < L) {
+        if ((1 << STEP) < lanes) {
+            double c = a, d = b, oa, ob;
+            partners<STEP>(c, oa);
+            partners<STEP>(d, ob);
+            a = larger(c, oa);
+            b = larger(fmin(c, oa), larger(d, ob));
+            seg_top2<L, STEP + 1>(a, b, lanes);
+        }
+    }
 }
 
-// Unsigned keys in the order of the values, 0 below all of them (an expert
-// that is not available).  Adding 0 makes -0 and +0 the same key.
-__device__ __forceinline__ uint32_t order_key(float v) {
-    const uint32_t u = __float_as_uint(v + 0.0f);
-    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
-}
-__device__ __forceinline__ uint64_t order_key(double v) {
-    const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
-    return u ^ ((u >> 63) ? ~0ull : 1ull << 63);
+// LDS written by some lanes of a wave is read by others: the wave's LDS
+// accesses happen in order, the compiler has to keep them so.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 
 __device__ __forceinline__ float load_logit(const float* p) { return *p; }
@@ -166,15 +195,15 @@ __device__ __forceinline__ void store_row(const float (&o)[VPL], uint16_t* row, 
 __device__ __forceinline__ double sigmoid64(double l) { return 1.0 / (1.0 + exp(-l)); }
 
 // FULL: choices in fp64 (a bias or groups); otherwise the logits decide.
-// Dynamic LDS, per token of the workgroup: K slots (int), then with groups
-// E choices (double, at an 8-byte boundary), NG group scores (double) and NG
-// flags (int).
+// Dynamic LDS, per token of the workgroup: K slots' expert (int) and logit
+// (float), then with groups that do not lie on whole lanes E choices (double),
+// NG group scores (double) and NG flags (int).
 template <typename LT, int VPL, int L, bool FULL>
 __global__ __launch_bounds__(kRouteThreads) void route_kernel(
     const LT* __restrict__ logits, const float* __restrict__ bias, int T, int E, int K,
     bool softmax, int NG, int TG, bool normalize, float scale, int64_t* __restrict__ topk_idx,
     float* __restrict__ topk_weights, bool vec) {
-    using Key = typename std::conditional<FULL, uint64_t, uint32_t>::type;
+    using Choice = typename std::conditional<FULL, double, float>::type;
     constexpr int kTokens = kRouteThreads / L;
     extern __shared__ EP_LDS_ALIGN unsigned char s_raw[];
     const int lane = threadIdx.x & 63;
@@ -183,15 +212,20 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(
     const int64_t t = (int64_t)blockIdx.x * kTokens + tok;
     const bool live = t < T;
     int* s_idx = reinterpret_cast<int*>(s_raw) + tok * K;
+    float* s_logit = reinterpret_cast<float*>(s_raw) + kTokens * K + tok * K;
 
     const int e0 = sl * VPL;
     float l[VPL];
-    const LT* row = logits + t * E;
     if (live) {
-        load_row<VPL>(l, row, e0, E, vec);
+        load_row<VPL>(l, logits + t * E, e0, E, vec);
     } else {
 #pragma unroll
         for (int j = 0; j < VPL; ++j) l[j] = -INFINITY;
+    }
+    float bj[VPL];
+    if constexpr (FULL) {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) bj[j] = bias && e0 + j < E ? bias[e0 + j] : 0.0f;
     }
     float lmax = -INFINITY;
 #pragma unroll
@@ -204,8 +238,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(
     // the softmax over all experts: its maximum and sum
     float m = 0.0f;
     double total = 1.0;
-    const bool need_total = softmax && (FULL || !normalize);
-    if (need_total) {
+    if (softmax && (FULL || !normalize)) {
         m = fmaxf(seg_max<L>(lmax), -kFltMax);
         if constexpr (FULL) {
             double a = 0.0;
@@ -220,108 +253,137 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(
         }
     }
 
-    Key key[VPL];
+    // what orders the experts; -inf: not available
+    Choice key[VPL];
     if constexpr (FULL) {
-        double ch[VPL];
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
             const double s = softmax ? exp((double)l[j] - (double)m) / total
                                      : sigmoid64((double)l[j]);
-            double c = s;
-            if (bias && e0 + j < E) c += (double)bias[e0 + j];
-            // not available: the logit, or a bias of -inf or NaN
-            ch[j] = (l[j] > -INFINITY && c > -INFINITY) ? c : -INFINITY;
-            key[j] = ch[j] > -INFINITY ? order_key(bias ? c : (double)l[j]) : 0;
+            const double c = s + (double)bj[j];
+            key[j] = (l[j] > -INFINITY && c > -INFINITY) ? c : -INFINITY;
         }
         if (NG > 1) {
-            const size_t idx_bytes = ((size_t)kTokens * K * 4 + 15) & ~(size_t)15;
-            double* s_ch = reinterpret_cast<double*>(s_raw + idx_bytes) + tok * (E + 2 * NG);
-            double* s_gs = s_ch + E;
-            int* s_flag = reinterpret_cast<int*>(s_gs + NG);
-#pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                if (e0 + j < E) s_ch[e0 + j] = ch[j];
-            __syncthreads();
             const int gsz = E / NG;
-            for (int g = sl; g < NG; g += L) {
-                double a = -INFINITY, b = -INFINITY;   // the two largest of the group
-                int i = g < gsz ? g : 0;               // lanes start at different banks
-                for (int n = 0; n < gsz; ++n) {
-                    const double v = s_ch[g * gsz + i];
-                    if (v > a) {
-                        b = a;
-                        a = v;
-                    } else if (v > b) {
-                        b = v;
-                    }
-                    if (++i == gsz) i = 0;
+            const int lanes = gsz / VPL;             // lanes of a group, if whole
+            if (gsz % VPL == 0 && (lanes & (lanes - 1)) == 0) {
+                double a = -INFINITY, b = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) {
+                    b = larger(b, fmin(a, key[j]));
+                    a = larger(a, key[j]);
                 }
-                s_gs[g] = b > -INFINITY ? a + b : a;
-            }
-            __syncthreads();
-            for (int g = sl; g < NG; g += L) {
-                const double v = s_gs[g];
+                seg_top2<L>(a, b, lanes);
+                const double mine = b > -INFINITY ? a + b : a;
+                const int g = e0 / gsz;
                 int better = 0;
                 for (int i = 0; i < NG; ++i) {
-                    const double o = s_gs[i];
-                    better += (o > v || (o == v && i < g)) ? 1 : 0;
+                    const double o = __shfl(mine, (lane - sl) + i * lanes);
+                    better += (o > mine || (o == mine && i < g)) ? 1 : 0;
                 }
-                s_flag[g] = better < TG ? 1 : 0;
-            }
-            __syncthreads();
 #pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                if (e0 + j < E && !s_flag[(e0 + j) / gsz]) key[j] = 0;
+                for (int j = 0; j < VPL; ++j) {
+                    const bool open = better < TG && key[j] > -INFINITY;
+                    const double by = bias ? key[j] : (double)l[j];
+                    key[j] = open ? by : -INFINITY;
+                }
+            } else {
+                const size_t head = ((size_t)kTokens * K * 8 + 15) & ~(size_t)15;
+                double* s_ch = reinterpret_cast<double*>(s_raw + head) + tok * (E + 2 * NG);
+                double* s_gs = s_ch + E;
+                int* s_flag = reinterpret_cast<int*>(s_gs + NG);
+#pragma unroll
+                for (int j = 0; j < VPL; ++j)
+                    if (e0 + j < E) s_ch[e0 + j] = key[j];
+                wave_sync();
+                for (int g = sl; g < NG; g += L) {
+                    double a = -INFINITY, b = -INFINITY;
+                    int i = g < gsz ? g : 0;         // lanes start at different banks
+                    for (int n = 0; n < gsz; ++n) {
+                        const double v = s_ch[g * gsz + i];
+                        b = larger(b, fmin(a, v));
+                        a = larger(a, v);
+                        if (++i == gsz) i = 0;
+                    }
+                    s_gs[g] = b > -INFINITY ? a + b : a;
+                }
+                wave_sync();
+                for (int g = sl; g < NG; g += L) {
+                    const double v = s_gs[g];
+                    int better = 0;
+                    for (int i = 0; i < NG; ++i) {
+                        const double o = s_gs[i];
+                        better += (o > v || (o == v && i < g)) ? 1 : 0;
+                    }
+                    s_flag[g] = better < TG ? 1 : 0;
+                }
+                wave_sync();
+                int g = e0 / gsz, in = e0 - g * gsz;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) {
+                    // (no expert of a group past the last one is available)
+                    const bool open = (s_flag[min(g, NG - 1)] != 0) & (key[j] > -INFINITY);
+                    const double by = bias ? key[j] : (double)l[j];
+                    key[j] = open ? by : -INFINITY;
+                    const bool next = ++in == gsz;
+                    in = next ? 0 : in;
+                    g += next ? 1 : 0;
+                }
+            }
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) key[j] = l[j] > -INFINITY ? order_key(l[j]) : 0;
+        for (int j = 0; j < VPL; ++j) key[j] = l[j];
     }
 
     const uint64_t segmask = (L == 64 ? ~0ull : ((1ull << (L & 63)) - 1)) << (lane - sl);
     for (int k = 0; k < K; ++k) {
-        Key best = 0;
+        Choice best = key[0];
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) best = key[j] > best ? key[j] : best;
-        const Key top = seg_max<L>(best);
-        const uint64_t eq = __ballot(best == top && top != 0) & segmask;
+        for (int j = 1; j < VPL; ++j) best = larger(best, key[j]);
+        const Choice top = seg_max<L>(best);
+        const uint64_t eq = __ballot(best == top && top > -INFINITY) & segmask;
         if (eq != 0 && __builtin_ctzll(eq) == (unsigned)lane) {
             int at = 0;
+            float lv = l[0];
 #pragma unroll
             for (int j = VPL - 1; j >= 0; --j)
-                if (key[j] == top) at = j;
+                if (key[j] == top) {
+                    at = j;
+                    lv = l[j];
+                }
 #pragma unroll
             for (int j = 0; j < VPL; ++j)
-                if (j == at) key[j] = 0;
+                if (j == at) key[j] = -INFINITY;
             s_idx[k] = e0 + at;
+            s_logit[k] = lv;
         }
     }
-    __syncthreads();
+    wave_sync();
 
     // slot k of the token: lanes k, k + L, ... of its segment
     if (normalize && softmax) {
         // over the selected experts alone, from their own maximum
         m = -kFltMax;
         for (int k = sl; k < K; k += L)
-            if (s_idx[k] >= 0) m = fmaxf(m, clean_logit(load_logit(row + s_idx[k])));
+            if (s_idx[k] >= 0) m = fmaxf(m, s_logit[k]);
         m = seg_max<L>(m);
     }
-    double sum = 0.0;
+    double sum = softmax ? total : 1.0;
     if (normalize) {
+        sum = 0.0;
         for (int k = sl; k < K; k += L)
             if (s_idx[k] >= 0) {
-                const double v = (double)clean_logit(load_logit(row + s_idx[k]));
+                const double v = (double)s_logit[k];
                 sum += softmax ? exp(v - (double)m) : sigmoid64(v);
             }
         sum = seg_sum<L>(sum);
-    } else {
-        sum = softmax ? total : 1.0;
     }
     for (int k = sl; k < K; k += L) {
         const int e = s_idx[k];
         double w = 0.0;
         if (e >= 0 && sum > 0.0) {
-            const double v = (double)clean_logit(load_logit(row + e));
+            const double v = (double)s_logit[k];
             w = (softmax ? exp(v - (double)m) : sigmoid64(v)) / sum * (double)scale;
         }
         if (live) {
@@ -427,7 +489,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(
         }
         s_val[k] = (float)d;
     }
-    __syncthreads();
+    wave_sync();
     float o[VPL];
 #pragma unroll
     for (int j = 0; j < VPL; ++j) o[j] = 0.0f;
@@ -459,7 +521,7 @@ hipError_t launch_route_l(const LT* logits, const float* bias, int T, int E, int
     constexpr int kTokens = kRouteThreads / L;
     const dim3 grid((unsigned)((T + kTokens - 1) / kTokens)), block(kRouteThreads);
     const bool vec = rows_vectorised(logits, sizeof(LT), E);
-    size_t lds = ((size_t)kTokens * K * 4 + 15) & ~(size_t)15;
+    size_t lds = ((size_t)kTokens * K * 8 + 15) & ~(size_t)15;
     if (NG > 1) lds += (size_t)kTokens * (E + 2 * NG) * 8;
     if (bias || NG > 1)
         hipLaunchKernelGGL((route_kernel<LT, VPL, L, true>), grid, block, lds, s, logits, bias, T,
@@ -485,16 +547,22 @@ hipError_t launch_route_backward_l(const LT* logits, const int64_t* topk_idx, co
     return hipGetLastError();
 }
 
-// The lanes per token and experts per lane: the fewest lanes that hold the
-// experts at 16 a lane.
-#define EP_ROUTE_DISPATCH(FN, LT, ...)                             \
-    do {                                                           \
-        if (E <= 8) return FN<LT, 1, 8>(__VA_ARGS__);              \
-        if (E <= 64) return FN<LT, 4, 16>(__VA_ARGS__);            \
-        if (E <= 128) return FN<LT, 8, 16>(__VA_ARGS__);           \
-        if (E <= 256) return FN<LT, 16, 16>(__VA_ARGS__);          \
-        if (E <= 512) return FN<LT, 16, 32>(__VA_ARGS__);          \
-        return FN<LT, 16, 64>(__VA_ARGS__);                        \
+// Experts per lane and lanes per token: a whole wave for a token while the
+// batch is small (short chains), else as few lanes as hold the experts at 16 a
+// lane (less work per token).
+#define EP_ROUTE_DISPATCH(FN, LT, ...)                              \
+    do {                                                            \
+        const bool few = T <= kRouteWideTokens;                     \
+        if (E <= 8) return FN<LT, 1, 8>(__VA_ARGS__);               \
+        if (E <= 64)                                                \
+            return few ? FN<LT, 1, 64>(__VA_ARGS__) : FN<LT, 4, 16>(__VA_ARGS__);  \
+        if (E <= 128)                                               \
+            return few ? FN<LT, 2, 64>(__VA_ARGS__) : FN<LT, 8, 16>(__VA_ARGS__);  \
+        if (E <= 256)                                               \
+            return few ? FN<LT, 4, 64>(__VA_ARGS__) : FN<LT, 16, 16>(__VA_ARGS__); \
+        if (E <= 512)                                               \
+            return few ? FN<LT, 8, 64>(__VA_ARGS__) : FN<LT, 16, 32>(__VA_ARGS__); \
+        return FN<LT, 16, 64>(__VA_ARGS__);                         \
     } while (0)
 
 template <typename LT>
