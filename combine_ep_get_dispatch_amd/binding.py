@@ -115,6 +115,9 @@ def _check(status: int, what: str):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(t: torch.Tensor):
     """torch's current stream on t's device, as a hipStream_t."""
     if _raw_stream is not None:
@@ -126,11 +129,19 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _addr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
 def _is_gpu(t: torch.Tensor) -> bool:
     return t.device.type == "cuda"
 
 
 def _need(t: torch.Tensor, dtype, name: str, shape=None, device=None):
+    # the usual case in one expression; what it does not pass is looked at below
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()
+            and (shape is None or t.shape == shape) and (device is None or t.device == device)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if not _is_gpu(t):
@@ -573,13 +584,15 @@ def combine(y: torch.Tensor, dst_row: torch.Tensor, topk_weights: torch.Tensor,
 def _launch(name: str, t: torch.Tensor, *args):
     """Call ``name`` with ``args`` and torch's current stream on t's device,
     with that device current."""
-    fn = getattr(lib(), name)
-    if t.device.index == torch.cuda.current_device():
-        status = fn(*args, _stream(t))
-    else:
+    fn = getattr(_lib or lib(), name)
+    index = t.get_device()
+    if _get_device is None or index != _get_device():
         with torch.cuda.device(t.device):
             status = fn(*args, _stream(t))
-    _check(status, name)
+    else:
+        status = fn(*args, _raw_stream(index) if _raw_stream is not None else _stream(t))
+    if status != EP_OK:
+        raise EpError(status, name)
 
 
 def combine_backward(grad_out: torch.Tensor, y: torch.Tensor | None, dst_row: torch.Tensor,
@@ -622,8 +635,8 @@ def combine_backward(grad_out: torch.Tensor, y: torch.Tensor | None, dst_row: to
         _need(grad_y, torch.bfloat16, "grad_y", (R, H), device=dev)
     elif grad_y is not None:
         raise ValueError("grad_y needs topk_weights")
-    _launch("ep_combine_backward", grad_out, _ptr(grad_out), _ptr(y), R, _ptr(dst_row),
-            _ptr(topk_weights), T, K, H, _ptr(grad_y), _ptr(grad_weights))
+    _launch("ep_combine_backward", grad_out, _addr(grad_out), _addr(y), R, _addr(dst_row),
+            _addr(topk_weights), T, K, H, _addr(grad_y), _addr(grad_weights))
     return grad_y, grad_weights
 
 
@@ -641,8 +654,8 @@ def dispatch_backward(grad_recv_x: torch.Tensor, dst_row: torch.Tensor,
     if out is None:
         out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
     _need(out, torch.bfloat16, "out", (T, H), device=dev)
-    _launch("ep_dispatch_backward", grad_recv_x, _ptr(grad_recv_x), R, _ptr(dst_row), T, K, H,
-            _ptr(out))
+    _launch("ep_dispatch_backward", grad_recv_x, _addr(grad_recv_x), R, _addr(dst_row), T, K, H,
+            _addr(out))
     return out
 
 
@@ -683,9 +696,9 @@ def route(logits: torch.Tensor, num_topk: int, expert_bias: torch.Tensor | None 
     idx, w = out
     _need(idx, torch.int64, "topk_idx", (T, K), device=dev)
     _need(w, torch.float32, "topk_weights", (T, K), device=dev)
-    _launch("ep_route", logits, _ptr(logits), dt, _ptr(expert_bias), T, E, K, _score(score),
-            int(num_groups), int(topk_groups), int(bool(normalize)), float(scale), _ptr(idx),
-            _ptr(w))
+    _launch("ep_route", logits, _addr(logits), dt, _addr(expert_bias), T, E, K, _score(score),
+            int(num_groups), int(topk_groups), int(bool(normalize)), float(scale), _addr(idx),
+            _addr(w))
     return idx, w
 
 
@@ -705,8 +718,8 @@ def route_backward(logits: torch.Tensor, topk_idx: torch.Tensor, grad_weights: t
     if out is None:
         out = torch.empty_like(logits)
     _need(out, logits.dtype, "out", (T, E), device=dev)
-    _launch("ep_route_backward", logits, _ptr(logits), dt, _ptr(topk_idx), _ptr(grad_weights), T,
-            E, K, _score(score), int(bool(normalize)), float(scale), _ptr(out))
+    _launch("ep_route_backward", logits, _addr(logits), dt, _addr(topk_idx), _addr(grad_weights), T,
+            E, K, _score(score), int(bool(normalize)), float(scale), _addr(out))
     return out
 
 
@@ -759,10 +772,10 @@ def expert_linear_w4(x: torch.Tensor, weight: torch.Tensor, scales: torch.Tensor
     if out is None:
         out = torch.empty((R, N), dtype=torch.bfloat16, device=dev)
     _need(out, torch.bfloat16, "out", (R, N), device=dev)
-    _launch("ep_expert_linear_w4", x, _ptr(x), _ptr(x_scales),
-            EP_DTYPE_FP8_E4M3 if fp8 else EP_DTYPE_BF16, R, _ptr(expert_offsets),
-            _ptr(num_tokens_per_expert), int(capacity), E, I, N, I // NG, _ptr(weight),
-            _ptr(scales), _ptr(zeros), int(bool(swiglu)), _ptr(out))
+    _launch("ep_expert_linear_w4", x, _addr(x), _addr(x_scales),
+            EP_DTYPE_FP8_E4M3 if fp8 else EP_DTYPE_BF16, R, _addr(expert_offsets),
+            _addr(num_tokens_per_expert), int(capacity), E, I, N, I // NG, _addr(weight),
+            _addr(scales), _addr(zeros), int(bool(swiglu)), _addr(out))
     return out
 
 

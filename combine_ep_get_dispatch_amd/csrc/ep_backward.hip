@@ -6,24 +6,30 @@
 // writes no row.  (The gradient of dispatch is combine with unit weights; it
 // runs combine's kernels, see ep_combine.hip.)
 //
-// The kernel is HBM-bound: every y row named is read once and every grad_y row
+// What bounds it.  The kernel is HBM-bound: every y row named is read once and every grad_y row
 // written once, about 3 flops per 4 bytes, so the design is combine's: 8
 // channels per lane, the row loads of a group of slots all in flight before
 // the first product, non-temporal loads and stores for rows touched once.  A
 // row of g is read once and used for all the token's slots.
+//
+// Large batches of many slots run in tiles that read all their rows and then
+// write all their gradient rows, so that the HBM turns between the directions
+// less often.  On MI355X, tiled against one workgroup per token:
+//   4096 tokens x 7168, top-8   170 / 193 us (5.9 TB/s of 6.1 for plain reads)
+//   2048 x 7168, top-8           88 /  99      4096 x 7168, top-4   89 /  99
+//   8192 x 4096, top-4          101 / 107      4096 x 5120, top-6   93 / 100
+//   4096 x 4096, top-10         127 / 139
+// but 103.4 / 102.9 at 8192 x 2048 top-8, 45 / 43 at 8192 x 1024 top-6 and
+// 262 / 228 at 32768 x 4096 top-2: few channels leave a tile's waves uneven
+// rounds, few slots a wave few loads in flight.  A batch that gives the CUs
+// one tile each loses too (4096 x 7168, top-4 in 256 tiles: 113 / 99).
+// Non-temporal accesses: 193 us, against 204 with write-through and 209 with
+// ordinary stores, and 208 with ordinary loads (4096 x 7168, top-8, untiled).
 #include "ep_internal.h"
 #include "ep_device.h"
 
 namespace ep {
 namespace {
-
-// Sum over the wave, the same for every lane.  The order is fixed, so equal
-// inputs give equal sums.
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m);
-    return v;
-}
 
 __device__ __forceinline__ void unpack8(float (&f)[8], const uint4& v) {
     f[0] = bf16_lo(v.x);
@@ -36,53 +42,75 @@ __device__ __forceinline__ void unpack8(float (&f)[8], const uint4& v) {
     f[7] = bf16_hi(v.w);
 }
 
-// Slots [k0, k0 + KN) of one token over one 512-channel chunk: load the rows,
-// write w * g into the gradient rows and add the chunk's part of <g, y> to dot.
-// Either half may be absent (y or gy null).
+// A token's slots: lane k holds slot k's row (-1: none) and weight.
+struct Slots {
+    int row;
+    float w;
+};
+__device__ __forceinline__ Slots load_slots(const int32_t* __restrict__ dst_row,
+                                            const float* __restrict__ w, int64_t nrows, int64_t t,
+                                            int K) {
+    const int lane = threadIdx.x & 63;
+    Slots s = {-1, 0.0f};
+    if (lane < K) {
+        s.row = dst_row[t * K + lane];
+        if (w) s.w = w[t * K + lane];
+        if (s.row >= nrows) s.row = -1;         // outside the rows: skipped like a masked slot
+    }
+    return s;
+}
+
+// Slots [k0, k0 + KN) over one 512-channel chunk: this lane's part of <g, y>.
 template <int KN>
-__device__ __forceinline__ void backward_slots(float (&dot)[KN], const float (&g)[8],
-                                               const uint16_t* __restrict__ y,
-                                               uint16_t* __restrict__ gy, int H, int h0, bool act,
-                                               int drow, float wl, int k0) {
+__device__ __forceinline__ void dot_rows(float (&dot)[KN], const float (&g)[8],
+                                         const uint16_t* __restrict__ y, const Slots& s, int k0,
+                                         int H, int h0, bool act) {
     uint4 v[KN];
-    if (y) {
 #pragma unroll
-        for (int i = 0; i < KN; ++i) {
-            const int d = __builtin_amdgcn_readlane(drow, k0 + i);
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (d >= 0 && act) v[i] = load_nt(y + (int64_t)d * H + h0);
-        }
+    for (int i = 0; i < KN; ++i) {
+        const int r = __builtin_amdgcn_readlane(s.row, k0 + i);
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (r >= 0 && act) v[i] = load_nt(y + (int64_t)r * H + h0);
     }
-    if (gy) {
 #pragma unroll
-        for (int i = 0; i < KN; ++i) {
-            const int d = __builtin_amdgcn_readlane(drow, k0 + i);
-            const float w = __builtin_bit_cast(
-                float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wl), k0 + i));
-            if (d >= 0 && act) {
-                uint4 o;
-                o.x = pack_bf16x2(w * g[0], w * g[1]);
-                o.y = pack_bf16x2(w * g[2], w * g[3]);
-                o.z = pack_bf16x2(w * g[4], w * g[5]);
-                o.w = pack_bf16x2(w * g[6], w * g[7]);
-                store_nt(gy + (int64_t)d * H + h0, o);
-            }
-        }
+    for (int i = 0; i < KN; ++i) {
+        float f[8];
+        unpack8(f, v[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dot[i] = __builtin_fmaf(g[j], f[j], dot[i]);
     }
-    if (y) {
+}
+
+// ... and w * g into their gradient rows.
+template <int KN>
+__device__ __forceinline__ void write_rows(const float (&g)[8], uint16_t* __restrict__ gy,
+                                           const Slots& s, int k0, int H, int h0, bool act) {
 #pragma unroll
-        for (int i = 0; i < KN; ++i) {
-            float f[8];
-            unpack8(f, v[i]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) dot[i] = __builtin_fmaf(g[j], f[j], dot[i]);
+    for (int i = 0; i < KN; ++i) {
+        const int r = __builtin_amdgcn_readlane(s.row, k0 + i);
+        const float w = __builtin_bit_cast(
+            float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, s.w), k0 + i));
+        if (r >= 0 && act) {
+            uint4 o;
+            o.x = pack_bf16x2(w * g[0], w * g[1]);
+            o.y = pack_bf16x2(w * g[2], w * g[3]);
+            o.z = pack_bf16x2(w * g[4], w * g[5]);
+            o.w = pack_bf16x2(w * g[6], w * g[7]);
+            store_nt(gy + (int64_t)r * H + h0, o);
         }
     }
 }
 
-// Workgroup of nw waves per token; wave i takes chunks i, i + nw, ...  Lane k
-// holds slot k's row and weight.  The waves' partial dot products of a group
-// of KN slots meet in LDS and are added in wave order.
+__device__ __forceinline__ void load_grad(float (&g)[8], const uint16_t* __restrict__ gout,
+                                          int64_t t, int H, int h0, bool act) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (act) v = *reinterpret_cast<const uint4*>(gout + t * H + h0);
+    unpack8(g, v);
+}
+
+// Workgroup of nw waves per token; wave i takes chunks i, i + nw, ...  The
+// waves' partial dot products of a group of KN slots meet in LDS and are added
+// in wave order.
 template <int KN>
 __global__ __launch_bounds__(kBackwardMaxThreads) void combine_backward_kernel(
     const uint16_t* __restrict__ gout, const uint16_t* __restrict__ y, int64_t nrows,
@@ -92,15 +120,9 @@ __global__ __launch_bounds__(kBackwardMaxThreads) void combine_backward_kernel(
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int nw = blockDim.x >> 6;
-    const int t = blockIdx.x;
-    int drow = -1;
-    float wl = 0.0f;
-    if (lane < K) {
-        drow = dst_row[(int64_t)t * K + lane];
-        if (w) wl = w[(int64_t)t * K + lane];
-        if (drow >= nrows) drow = -1;   // outside the rows: skipped like a masked slot
-    }
+    const int64_t t = blockIdx.x;
     const int nchunk = (H + kCombineChunk - 1) / kCombineChunk;
+    const Slots s = load_slots(dst_row, w, nrows, t, K);
     for (int k0 = 0; k0 < K; k0 += KN) {
         float dot[KN];
 #pragma unroll
@@ -108,27 +130,104 @@ __global__ __launch_bounds__(kBackwardMaxThreads) void combine_backward_kernel(
         for (int c = wave; c < nchunk; c += nw) {
             const int h0 = c * kCombineChunk + lane * 8;
             const bool act = h0 < H;
-            uint4 gv = make_uint4(0, 0, 0, 0);
-            if (act) gv = *reinterpret_cast<const uint4*>(gout + (int64_t)t * H + h0);
             float g[8];
-            unpack8(g, gv);
-            backward_slots<KN>(dot, g, y, gy, H, h0, act, drow, wl, k0);
+            load_grad(g, gout, t, H, h0, act);
+            if (y) dot_rows<KN>(dot, g, y, s, k0, H, h0, act);
+            if (gy) write_rows<KN>(g, gy, s, k0, H, h0, act);
         }
         if (gw) {
 #pragma unroll
             for (int i = 0; i < KN; ++i) {
-                const float s = wave_sum(dot[i]);
-                if (lane == i) s_part[wave][i] = s;
+                const float v = seg_sum<64>(dot[i]);
+                if (lane == i) s_part[wave][i] = v;
             }
             __syncthreads();
             if (threadIdx.x < KN && k0 + (int)threadIdx.x < K) {
-                float s = 0.0f;
-                for (int i = 0; i < nw; ++i) s += s_part[i][threadIdx.x];
-                gw[(int64_t)t * K + k0 + threadIdx.x] = s;
+                float v = 0.0f;
+                for (int i = 0; i < nw; ++i) v += s_part[i][threadIdx.x];
+                gw[t * K + k0 + threadIdx.x] = v;
             }
             __syncthreads();
         }
     }
+}
+
+// Large batches: a workgroup owns a tile of consecutive tokens and first reads
+// all their rows (dot products of every (token, chunk) to LDS), then writes all
+// their gradient rows.  g is read again for the second phase, from a cache.
+template <int KN>
+__global__ __launch_bounds__(kBackwardTileThreads) void combine_backward_tile_kernel(
+    const uint16_t* __restrict__ gout, const uint16_t* __restrict__ y, int64_t nrows,
+    const int32_t* __restrict__ dst_row, const float* __restrict__ w, int T, int K, int H,
+    int tile, uint16_t* __restrict__ gy, float* __restrict__ gw) {
+    extern __shared__ EP_LDS_ALIGN float s_dot[];       // [tile * nchunk][K]
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int kWaves = kBackwardTileThreads / 64;
+    const int64_t t0 = (int64_t)blockIdx.x * tile;
+    const int nt = (int)min((int64_t)tile, T - t0);
+    const int nchunk = (H + kCombineChunk - 1) / kCombineChunk;
+    const int ntask = nt * nchunk;
+    for (int task = wave; task < ntask; task += kWaves) {
+        const int tt = task / nchunk;
+        const int h0 = (task - tt * nchunk) * kCombineChunk + lane * 8;
+        const bool act = h0 < H;
+        const Slots s = load_slots(dst_row, nullptr, nrows, t0 + tt, K);
+        float g[8];
+        load_grad(g, gout, t0 + tt, H, h0, act);
+        for (int k0 = 0; k0 < K; k0 += KN) {
+            float dot[KN];
+#pragma unroll
+            for (int i = 0; i < KN; ++i) dot[i] = 0.0f;
+            dot_rows<KN>(dot, g, y, s, k0, H, h0, act);
+#pragma unroll
+            for (int i = 0; i < KN; ++i) {
+                const float v = seg_sum<64>(dot[i]);
+                if (lane == i && k0 + i < K) s_dot[task * K + k0 + i] = v;
+            }
+        }
+    }
+    __syncthreads();
+    for (int task = wave; task < ntask; task += kWaves) {
+        const int tt = task / nchunk;
+        const int h0 = (task - tt * nchunk) * kCombineChunk + lane * 8;
+        const bool act = h0 < H;
+        const Slots s = load_slots(dst_row, w, nrows, t0 + tt, K);
+        float g[8];
+        load_grad(g, gout, t0 + tt, H, h0, act);
+        for (int k0 = 0; k0 < K; k0 += KN) write_rows<KN>(g, gy, s, k0, H, h0, act);
+    }
+    for (int i = threadIdx.x; i < nt * K; i += kBackwardTileThreads) {
+        const int tt = i / K, k = i - tt * K;
+        float v = 0.0f;
+        for (int c = 0; c < nchunk; ++c) v += s_dot[(tt * nchunk + c) * K + k];
+        gw[t0 * K + i] = v;
+    }
+}
+
+template <int KN>
+hipError_t launch_backward_k(const uint16_t* gout, const uint16_t* y, int64_t nrows,
+                             const int32_t* dst_row, const float* w, int T, int K, int H,
+                             uint16_t* gy, float* gw, hipStream_t s) {
+    const int nchunk = (H + kCombineChunk - 1) / kCombineChunk;
+    // Tiles of as many slots as keep 8 per wave, while the batch still gives
+    // every CU of a 256-CU part two tiles, where both gradients are asked for
+    // and a tile's sums fit its LDS.
+    int tile = kBackwardTileSlots / K;
+    if (tile > T / kBackwardMinTiles) tile = T / kBackwardMinTiles;
+    const size_t lds = (size_t)tile * nchunk * K * sizeof(float);
+    if (y && gy && gw && K >= kBackwardTileMinK && H >= kBackwardTileMinH &&
+        2 * tile * K >= kBackwardTileSlots && lds <= 64 * 1024) {
+        hipLaunchKernelGGL(combine_backward_tile_kernel<KN>,
+                           dim3((unsigned)(((int64_t)T + tile - 1) / tile)),
+                           dim3(kBackwardTileThreads), lds, s, gout, y, nrows, dst_row, w, T, K, H,
+                           tile, gy, gw);
+    } else {
+        const int nw = nchunk < kBackwardMaxThreads / 64 ? nchunk : kBackwardMaxThreads / 64;
+        hipLaunchKernelGGL(combine_backward_kernel<KN>, dim3((unsigned)T), dim3(nw * 64), 0, s,
+                           gout, y, nrows, dst_row, w, K, H, gy, gw);
+    }
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -137,19 +236,15 @@ hipError_t launch_combine_backward(const uint16_t* gout, const uint16_t* y, int6
                                    const int32_t* dst_row, const float* w, int T, int K, int H,
                                    uint16_t* gy, float* gw, hipStream_t s) {
     if (T == 0) return hipSuccess;
-    const int nchunk = (H + kCombineChunk - 1) / kCombineChunk;
-    const int nw = nchunk < kBackwardMaxThreads / 64 ? nchunk : kBackwardMaxThreads / 64;
-    const dim3 grid((unsigned)T), block(nw * 64);
-#define EP_B_ARGS grid, block, 0, s, gout, y, nrows, dst_row, w, K, H, gy, gw
+#define EP_B_ARGS gout, y, nrows, dst_row, w, T, K, H, gy, gw, s
     switch (K) {
-        case 1: hipLaunchKernelGGL(combine_backward_kernel<1>, EP_B_ARGS); break;
-        case 2: hipLaunchKernelGGL(combine_backward_kernel<2>, EP_B_ARGS); break;
-        case 4: hipLaunchKernelGGL(combine_backward_kernel<4>, EP_B_ARGS); break;
-        case 6: hipLaunchKernelGGL(combine_backward_kernel<6>, EP_B_ARGS); break;
-        default: hipLaunchKernelGGL(combine_backward_kernel<8>, EP_B_ARGS); break;
+        case 1: return launch_backward_k<1>(EP_B_ARGS);
+        case 2: return launch_backward_k<2>(EP_B_ARGS);
+        case 4: return launch_backward_k<4>(EP_B_ARGS);
+        case 6: return launch_backward_k<6>(EP_B_ARGS);
+        default: return launch_backward_k<8>(EP_B_ARGS);
     }
 #undef EP_B_ARGS
-    return hipGetLastError();
 }
 
 }  // namespace ep

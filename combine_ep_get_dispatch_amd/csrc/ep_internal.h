@@ -236,6 +236,13 @@ hipError_t launch_combine(const uint16_t* y, int64_t nrows, const int32_t* dst_r
 
 // --------------------------------------------------------------- backward ---
 constexpr int kBackwardMaxThreads = 1024;
+// Tiled form (reads, then writes): 8 waves and up to 64 slots a tile, while the
+// batch gives every CU of a 256-CU part two tiles.
+constexpr int kBackwardTileThreads = 512;
+constexpr int kBackwardTileSlots = 64;
+constexpr int kBackwardMinTiles = 512;
+constexpr int kBackwardTileMinK = 4;
+constexpr int kBackwardTileMinH = 4096;
 
 // Gradient of combine.  gy null: no row gradients (w is then unused); gw null:
 // no weight gradients (y is then unused).

@@ -30,61 +30,6 @@ namespace {
 
 constexpr float kFltMax = 3.4028234663852886e38f;
 
-// Maximum and sum over aligned segments of L lanes, the same for every lane of
-// a segment; all lanes active.  Inside a row of 16 lanes a step is one DPP move
-// (neighbours, pairs, half rows and rows mirrored), across rows one swap of
-// rows or halves, after which both partners stand in one lane.
-template <int STEP>
-__device__ __forceinline__ void partners(uint32_t& a, uint32_t& b) {
-    constexpr int kDpp[4] = {0xB1, 0x4E, 0x141, 0x140};
-    if constexpr (STEP < 4) {
-        b = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a, kDpp[STEP], 0xf, 0xf, false);
-    } else if constexpr (STEP == 4) {
-        const auto r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
-        a = r[0];
-        b = r[1];
-    } else {
-        const auto r = __builtin_amdgcn_permlane32_swap(a, a, false, false);
-        a = r[0];
-        b = r[1];
-    }
-}
-template <int STEP>
-__device__ __forceinline__ void partners(float& a, float& b) {
-    uint32_t x = __float_as_uint(a), y;
-    partners<STEP>(x, y);
-    a = __uint_as_float(x);
-    b = __uint_as_float(y);
-}
-template <int STEP>
-__device__ __forceinline__ void partners(double& a, double& b) {
-    const uint64_t u = __builtin_bit_cast(uint64_t, a);
-    uint32_t x0 = (uint32_t)u, x1 = (uint32_t)(u >> 32), y0, y1;
-    partners<STEP>(x0, y0);
-    partners<STEP>(x1, y1);
-    a = __builtin_bit_cast(double, (uint64_t)x1 << 32 | x0);
-    b = __builtin_bit_cast(double, (uint64_t)y1 << 32 | y0);
-}
-__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
-__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
-template <int L, int STEP = 0, typename V>
-__device__ __forceinline__ V seg_max(V v) {
-    if constexpr ((1 << STEP) < L) {
-        V o;
-        partners<STEP>(v, o);
-        return seg_max<L, STEP + 1>(larger(v, o));
-    }
-    return v;
-}
-template <int L, int STEP = 0, typename V>
-__device__ __forceinline__ V seg_sum(V v) {
-    if constexpr ((1 << STEP) < L) {
-        V o;
-        partners<STEP>(v, o);
-        return seg_sum<L, STEP + 1>(v + o);
-    }
-    return v;
-}
 // The two largest values of a segment of `lanes` lanes (a power of two, at
 // most L), from the two largest of each lane.
 template <int L, int STEP = 0>

@@ -253,6 +253,35 @@ def test_combine_and_dispatch_backward(T, H, K, extra, masked):
     within(gx, rgx, ref.UBF * rgx.abs() + K * 2 * ref.U32 * size + ref.TINY, "grad_x")
 
 
+@pytest.mark.parametrize("T,H,K,masked", [(2048, 4104, 8, 0.1), (4099, 4096, 4, 0.0),
+                                          (2900, 4608, 6, 0.02), (1100, 5000, 17, 0.05)])
+def test_combine_backward_of_large_batches(T, H, K, masked):
+    """Batches that run in tiles (ragged tail tiles and chunks among them),
+    against the two halves alone, which run one workgroup per token: the rows
+    bit for bit, the sums within the roundings of both orders."""
+    announce("backward tiles T=%d H=%d K=%d" % (T, H, K))
+    dst, R = slots(T, K, 3, masked, H + K)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    go = torch.randn((T, H), device="cuda", generator=g).bfloat16()
+    y = torch.randn((R, H), device="cuda", generator=g).bfloat16()
+    w = torch.rand((T, K), device="cuda", generator=g)
+    d_dst = dst.cuda()
+    both = ep.combine_backward(go, y, d_dst, w, out=(torch.full_like(y, 2.5), None))
+    gy, _ = ep.combine_backward(go, None, d_dst, w, out=(torch.full_like(y, 2.5), None))
+    _, gw = ep.combine_backward(go, y, d_dst, None)
+    torch.cuda.synchronize()
+    assert torch.equal(both[0], gy)
+    ok = (d_dst >= 0) & (d_dst < R)
+    for k in range(K):
+        rows = y[d_dst[:, k].clamp(0, R - 1).long()].double() * go.double()
+        want = torch.where(ok[:, k], rows.sum(1), 0.0)
+        tol = 64 * ref.U32 * rows.abs().sum(1) + ref.TINY
+        for got in (both[1][:, k], gw[:, k]):
+            assert bool(((got.double() - want).abs() <= tol).all()), k
+    again = ep.combine_backward(go, y, d_dst, w, out=(torch.full_like(y, 2.5), None))
+    assert torch.equal(again[0], both[0]) and torch.equal(again[1], both[1])
+
+
 def test_backward_without_rows_or_tokens():
     dst = torch.full((3, 2), -1, dtype=torch.int32, device="cuda")
     go = torch.ones((3, 16), dtype=torch.bfloat16, device="cuda")
