@@ -160,6 +160,7 @@ __device__ __forceinline__ void partners(double& a, double& b) {
     a = __builtin_bit_cast(double, (uint64_t)x1 << 32 | x0);
     b = __builtin_bit_cast(double, (uint64_t)y1 << 32 | y0);
 }
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
 __device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
 __device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
 template <int L, int STEP = 0, typename V>

@@ -17,9 +17,13 @@
 //
 // Layout.  A token belongs to a segment of L lanes of a wave and a lane holds
 // VPL consecutive experts, so that lower lanes hold lower ids: the lowest lane
-// among equals, and the lowest value in it, is the lowest id, and the maximum
-// needs no index beside it.  Maxima over a segment of up to 16 lanes stay
-// inside a DPP row.
+// among equals, and the first of it, is the lowest id, and the maximum needs no
+// index beside it.
+//
+// What bounds it: not the logits (4.5 MB at 4096 tokens of 256 experts, 1 us)
+// but the instructions per token -- about 1000 with a bias and groups, most of
+// them the fp64 scores and the K maxima -- and, in a decode batch, their chain:
+// 7.0 us per launch at 128 tokens, 2 us of them the launch itself.
 #include "ep_internal.h"
 #include "ep_device.h"
 
@@ -137,18 +141,87 @@ __device__ __forceinline__ void store_row(const float (&o)[VPL], uint16_t* row, 
     }
 }
 
+// v of lane i (within the wave; the same i for every lane where L is 64).
+template <int L>
+__device__ __forceinline__ double from_lane(double v, int i) {
+    if constexpr (L == 64) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);
+        const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, i);
+        const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), i);
+        return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+    }
+    return __shfl(v, i);
+}
+
+// Unsigned keys in the order of the values, above 0 (which is the key of an
+// expert that is not available).  Adding 0 makes -0 and +0 the same key.
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t u = __float_as_uint(v + 0.0f);
+    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ uint64_t order_key(double v) {
+    const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
+    return u ^ ((u >> 63) ? ~0ull : 1ull << 63);
+}
+
 __device__ __forceinline__ double sigmoid64(double l) { return 1.0 / (1.0 + exp(-l)); }
 
+// A lane's experts in descending order of their keys, equal ones by id.
+template <int VPL, bool FULL>
+struct Ranked {
+    uint32_t hi[VPL], lo[FULL ? VPL : 1];   // key; lo: its lower half, of 64 bits
+    int at[VPL];                            // expert, from the lane's first
+
+    __device__ __forceinline__ bool above(int i, int j) const {
+        if constexpr (FULL)
+            return ((uint64_t)hi[i] << 32 | lo[i]) > ((uint64_t)hi[j] << 32 | lo[j]);
+        return hi[i] > hi[j];
+    }
+    // Neighbours change places only where the later one is larger, so equal
+    // keys keep their order.
+    __device__ __forceinline__ void sort() {
+#pragma unroll
+        for (int n = 0; n < VPL - 1; ++n)
+#pragma unroll
+            for (int j = VPL - 1; j > n; --j) {
+                const bool up = above(j, j - 1);
+                swap_if(up, hi[j], hi[j - 1]);
+                if constexpr (FULL) swap_if(up, lo[j], lo[j - 1]);
+                swap_if(up, at[j], at[j - 1]);
+            }
+    }
+    template <typename V>
+    static __device__ __forceinline__ void swap_if(bool c, V& a, V& b) {
+        const V x = c ? b : a, y = c ? a : b;
+        a = x;
+        b = y;
+    }
+    // The first one leaves; a key of 0 (not available) follows the last.
+    __device__ __forceinline__ void pop() {
+#pragma unroll
+        for (int j = 0; j < VPL - 1; ++j) {
+            hi[j] = hi[j + 1];
+            if constexpr (FULL) lo[j] = lo[j + 1];
+            at[j] = at[j + 1];
+        }
+        hi[VPL - 1] = 0;
+        if constexpr (FULL) lo[VPL - 1] = 0;
+    }
+};
+
 // FULL: choices in fp64 (a bias or groups); otherwise the logits decide.
-// Dynamic LDS, per token of the workgroup: K slots' expert (int) and logit
-// (float), then with groups that do not lie on whole lanes E choices (double),
+// Dynamic LDS, per token of the workgroup: its E logits and its K slots'
+// experts, then with groups that do not lie on whole lanes E choices (double),
 // NG group scores (double) and NG flags (int).
+//
+// A lane ranks its own experts once; a slot then takes one maximum over the
+// lanes' first ones.  64-bit keys are compared by their upper halves, and by
+// the lower ones only where two lanes have the same upper half.
 template <typename LT, int VPL, int L, bool FULL>
 __global__ __launch_bounds__(kRouteThreads) void route_kernel(
     const LT* __restrict__ logits, const float* __restrict__ bias, int T, int E, int K,
     bool softmax, int NG, int TG, bool normalize, float scale, int64_t* __restrict__ topk_idx,
     float* __restrict__ topk_weights, bool vec) {
-    using Choice = typename std::conditional<FULL, double, float>::type;
     constexpr int kTokens = kRouteThreads / L;
     extern __shared__ EP_LDS_ALIGN unsigned char s_raw[];
     const int lane = threadIdx.x & 63;
@@ -156,8 +229,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(
     const int tok = threadIdx.x / L;                 // token of the workgroup
     const int64_t t = (int64_t)blockIdx.x * kTokens + tok;
     const bool live = t < T;
-    int* s_idx = reinterpret_cast<int*>(s_raw) + tok * K;
-    float* s_logit = reinterpret_cast<float*>(s_raw) + kTokens * K + tok * K;
+    float* s_logit = reinterpret_cast<float*>(s_raw) + tok * E;
+    int* s_idx = reinterpret_cast<int*>(s_raw) + kTokens * E + tok * K;
 
     const int e0 = sl * VPL;
     float l[VPL];
@@ -177,6 +250,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(
     for (int j = 0; j < VPL; ++j) {
         l[j] = clean_logit(l[j]);
         lmax = fmaxf(lmax, l[j]);
+        if (e0 + j < E) s_logit[e0 + j] = l[j];
     }
     for (int k = sl; k < K; k += L) s_idx[k] = -1;
 
@@ -198,9 +272,9 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(
         }
     }
 
-    // what orders the experts; -inf: not available
-    Choice key[VPL];
+    Ranked<VPL, FULL> r;
     if constexpr (FULL) {
+        double key[VPL];        // what orders the experts; -inf: not available
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
             const double s = softmax ? exp((double)l[j] - (double)m) / total
@@ -223,7 +297,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(
                 const int g = e0 / gsz;
                 int better = 0;
                 for (int i = 0; i < NG; ++i) {
-                    const double o = __shfl(mine, (lane - sl) + i * lanes);
+                    const double o = from_lane<L>(mine, (lane - sl) + i * lanes);
                     better += (o > mine || (o == mine && i < g)) ? 1 : 0;
                 }
 #pragma unroll
@@ -233,7 +307,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(
                     key[j] = open ? by : -INFINITY;
                 }
             } else {
-                const size_t head = ((size_t)kTokens * K * 8 + 15) & ~(size_t)15;
+                const size_t head = ((size_t)kTokens * (E + K) * 4 + 15) & ~(size_t)15;
                 double* s_ch = reinterpret_cast<double*>(s_raw + head) + tok * (E + 2 * NG);
                 double* s_gs = s_ch + E;
                 int* s_flag = reinterpret_cast<int*>(s_gs + NG);
@@ -276,32 +350,35 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(
                 }
             }
         }
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            const uint64_t u = key[j] > -INFINITY ? order_key(key[j]) : 0;
+            r.hi[j] = (uint32_t)(u >> 32);
+            r.lo[j] = (uint32_t)u;
+            r.at[j] = j;
+        }
     } else {
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) key[j] = l[j];
+        for (int j = 0; j < VPL; ++j) {
+            r.hi[j] = l[j] > -INFINITY ? order_key(l[j]) : 0;
+            r.at[j] = j;
+        }
     }
+    r.sort();
 
     const uint64_t segmask = (L == 64 ? ~0ull : ((1ull << (L & 63)) - 1)) << (lane - sl);
     for (int k = 0; k < K; ++k) {
-        Choice best = key[0];
-#pragma unroll
-        for (int j = 1; j < VPL; ++j) best = larger(best, key[j]);
-        const Choice top = seg_max<L>(best);
-        const uint64_t eq = __ballot(best == top && top > -INFINITY) & segmask;
+        const uint32_t top = seg_max<L>(r.hi[0]);
+        uint64_t eq = __ballot(r.hi[0] == top && top != 0) & segmask;
+        if constexpr (FULL) {
+            if (__ballot((eq & (eq - 1)) != 0)) {
+                const uint32_t low = seg_max<L>(r.hi[0] == top ? r.lo[0] : 0u);
+                eq = __ballot(r.hi[0] == top && r.lo[0] == low && top != 0) & segmask;
+            }
+        }
         if (eq != 0 && __builtin_ctzll(eq) == (unsigned)lane) {
-            int at = 0;
-            float lv = l[0];
-#pragma unroll
-            for (int j = VPL - 1; j >= 0; --j)
-                if (key[j] == top) {
-                    at = j;
-                    lv = l[j];
-                }
-#pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                if (j == at) key[j] = -INFINITY;
-            s_idx[k] = e0 + at;
-            s_logit[k] = lv;
+            s_idx[k] = e0 + r.at[0];
+            r.pop();
         }
     }
     wave_sync();
@@ -311,7 +388,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(
         // over the selected experts alone, from their own maximum
         m = -kFltMax;
         for (int k = sl; k < K; k += L)
-            if (s_idx[k] >= 0) m = fmaxf(m, s_logit[k]);
+            if (s_idx[k] >= 0) m = fmaxf(m, s_logit[s_idx[k]]);
         m = seg_max<L>(m);
     }
     double sum = softmax ? total : 1.0;
@@ -319,7 +396,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(
         sum = 0.0;
         for (int k = sl; k < K; k += L)
             if (s_idx[k] >= 0) {
-                const double v = (double)s_logit[k];
+                const double v = (double)s_logit[s_idx[k]];
                 sum += softmax ? exp(v - (double)m) : sigmoid64(v);
             }
         sum = seg_sum<L>(sum);
@@ -328,7 +405,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(
         const int e = s_idx[k];
         double w = 0.0;
         if (e >= 0 && sum > 0.0) {
-            const double v = (double)s_logit[k];
+            const double v = (double)s_logit[e];
             w = (softmax ? exp(v - (double)m) : sigmoid64(v)) / sum * (double)scale;
         }
         if (live) {
@@ -466,7 +543,7 @@ hipError_t launch_route_l(const LT* logits, const float* bias, int T, int E, int
     constexpr int kTokens = kRouteThreads / L;
     const dim3 grid((unsigned)((T + kTokens - 1) / kTokens)), block(kRouteThreads);
     const bool vec = rows_vectorised(logits, sizeof(LT), E);
-    size_t lds = ((size_t)kTokens * K * 8 + 15) & ~(size_t)15;
+    size_t lds = ((size_t)kTokens * (E + K) * 4 + 15) & ~(size_t)15;
     if (NG > 1) lds += (size_t)kTokens * (E + 2 * NG) * 8;
     if (bias || NG > 1)
         hipLaunchKernelGGL((route_kernel<LT, VPL, L, true>), grid, block, lds, s, logits, bias, T,
@@ -493,21 +570,23 @@ hipError_t launch_route_backward_l(const LT* logits, const int64_t* topk_idx, co
 }
 
 // Experts per lane and lanes per token: a whole wave for a token while the
-// batch is small (short chains), else as few lanes as hold the experts at 16 a
-// lane (less work per token).
-#define EP_ROUTE_DISPATCH(FN, LT, ...)                              \
-    do {                                                            \
-        const bool few = T <= kRouteWideTokens;                     \
-        if (E <= 8) return FN<LT, 1, 8>(__VA_ARGS__);               \
-        if (E <= 64)                                                \
+// batch is small (short chains), fewer lanes beyond (less work per token).  On
+// MI355X, wave / fewer: router of 256 experts with bias and groups, 128 tokens
+// 7.0 / 8.6 us, 4096 tokens 11.3 / 11.5, 32768 tokens 54 / 50; of 128 experts by
+// logits, 16384 tokens 13.7 / 7.9; of 64, 4096 tokens 5.5 / 4.5.
+#define EP_ROUTE_DISPATCH(FN, LT, ...)                                             \
+    do {                                                                           \
+        const bool few = T <= kRouteWideTokens;                                    \
+        if (E <= 8) return FN<LT, 1, 8>(__VA_ARGS__);                              \
+        if (E <= 64)                                                               \
             return few ? FN<LT, 1, 64>(__VA_ARGS__) : FN<LT, 4, 16>(__VA_ARGS__);  \
-        if (E <= 128)                                               \
+        if (E <= 128)                                                              \
             return few ? FN<LT, 2, 64>(__VA_ARGS__) : FN<LT, 8, 16>(__VA_ARGS__);  \
-        if (E <= 256)                                               \
-            return few ? FN<LT, 4, 64>(__VA_ARGS__) : FN<LT, 16, 16>(__VA_ARGS__); \
-        if (E <= 512)                                               \
+        if (E <= 256)                                                              \
+            return few ? FN<LT, 4, 64>(__VA_ARGS__) : FN<LT, 8, 32>(__VA_ARGS__);  \
+        if (E <= 512)                                                              \
             return few ? FN<LT, 8, 64>(__VA_ARGS__) : FN<LT, 16, 32>(__VA_ARGS__); \
-        return FN<LT, 16, 64>(__VA_ARGS__);                         \
+        return FN<LT, 16, 64>(__VA_ARGS__);                                        \
     } while (0)
 
 template <typename LT>

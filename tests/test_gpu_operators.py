@@ -52,6 +52,7 @@ ROUTE = [
     (6, 1024, 33, "bf16", "sigmoid", 1, 1, False, True, 1.0),
     (12, 64, 1, "fp32", "softmax", 64, 1, False, True, 1.0),
     (8, 24, 12, "fp32", "sigmoid", 3, 2, True, True, 1.0),
+    (11, 256, 9, "bf16", "softmax", 64, 12, True, True, 1.0),
 ]
 
 
@@ -99,6 +100,37 @@ def test_route(T, E, K, dtype, score, ng, tg, bias, norm, scale):
     within(w, rw, ref.route_weight_tol(rw, E), "weights")
     again = ep.route(l.cuda(), K, expert_bias=None if b is None else b.cuda(), **kw)
     assert torch.equal(again[0], idx) and torch.equal(again[1], w)
+
+
+LARGE = [(2100, 5, 2, "bf16", "softmax", 1, 1, False), (2300, 40, 4, "fp32", "sigmoid", 5, 2, True),
+         (2200, 100, 8, "bf16", "softmax", 1, 1, False), (2049, 256, 8, "fp32", "sigmoid", 8, 4, True),
+         (2500, 160, 6, "bf16", "sigmoid", 8, 3, True), (2100, 400, 12, "fp32", "softmax", 4, 2, False),
+         (2048, 256, 8, "bf16", "sigmoid", 64, 9, True), (2060, 256, 8, "fp32", "softmax", 64, 9, False)]
+
+
+@pytest.mark.parametrize("T,E,K,dtype,score,ng,tg,bias", LARGE,
+                         ids=["T%d_E%d_K%d_%s_%s_g%d" % c[:6] for c in LARGE])
+def test_route_and_gradient_of_large_batches(T, E, K, dtype, score, ng, tg, bias):
+    """Batches past where a token has a wave of its own: the same tokens in
+    small calls give the same bits, and a sample of them the reference's."""
+    announce("route T=%d E=%d K=%d %s %s groups=%d" % (T, E, K, dtype, score, ng))
+    l = route_logits(T, E, dtype, T + E)
+    b = torch.randn(E, generator=gen(E)) * 0.1 if bias else None
+    kw = dict(score=score, num_groups=ng, topk_groups=tg, normalize=True, scale=1.5)
+    db = None if b is None else b.cuda()
+    idx, w = ep.route(l.cuda(), K, expert_bias=db, **kw)
+    parts = [ep.route(p.cuda(), K, expert_bias=db, **kw) for p in l.split(1000)]
+    assert torch.equal(idx, torch.cat([p[0] for p in parts]))
+    some = torch.cat([torch.arange(12), torch.randint(0, T, (28,), generator=gen(1)),
+                      torch.arange(T - 4, T)])
+    ri, rw = ref.route(l[some], K, bias=b, **kw)
+    assert torch.equal(idx.cpu()[some], ri)
+    within(w.cpu()[some], rw, ref.route_weight_tol(rw, E), "weights")
+    gw = torch.randn((T, K), generator=gen(E))
+    for norm in (False, True):
+        got = ep.route_backward(l.cuda(), idx, gw.cuda(), score=score, normalize=norm, scale=1.5)
+        g, size = ref.route_backward(l, idx.cpu(), gw, score, norm, 1.5)
+        within(got, g, ref.route_backward_tol(g, size, E, l.dtype), "grad_logits")
 
 
 def test_route_at_unaligned_rows_and_in_given_outputs():
