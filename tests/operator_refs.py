@@ -177,8 +177,10 @@ def expert_linear(x, x_scales, weight, scales, zeros, ranges, N, swiglu):
     The bound: a group's sum is formed from |x| (q + 128) <= 143 |x| or from
     |x| q <= 15 |x| and its zero point's part, in fp32; G products are added
     in at most G roundings, counted at a full step 2^-23 each since a matrix
-    instruction may cut instead of rounding; the groups' results, scaled, are
-    added with at most I/G + 64 roundings more."""
+    instruction may cut instead of rounding; where a block's zero points are
+    taken off after its four groups, the four scaled sums and the four
+    corrections are added at that size, 8 roundings more; the groups' results,
+    scaled, are added with at most I/G + 64 roundings more."""
     R, I = x.shape
     E, W, _ = weight.shape
     NG = scales.shape[1]
@@ -202,7 +204,7 @@ def expert_linear(x, x_scales, weight, scales, zeros, ranges, N, swiglu):
         a = rows @ ((q - z) * s).t()
         big = rows.abs() @ (143.0 * s.abs()).t()
         each = rows.abs() @ ((q - z).abs() * s.abs()).t()
-        err = G * 2 * U32 * big + (NG + 64) * U32 * each
+        err = (G + 8) * 2 * U32 * big + (NG + 64) * U32 * each
         if swiglu:
             g, u, eg, eu = a[:, :N], a[:, N:], err[:, :N], err[:, N:]
             sg = g * torch.sigmoid(g)
