@@ -65,6 +65,14 @@ struct ExpertArgs {
     uint16_t* y;
 };
 
+// The same value, unknown to the compiler, which would otherwise compute what
+// follows from it once, ahead of the loop over tasks, and hold it in registers
+// that the loop over blocks needs.
+__device__ __forceinline__ int opaque(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 // Dword j of lane group g becomes dword g of lane group j.
 __device__ __forceinline__ void transpose_groups(i32x4& v) {
     auto a = __builtin_amdgcn_permlane32_swap((unsigned)v[0], (unsigned)v[2], false, false);
@@ -82,14 +90,15 @@ __device__ __forceinline__ void codes_e4m3(int (&o)[2], int v) {
     o[0] = v & 0x0f0f0f0f;
     o[1] = (int)((unsigned)v >> 4) & 0x0f0f0f0f;
 }
-// ... and as bf16 pairs 128 + q: (0,4) (1,5) (2,6) (3,7).
-__device__ __forceinline__ i32x4 codes_bf16(int v) {
+// ... and as bf16 pairs 128 + q: (0,4) (1,5) (2,6) (3,7).  one28 = 0x43004300
+// in a register, so that mask and constant are one instruction.
+__device__ __forceinline__ i32x4 codes_bf16(int v, unsigned one28) {
     const unsigned u = (unsigned)v;
     i32x4 o;
-    o[0] = (int)((u & 0x000f000fu) | 0x43004300u);
-    o[1] = (int)(((u >> 4) & 0x000f000fu) | 0x43004300u);
-    o[2] = (int)(((u >> 8) & 0x000f000fu) | 0x43004300u);
-    o[3] = (int)(((u >> 12) & 0x000f000fu) | 0x43004300u);
+    o[0] = (int)((u & 0x000f000fu) | one28);
+    o[1] = (int)(((u >> 4) & 0x000f000fu) | one28);
+    o[2] = (int)(((u >> 8) & 0x000f000fu) | one28);
+    o[3] = (int)(((u >> 12) & 0x000f000fu) | one28);
     return o;
 }
 // Eight E4M3 values (two dwords) and eight bf16 values in the same orders.
@@ -99,12 +108,14 @@ __device__ __forceinline__ void order_e4m3(int& a, int& b) {
     a = lo;
     b = hi;
 }
-__device__ __forceinline__ i32x4 order_bf16(const i32x4& v) {
+// held false: zeros (the byte selector 0x0c).
+__device__ __forceinline__ i32x4 order_bf16(const i32x4& v, bool held) {
+    const unsigned lo = held ? 0x05040100u : 0x0c0c0c0cu, hi = held ? 0x07060302u : 0x0c0c0c0cu;
     i32x4 o;
-    o[0] = (int)__builtin_amdgcn_perm((unsigned)v[2], (unsigned)v[0], 0x05040100u);
-    o[1] = (int)__builtin_amdgcn_perm((unsigned)v[2], (unsigned)v[0], 0x07060302u);
-    o[2] = (int)__builtin_amdgcn_perm((unsigned)v[3], (unsigned)v[1], 0x05040100u);
-    o[3] = (int)__builtin_amdgcn_perm((unsigned)v[3], (unsigned)v[1], 0x07060302u);
+    o[0] = (int)__builtin_amdgcn_perm((unsigned)v[2], (unsigned)v[0], lo);
+    o[1] = (int)__builtin_amdgcn_perm((unsigned)v[2], (unsigned)v[0], hi);
+    o[2] = (int)__builtin_amdgcn_perm((unsigned)v[3], (unsigned)v[1], lo);
+    o[3] = (int)__builtin_amdgcn_perm((unsigned)v[3], (unsigned)v[1], hi);
     return o;
 }
 
@@ -122,6 +133,11 @@ __device__ __forceinline__ f32x4 mfma32_e4m3(const int (&a)[2], const int (&b)[2
     const long lb = (long)((uint64_t)(unsigned)b[1] << 32 | (unsigned)b[0]);
     return __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(la, lb, c, 0, 0, 0);
 }
+
+// Whether the last block of 128 input channels may be short.  Its missing
+// channels are read at places that exist and enter as rows of zeros.
+template <bool FP8, int G>
+constexpr bool kTail = !FP8 && G < 128;
 
 // What a wave reads for 128 input channels (block b) of its channel and row
 // tiles.  All of a block's loads are issued together, one block ahead of the
@@ -150,9 +166,10 @@ struct Lane {
 template <bool FP8, int G, bool ZP, int RT, int CT>
 __device__ __forceinline__ void load_weights(Block<FP8, G, ZP, RT, CT>& k,
                                              const Lane<RT, CT>& a, int ct, int b) {
-    k.w[ct] = i32x4{0, 0, 0, 0};
-    if (G == 128 || b * 128 + a.lg * 32 < a.I)              // the last block may be short
-        k.w[ct] = *reinterpret_cast<const i32x4*>(a.w + (a.woff[ct] + b * 64));
+    uint32_t at = b * 64;
+    // in a short last block the lane groups past it load codes that meet zeros
+    if (kTail<FP8, G>) at = min(at, a.I / 2 - 16 - a.lg * 16);
+    k.w[ct] = *reinterpret_cast<const i32x4*>(a.w + (a.woff[ct] + at));
 }
 
 template <bool FP8, int G, bool ZP, int RT, int CT>
@@ -170,13 +187,12 @@ __device__ __forceinline__ void load_rows(Block<FP8, G, ZP, RT, CT>& k, const La
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 // the 8 channels of step j that this lane holds codes of
-                const uint32_t c = kb + (G < 128 ? j * 32 + a.lg * 8 : a.lg * 32 + j * 8);
-                k.x[rt][j] = {};
-                if (G == 128 || kb + j * 32 < I) {
-                    using XV = typename Block<FP8, G, ZP, RT, CT>::XV;
-                    k.x[rt][j] = *reinterpret_cast<const XV*>(
-                        a.x + (a.xrow[rt] * I + c) * (FP8 ? 1 : 2));
-                }
+                uint32_t step = G < 128 ? kb + j * 32 : kb + j * 8;
+                if (kTail<FP8, G>) step = min(step, I - 32);
+                const uint32_t c = step + a.lg * (G < 128 ? 8 : 32);
+                using XV = typename Block<FP8, G, ZP, RT, CT>::XV;
+                k.x[rt][j] =
+                    *reinterpret_cast<const XV*>(a.x + (a.xrow[rt] * I + c) * (FP8 ? 1 : 2));
             }
         }
         k.xs[rt] = 1.0f;
@@ -218,8 +234,10 @@ __device__ __forceinline__ void use_block(f32x4 (&acc)[CT][RT],
                                           Block<FP8, G, ZP, RT, CT>& k, int b, int I,
                                           const uint2* s_sc, const unsigned* s_z) {
     const int lg = (threadIdx.x & 63) >> 4, lr = threadIdx.x & 15;
-    // the scales and zero points of the lane's channels of tile ct, group i of the block
-    auto scale = [&](int ct, int i) { return s_sc[i * (CT * 4) + ct * 4 + lg]; };
+    // the scales and zero points of the lane's channels of tile ct, group i of
+    // the block (of a short block: a group that exists, its sums are 0)
+    const int last = (kTail<FP8, G> ? min(I - b * 128, 128) : 128) / G - 1;
+    auto scale = [&](int ct, int i) { return s_sc[min(i, last) * (CT * 4) + ct * 4 + lg]; };
     auto zero_point = [&](int ct, int i) {
         return ZP && G == 128 ? s_z[i * (CT * 4) + ct * 4 + lg] : 0u;
     };
@@ -266,6 +284,7 @@ __device__ __forceinline__ void use_block(f32x4 (&acc)[CT][RT],
         constexpr int kSteps = G / 32;     // matrix instructions per group of scales
         const i32x4 ones = {0x3f803f80, 0x3f803f80, 0x3f803f80, 0x3f803f80};
         const int ones8[2] = {0x38383838, 0x38383838};
+        const unsigned one28 = opaque(0x43004300);
         float sums[RT][4 / kSteps];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
@@ -273,7 +292,6 @@ __device__ __forceinline__ void use_block(f32x4 (&acc)[CT][RT],
             for (int i = 0; i < 4 / kSteps; ++i) sums[rt][i] = 0.0f;
 #pragma unroll
         for (int j0 = 0; j0 < 4; j0 += kSteps) {
-            if (G < 128 && b * 128 + j0 * 32 >= I) break;
             f32x4 d[CT][RT];
             if constexpr (FP8) {
                 int xv[RT][kSteps][2];
@@ -311,7 +329,8 @@ __device__ __forceinline__ void use_block(f32x4 (&acc)[CT][RT],
                     f32x4 sx = zero;
 #pragma unroll
                     for (int j = 0; j < kSteps; ++j) {
-                        xv[rt][j] = order_bf16(k.x[rt][j0 + j]);
+                        xv[rt][j] = order_bf16(
+                            k.x[rt][j0 + j], !kTail<FP8, G> || b * 128 + (j0 + j) * 32 < I);
                         sx = mfma32(ones, xv[rt][j], sx);
                     }
                     sums[rt][j0 / kSteps] = sx[0];
@@ -325,7 +344,7 @@ __device__ __forceinline__ void use_block(f32x4 (&acc)[CT][RT],
                 for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
                     for (int j = 0; j < kSteps; ++j) {
-                        const i32x4 a = codes_bf16(k.w[ct][j0 + j]);
+                        const i32x4 a = codes_bf16(k.w[ct][j0 + j], one28);
 #pragma unroll
                         for (int rt = 0; rt < RT; ++rt)
                             d[ct][rt] = mfma32(a, xv[rt][j], d[ct][rt]);
@@ -341,7 +360,7 @@ __device__ __forceinline__ void use_block(f32x4 (&acc)[CT][RT],
         if constexpr (kLate) {
             // - sum over the block's groups of (z s) (sum x): one fp32 matrix
             // instruction a tile, lane group g holding group g's factors
-            const bool held = lg < 4 / kSteps && (uint32_t)(b * 128 + lg * G) < (uint32_t)I;
+            const bool held = lg <= last;
             float bx[RT];
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
@@ -365,14 +384,6 @@ __device__ __forceinline__ void use_block(f32x4 (&acc)[CT][RT],
             }
         }
     }
-}
-
-// The same value, unknown to the compiler, which would otherwise compute what
-// follows from it once, ahead of the loop over tasks, and hold it in registers
-// that the loop over blocks needs.
-__device__ __forceinline__ int opaque(int v) {
-    asm volatile("" : "+v"(v));
-    return v;
 }
 
 // Rows of expert e: the first one, and how many (0 or less: none).
