@@ -483,7 +483,8 @@ ep_status_t ep_expert_linear_w4(const void* x, const float* x_scales, ep_dtype_t
             return EP_ERR_INVALID_ARG;
     }
     const int64_t W = (int64_t)N * (swiglu ? 2 : 1);
-    if (E > EP_MAX_EXPERTS || W * (I / 2) >= kMaxRows) return EP_ERR_UNSUPPORTED;
+    if (E > EP_MAX_EXPERTS || I > EP_MAX_EXPERT_IN || W * (I / 2) >= kMaxRows)
+        return EP_ERR_UNSUPPORTED;
     return from_hip(ep::launch_expert_linear_w4(
         x, x_scales, fp8, num_rows, expert_offsets, num_tokens_per_expert, capacity, E, I, N, G,
         weight, static_cast<const uint16_t*>(scales), zeros, swiglu != 0,

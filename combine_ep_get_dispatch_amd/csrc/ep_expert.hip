@@ -24,8 +24,8 @@
 // products are exact and the sums fp32; the 128 costs five bits of the 24
 // before a result that is rounded to 8.  A group's sums start from -z sum x (or,
 // where groups are short and have zero points of their own, a block's four
-// corrections are one fp32 matrix instruction: 4 x 4 x 13 instructions a tile
-// less, 9.9 against 17 us at 12 experts x 500 rows of 1440 x 1000, G = 32).
+// corrections are one fp32 matrix instruction: 85 against 92 us at 32 experts
+// x 128 rows, 2048 -> 7168, G = 32).
 //
 // Layout.  Weights are the A operand (16 channels by k), rows the B operand
 // (k by 16 rows), so a lane ends with four neighbouring channels of one row.
@@ -35,9 +35,19 @@
 // 4x4 transpose between them (two swaps of half rows, two of rows) first gives
 // every instruction 32 neighbouring codes.
 //
-// A workgroup owns a tile of channels of one expert for a block of its rows;
-// its waves take every kWaves-th block of 128 input channels and their sums
-// meet in LDS, in wave order.
+// A workgroup owns a tile of 64 weight channels of one expert for a block of
+// its rows; its four waves take every fourth step along the input channels and
+// their sums meet in LDS, in wave order.  Experts of up to 16 rows run with one
+// row tile, others with two (16 experts x 4096 -> 2 x 2048, E4M3 rows: 4 rows
+// each 35 / 37 us, 16 rows 57 / 42, 64 rows 146 / 106).
+//
+// What it took on MI355X, 32 experts x 128 rows, 7168 -> 2 x 2048 with SWIGLU,
+// E4M3 rows (484 MB): 3670 us with a wave per channel, 111 on matrix
+// instructions, 98 with the loads a step ahead and the scales through LDS,
+// 90-95 with the two 64-byte halves of a weight line asked for together (5.4
+// TB/s in the kernel; reading the weights alone in this pattern took 81).  bf16
+// rows, which leave registers for one block at a time: 107-110 us.  One token's
+// eight experts, 2048 -> 7168 (60 MB): 17 us, 10 of them the weights.
 #include "ep_internal.h"
 #include "ep_device.h"
 
@@ -403,16 +413,36 @@ struct Task {
     int64_t begin;
 };
 
-// The experts' row blocks: the first 64 experts' (which a workgroup counts
-// once) in LDS, the others' counted again for every task.
+// The experts come in two classes by their rows: up to 16, which one row tile
+// holds, and more, which two take at once.  A class's row blocks of n rows:
+template <int RT>
+__device__ __forceinline__ int row_blocks(int n) {
+    const bool mine = RT == 1 ? n <= 16 : n > 16;
+    return mine ? (int)(((unsigned)n + RT * 16 - 1) / (RT * 16)) : 0;
+}
+
+// The first kKnown experts, which a workgroup counts once: first row, rows, and
+// the class's row blocks of experts 0..i; the others are counted again for
+// every task.
+constexpr int kKnown = 256;
 struct RowBlocks {
-    int first[64], rows[64], upto[64];   // first row, rows, row blocks of experts 0..i
+    int first[kKnown], rows[kKnown], upto[2][kKnown];
 };
 
+__device__ __forceinline__ int prefix_sum(int v) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(v, d);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+
 // The task at place `task` of the order: the (row block, channel tile) pairs of
-// the experts that have rows, the row blocks of a tile next to each other (they
-// share its weights) and the tiles of an expert next to each other (they share
-// its rows, and lines of its scales).  False if there is none.
+// the class's experts, the row blocks of a tile next to each other (they share
+// its weights) and the tiles of an expert next to each other (they share its
+// rows, and lines of its scales).  False if there is none.
 template <int RT>
 __device__ __forceinline__ bool find_task(Task& t, const ExpertArgs& p, const RowBlocks& rbs,
                                           int task, int ntile, int channels) {
@@ -420,22 +450,16 @@ __device__ __forceinline__ bool find_task(Task& t, const ExpertArgs& p, const Ro
     int before = 0;
     for (int e0 = 0; e0 < p.E; e0 += 64) {
         int first, rows, upto;
-        if (e0 == 0) {
-            first = rbs.first[lane];
-            rows = rbs.rows[lane];
-            upto = rbs.upto[lane];
+        if (e0 < kKnown) {
+            first = rbs.first[e0 + lane];
+            rows = rbs.rows[e0 + lane];
+            upto = rbs.upto[RT - 1][e0 + lane];
         } else {
             int64_t b = 0, m = 0;
             if (e0 + lane < p.E) m = expert_rows(p, e0 + lane, b);
             first = (int)b;
             rows = m > 0 ? (int)m : 0;
-            upto = (rows + RT * 16 - 1) / (RT * 16);
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int o = __shfl_up(upto, d);
-                if (lane >= d) upto += o;
-            }
-            upto += before;
+            upto = prefix_sum(row_blocks<RT>(rows)) + before;
         }
         const uint64_t hit = __ballot(upto * ntile > task);
         if (hit) {
@@ -443,7 +467,7 @@ __device__ __forceinline__ bool find_task(Task& t, const ExpertArgs& p, const Ro
             t.e = e0 + at;
             t.n = __builtin_amdgcn_readlane(rows, at);
             t.begin = __builtin_amdgcn_readlane(first, at);
-            const int nb = (t.n + RT * 16 - 1) / (RT * 16);
+            const int nb = row_blocks<RT>(t.n);
             const unsigned local = task - (__builtin_amdgcn_readlane(upto, at) - nb) * ntile;
             const unsigned tile = nb == 1 ? local : local / (unsigned)nb;
             t.n0 = tile * channels;
@@ -457,24 +481,25 @@ __device__ __forceinline__ bool find_task(Task& t, const ExpertArgs& p, const Ro
 
 // The scales and zero points of a workgroup's channels for a chunk of input
 // channels, [group][channel / 4], and the waves' sums.
-template <int G, bool ZP, int RT, int CT>
+template <int G, bool ZP>
 struct ExpertLds {
+    static constexpr int CT = kExpertTiles;
     static constexpr int kChunk = G == 32 ? 32 : 64;       // blocks of 128 channels
     static constexpr int kEntries = kChunk * (128 / G) * CT * 4;
     uint2 sc[kEntries];
     unsigned z[ZP ? kEntries : 1];
-    f32x4 part[kExpertWaves * CT * RT * 64];
+    f32x4 part[kExpertWaves * CT * 2 * 64];
     RowBlocks rbs;
 };
 
-// Every XCD (workgroups i, i + 8, ...) gets one run of the tasks, which its
-// workgroups stride over.  Experts without rows have no tasks.  The first loads
-// of a workgroup's next task are issued before it finishes the one at hand.
-template <bool FP8, int G, bool ZP, bool SWIGLU, int RT, int CT, int NB, int WPS>
-__global__ __launch_bounds__(kExpertWaves * 64, WPS) void expert_linear_kernel(const ExpertArgs p) {
-    using Lds = ExpertLds<G, ZP, RT, CT>;
+// A workgroup's tasks of one class: task, task + stride, ... below end.  The
+// first loads of its next task are issued before it finishes the one at hand.
+template <bool FP8, int G, bool ZP, bool SWIGLU, int RT, int NB>
+__device__ __forceinline__ void run_tasks(const ExpertArgs& p, ExpertLds<G, ZP>& lds, int task,
+                                          int end, int stride) {
+    constexpr int CT = kExpertTiles;
+    using Lds = ExpertLds<G, ZP>;
     using Blk = Block<FP8, G, ZP, RT, CT>;
-    __shared__ Lds lds;
     constexpr int kChannels = CT * 16 / (SWIGLU ? 2 : 1);
     constexpr int kThreads = kExpertWaves * 64;
     const int lane = threadIdx.x & 63;
@@ -484,33 +509,6 @@ __global__ __launch_bounds__(kExpertWaves * 64, WPS) void expert_linear_kernel(c
     const int W = SWIGLU ? 2 * N : N;
     const int nblk = (I + 127) / 128;
     const int ntile = (N + kChannels - 1) / kChannels;
-
-    // Row blocks of the experts; every wave writes the same numbers, and reads
-    // its own.
-    int64_t total = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 64) {
-        int64_t b = 0, m = 0;
-        if (e0 + lane < p.E) m = expert_rows(p, e0 + lane, b);
-        const int rows = m > 0 ? (int)m : 0;
-        int upto = (rows + RT * 16 - 1) / (RT * 16);
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(upto, d);
-            if (lane >= d) upto += o;
-        }
-        if (e0 == 0) {
-            lds.rbs.first[lane] = (int)b;
-            lds.rbs.rows[lane] = rows;
-            lds.rbs.upto[lane] = upto;
-        }
-        total += __builtin_amdgcn_readlane(upto, 63);
-    }
-    // (a y of 2^31 tasks fits no memory: such counts do not belong to these rows)
-    const int tasks = total * ntile < (1 << 30) ? (int)total * ntile : 0;
-    const int per = (tasks + kXcds - 1) / kXcds;
-    const int end = min(tasks, (int)(blockIdx.x % kXcds + 1) * per);
-    int task = blockIdx.x % kXcds * per + blockIdx.x / kXcds;
-    const int stride = gridDim.x / kXcds;
 
     Task t;
     Lane<RT, CT> a;
@@ -682,41 +680,73 @@ __global__ __launch_bounds__(kExpertWaves * 64, WPS) void expert_linear_kernel(c
     }
 }
 
+// Every XCD (workgroups i, i + 8, ...) gets one run of a class's tasks, which
+// its workgroups stride over; the second class goes on where the first left
+// off.  Experts without rows have no tasks.
 template <bool FP8, int G, bool ZP, bool SWIGLU>
-void launch_r(dim3 grid, hipStream_t s, const ExpertArgs& p, int rt) {
-    const dim3 block(kExpertWaves * 64);
-    if (rt == 1)
-        hipLaunchKernelGGL(
-            (expert_linear_kernel<FP8, G, ZP, SWIGLU, 1, kExpertTiles,
-                                  few_blocks(FP8), few_waves(FP8)>), grid,
-            block, 0, s, p);
-    else
-        hipLaunchKernelGGL(
-            (expert_linear_kernel<FP8, G, ZP, SWIGLU, kExpertRowTiles, kExpertTiles, 1, 2>), grid,
-            block, 0, s, p);
+__global__ __launch_bounds__(kExpertWaves * 64, kExpertWavesPerSimd) void expert_linear_kernel(
+    const ExpertArgs p) {
+    __shared__ ExpertLds<G, ZP> lds;
+    constexpr int kChannels = kExpertTiles * 16 / (SWIGLU ? 2 : 1);
+    const int lane = threadIdx.x & 63;
+    const int ntile = (p.N + kChannels - 1) / kChannels;
+
+    // Row blocks of the classes; every wave writes the same numbers, and reads
+    // its own.
+    int64_t few = 0, many = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 64) {
+        int64_t b = 0, m = 0;
+        if (e0 + lane < p.E) m = expert_rows(p, e0 + lane, b);
+        const int rows = m > 0 ? (int)m : 0;
+        const int f = prefix_sum(row_blocks<1>(rows)), g = prefix_sum(row_blocks<2>(rows));
+        if (e0 < kKnown) {
+            lds.rbs.first[e0 + lane] = (int)b;
+            lds.rbs.rows[e0 + lane] = rows;
+            lds.rbs.upto[0][e0 + lane] = (int)few + f;
+            lds.rbs.upto[1][e0 + lane] = (int)many + g;
+        }
+        few += __builtin_amdgcn_readlane(f, 63);
+        many += __builtin_amdgcn_readlane(g, 63);
+    }
+    // (a y of 2^30 tasks fits no memory: such counts do not belong to these rows)
+    if ((few + many) * ntile >= 1 << 30) return;
+    const int stride = gridDim.x / kXcds, xcd = blockIdx.x % kXcds;
+    int slot = blockIdx.x / kXcds;
+    if (few > 0) {
+        const int tasks = (int)few * ntile, per = (tasks + kXcds - 1) / kXcds;
+        run_tasks<FP8, G, ZP, SWIGLU, 1, few_blocks(FP8)>(p, lds, xcd * per + slot,
+                                                          min(tasks, (xcd + 1) * per), stride);
+        slot = (slot + stride - per % stride) % stride;
+    }
+    if (many > 0) {
+        const int tasks = (int)many * ntile, per = (tasks + kXcds - 1) / kXcds;
+        run_tasks<FP8, G, ZP, SWIGLU, 2, 1>(p, lds, xcd * per + slot,
+                                            min(tasks, (xcd + 1) * per), stride);
+    }
 }
 
 template <bool FP8, int G>
-void launch_g(dim3 grid, hipStream_t s, const ExpertArgs& p, bool swiglu, int rt) {
+void launch_g(dim3 grid, hipStream_t s, const ExpertArgs& p, bool swiglu) {
+    const dim3 block(kExpertWaves * 64);
     if (p.zeros) {
         if (swiglu)
-            launch_r<FP8, G, true, true>(grid, s, p, rt);
+            hipLaunchKernelGGL((expert_linear_kernel<FP8, G, true, true>), grid, block, 0, s, p);
         else
-            launch_r<FP8, G, true, false>(grid, s, p, rt);
+            hipLaunchKernelGGL((expert_linear_kernel<FP8, G, true, false>), grid, block, 0, s, p);
     } else {
         if (swiglu)
-            launch_r<FP8, G, false, true>(grid, s, p, rt);
+            hipLaunchKernelGGL((expert_linear_kernel<FP8, G, false, true>), grid, block, 0, s, p);
         else
-            launch_r<FP8, G, false, false>(grid, s, p, rt);
+            hipLaunchKernelGGL((expert_linear_kernel<FP8, G, false, false>), grid, block, 0, s, p);
     }
 }
 
 template <bool FP8>
-void launch_t(int G, dim3 grid, hipStream_t s, const ExpertArgs& p, bool swiglu, int rt) {
+void launch_t(int G, dim3 grid, hipStream_t s, const ExpertArgs& p, bool swiglu) {
     switch (G) {
-        case 32: launch_g<FP8, 32>(grid, s, p, swiglu, rt); break;
-        case 64: launch_g<FP8, 64>(grid, s, p, swiglu, rt); break;
-        default: launch_g<FP8, 128>(grid, s, p, swiglu, rt); break;
+        case 32: launch_g<FP8, 32>(grid, s, p, swiglu); break;
+        case 64: launch_g<FP8, 64>(grid, s, p, swiglu); break;
+        default: launch_g<FP8, 128>(grid, s, p, swiglu); break;
     }
 }
 
@@ -730,19 +760,16 @@ hipError_t launch_expert_linear_w4(const void* x, const float* xs, bool fp8, int
     if (num_rows == 0) return hipSuccess;
     const ExpertArgs p = {static_cast<const uint8_t*>(x), xs, num_rows, offsets, counts, capacity,
                           E, I, N, w, scales, zeros, y};
-    const int64_t avg = offsets ? num_rows / E : capacity;
-    const int rt = avg <= kExpertFewRows ? 1 : kExpertRowTiles;
     const int tile = kExpertTiles * 16 / (swiglu ? 2 : 1);
     // at most one workgroup per task, and no more than the GPU holds at once
-    const int64_t blocks = offsets ? E + num_rows / (rt * 16)
-                                   : (int64_t)E * ((capacity + rt * 16 - 1) / (rt * 16));
+    const int64_t blocks = offsets ? E + num_rows / 16 : (int64_t)E * ((capacity + 15) / 16);
     const int64_t tasks = blocks * ((N + tile - 1) / tile);
-    const int64_t held = (rt == 1 ? few_waves(fp8) : 2) * 4 / kExpertWaves * kCus;
+    const int64_t held = kExpertWavesPerSimd * 4 / kExpertWaves * kCus;
     const dim3 grid((unsigned)(((tasks < held ? tasks : held) + kXcds - 1) / kXcds * kXcds));
     if (fp8)
-        launch_t<true>(G, grid, s, p, swiglu, rt);
+        launch_t<true>(G, grid, s, p, swiglu);
     else
-        launch_t<false>(G, grid, s, p, swiglu, rt);
+        launch_t<false>(G, grid, s, p, swiglu);
     return hipGetLastError();
 }
 

@@ -264,17 +264,14 @@ hipError_t launch_route_backward(const void* logits, bool bf16, const int64_t* t
 
 // ---------------------------------------------------------------- experts ---
 // A workgroup's waves, its channel tiles of 16 (gate and up halves with the
-// activation) and the row tiles of 16 it takes at once.
+// activation), and the waves per SIMD that leave registers for two steps.
 constexpr int kExpertWaves = 4;
-// With one row tile: blocks of 128 input channels a wave takes at a time, and
-// waves per SIMD (registers for two such steps under way).  E4M3 rows leave
-// room for two blocks, so a wave reads whole 128-byte lines of the weights;
+constexpr int kExpertTiles = 4;
+constexpr int kExpertWavesPerSimd = 2;
+// With one row tile: blocks of 128 input channels a wave takes at a time.  E4M3
+// rows leave room for two, so a wave reads whole 128-byte lines of the weights;
 // bf16 rows fill the registers that this would take.
 constexpr int few_blocks(bool fp8) { return fp8 ? 2 : 1; }
-constexpr int few_waves(bool fp8) { return fp8 ? 2 : 3; }
-constexpr int kExpertTiles = 4;
-constexpr int kExpertRowTiles = 2;
-constexpr int kExpertFewRows = 64;
 constexpr int kXcds = 8;
 constexpr int kCus = 256;
 

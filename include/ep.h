@@ -83,6 +83,7 @@ typedef enum EP_ENUM_BASE {
 #define EP_MAX_EXPERT_ALIGNMENT 1024   /* of ep_layout_dispatch_aligned */
 #define EP_STATIC_SCRATCH_BYTES (8u << 20)   /* per GPU, of ep_layout_dispatch_static */
 #define EP_MAX_ROUTE_GROUPS 64   /* expert groups of ep_route */
+#define EP_MAX_EXPERT_IN (1 << 24)   /* input channels of ep_expert_linear_w4 */
 
 /*
  * Bytes of device workspace that ep_get_dispatch_layout and ep_dispatch need
@@ -510,7 +511,7 @@ ep_status_t ep_route_backward(const void *logits, ep_dtype_t logits_dtype,
  * I > 0, N > 0, N % 8 == 0; x, weight, y 16-byte aligned, scales 8-byte,
  * zeros 4-byte.  capacity is ignored with expert_offsets, else >= 1 with
  * E*capacity <= num_rows; num_rows < 2^31.  EP_ERR_UNSUPPORTED for
- * E > EP_MAX_EXPERTS or W * I/2 >= 2^31.  x and the scales are expected
+ * E > EP_MAX_EXPERTS, I > EP_MAX_EXPERT_IN or W * I/2 >= 2^31.  x and the scales are expected
  * finite, |x| < 2^119.  No workspace; the order of the sums is fixed by the
  * arguments' shapes.  (No page describes the experts themselves; format and
  * definition are this library's.)

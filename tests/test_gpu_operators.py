@@ -372,6 +372,17 @@ EXPERT = [
     (1, 300, [290], 896, 64, 128, False, False, False, True),
     (2, 16, [16, 11], 7168, 64, 128, True, False, True, False),
     (2, 16, [3, 11], 7168, 40, 64, False, True, False, False),
+    # many experts, few and many rows among them
+    (70, 20, [(7 * e) % 23 for e in range(70)], 128, 40, 64, False, True, False, False),
+    (130, 36, [(11 * e) % 37 for e in range(130)], 256, 72, 128, True, False, True, True),
+    (66, 18, [0] * 64 + [17, 2], 96, 16, 32, False, True, False, True),
+    (400, 18, [(5 * e) % 19 if e > 250 else 0 for e in range(400)], 64, 16, 32, False, False, False,
+     False),
+    # more input channels than the scales of one round
+    (2, 20, [20, 9], 8320, 24, 128, True, True, False, False),
+    (2, 20, [4, 18], 4192, 72, 32, False, True, True, False),
+    (1, 40, [40], 16576, 16, 64, False, False, False, True),
+    (2, 3, [3, 2], 4224, 16, 32, True, True, False, False),
 ]
 
 
@@ -446,6 +457,28 @@ def test_expert_linear_ignores_rows_outside_the_buffer():
     want, err = ref.expert_linear(x, None, w, s, None, [(0, 2), (0, 0), (8, 2), (0, 0)], N, False)
     within(got, want, err * (1 + ref.UBF) + ref.UBF * want.abs() + ref.TINY, "y")
     assert bool((got.cpu()[torch.isnan(want[:, 0])] == 6.5).all())
+
+
+@pytest.mark.parametrize("n", [1, 15, 16, 17, 31, 32, 33, 48, 64, 65])
+def test_expert_linear_row_counts_share_their_rows_results(n):
+    """A row's result does not depend on how many rows stand beside it by more
+    than the sums' roundings, and not at all on what stands in the rows after
+    the expert's last one."""
+    C, I, N, G = 70, 512, 40, 128
+    x, xs, w, s, _ = expert_inputs(1, C, I, N, G, True, False, False, 11)
+    full = ep.expert_linear_w4(x.cuda(), w.cuda(), s.cuda(),
+                               torch.tensor([C], dtype=torch.int32, device="cuda"), capacity=C,
+                               x_scales=xs.cuda())
+    x2, xs2 = x.clone(), xs.clone()
+    x2[n:] = 0x7f                                     # NaN codes past the rows held
+    xs2[n:] = math.nan
+    part = ep.expert_linear_w4(x2.cuda(), w.cuda(), s.cuda(),
+                               torch.tensor([n], dtype=torch.int32, device="cuda"), capacity=C,
+                               x_scales=xs2.cuda(), out=torch.full_like(full, 6.5))
+    want, err = ref.expert_linear(x, xs, w, s, None, [(0, n)], N, False)
+    for got in (full, part):
+        within(got, want, err * (1 + ref.UBF) + ref.UBF * want.abs() + ref.TINY, "y")
+    assert bool((part.cpu()[n:] == 6.5).all())
 
 
 def test_expert_linear_with_exact_numbers():

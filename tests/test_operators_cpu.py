@@ -106,6 +106,7 @@ def test_expert_linear_rejects_bad_arguments(buf):
     assert call(E=2048, C=1, rows=4096) == UNSUPPORTED
     assert call(I=1 << 20, N=1 << 12) == UNSUPPORTED
     assert call(I=1 << 20, N=1 << 11, act=1) == UNSUPPORTED
+    assert call(I=(1 << 24) + 128, N=8) == UNSUPPORTED
 
 
 @pytest.fixture
