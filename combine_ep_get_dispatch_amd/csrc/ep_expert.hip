@@ -448,6 +448,7 @@ __device__ __forceinline__ bool find_task(Task& t, const ExpertArgs& p, const Ro
                                           int task, int ntile, int channels) {
     const int lane = threadIdx.x & 63;
     int before = 0;
+#pragma unroll 1
     for (int e0 = 0; e0 < p.E; e0 += 64) {
         int first, rows, upto;
         if (e0 < kKnown) {
@@ -492,8 +493,7 @@ struct ExpertLds {
     RowBlocks rbs;
 };
 
-// A workgroup's tasks of one class: task, task + stride, ... below end.  The
-// first loads of its next task are issued before it finishes the one at hand.
+// A workgroup's tasks of one class: task, task + stride, ... below end.
 template <bool FP8, int G, bool ZP, bool SWIGLU, int RT, int NB>
 __device__ __forceinline__ void run_tasks(const ExpertArgs& p, ExpertLds<G, ZP>& lds, int task,
                                           int end, int stride) {
@@ -571,9 +571,7 @@ __device__ __forceinline__ void run_tasks(const ExpertArgs& p, ExpertLds<G, ZP>&
     };
 
     // A wave takes steps of NB neighbouring blocks, every kExpertWaves-th step
-    // of a chunk.  The load after its last step takes that step again, and a
-    // step's second block past the end the last one, so that the number of
-    // loads under way is the same on every path.
+    // of a chunk; a step's second block past the end is the last one again.
     Blk k0[NB], k1[NB];
     f32x4 acc[CT][RT];
     auto load = [&](Blk (&k)[NB], int c0, int st) {
@@ -602,54 +600,73 @@ __device__ __forceinline__ void run_tasks(const ExpertArgs& p, ExpertLds<G, ZP>&
         }
         __builtin_amdgcn_sched_barrier(0);
     };
-    // A chunk's first loads: the scales ahead of the weights, which then travel
-    // while the scales are put in place.
-    auto start = [&](int c0) {
+    auto nsteps = [&](int c0) { return (min(Lds::kChunk, nblk - c0) + NB - 1) / NB; };
+    // The first loads of a chunk: its scales ahead of the weights, which then
+    // travel while the scales are put in place.  They are issued before the last
+    // step of the chunk ahead of it (of this task or the last one) is worked on.
+    // (Where a step is worked on, the number of loads under way is the same on
+    // every path to it, so that it waits for its own alone.)
+    int c0 = 0;
+    if (task >= end || !find_task<RT>(t, p, lds.rbs, task, ntile, kChannels)) return;
+    auto start = [&]() {
         fetch(c0, 0);
         __builtin_amdgcn_sched_barrier(0);
-        if (wave * NB < min(Lds::kChunk, nblk - c0)) load(k0, c0, wave);
+        load(k0, c0, min(wave, nsteps(c0) - 1));
     };
-
-    bool more = task < end && find_task<RT>(t, p, lds.rbs, task, ntile, kChannels);
-    if (more) {
-        aim();
-        start(0);
-    }
-    while (more) {
+    aim();
+    start();
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
+    for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) acc[ct][rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int c0 = 0; c0 < nblk; c0 += Lds::kChunk) {
-            if (c0 > 0) {
-                start(c0);
-                __syncthreads();                // the last chunk's scales are done with
-            }
-            keep(c0, 0);
-            for (int first = kRound; first < entries(c0); first += kRound) {
-                fetch(c0, first);
-                keep(c0, first);
-            }
-            __syncthreads();
-            const int nstep = (min(Lds::kChunk, nblk - c0) + NB - 1) / NB;
-            if (wave < nstep) {
-                const int last = wave + (nstep - 1 - wave) / kExpertWaves * kExpertWaves;
-                int st = wave;
-                for (; st < last; st += 2 * kExpertWaves) {
-                    load(k1, c0, st + kExpertWaves);
-                    use(k0, c0, st);
-                    load(k0, c0, min(st + 2 * kExpertWaves, last));
-                    use(k1, c0, st + kExpertWaves);
-                }
-                if (st == last) use(k0, c0, st);
-            }
-        }
+        for (int rt = 0; rt < RT; ++rt) acc[ct][rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    while (true) {
         const Task done = t;
-        task += stride;
-        more = task < end && find_task<RT>(t, p, lds.rbs, task, ntile, kChannels);
-        if (more) {
+        const int b0 = c0, nstep = nsteps(b0);
+        const bool whole = b0 + Lds::kChunk >= nblk;        // the task's last chunk
+        Task then = t;
+        bool more = true;
+        if (whole) {
+            task += stride;
+            more = task < end && find_task<RT>(then, p, lds.rbs, task, ntile, kChannels);
+        }
+        auto next = [&]() {
+            t = then;
+            c0 = whole ? 0 : b0 + Lds::kChunk;
             aim();
-            start(0);
+            start();
+        };
+        keep(b0, 0);
+        for (int first = kRound; first < entries(b0); first += kRound) {
+            fetch(b0, first);
+            keep(b0, first);
+        }
+        __syncthreads();
+        // (a wave without a step has last = wave - kExpertWaves)
+        const int last =
+            wave + (nstep + kExpertWaves - 1 - wave) / kExpertWaves * kExpertWaves - kExpertWaves;
+        int st = wave;
+        for (; st + 2 * kExpertWaves <= last; st += 2 * kExpertWaves) {
+            load(k1, b0, st + kExpertWaves);
+            use(k0, b0, st);
+            load(k0, b0, st + 2 * kExpertWaves);
+            use(k1, b0, st + kExpertWaves);
+        }
+        if (st < last) {
+            load(k1, b0, st + kExpertWaves);
+            use(k0, b0, st);
+            if (more) {
+                next();
+                use(k1, b0, st + kExpertWaves);
+            } else {
+                use(k1, b0, st + kExpertWaves);
+            }
+        } else {
+            if (st == last) use(k0, b0, st);
+            if (more) next();
+        }
+        if (!whole) {
+            __syncthreads();                    // this chunk's scales are done with
+            continue;
         }
 
         // the waves' sums, in wave order; wave i finishes tiles i, i + kExpertWaves, ...
@@ -677,6 +694,11 @@ __device__ __forceinline__ void run_tasks(const ExpertArgs& p, ExpertLds<G, ZP>&
                 *reinterpret_cast<uint2*>(p.y + (done.begin + row) * N + c) = o2;
             }
         }
+        if (!more) break;
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) acc[ct][rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 }
 
@@ -694,6 +716,7 @@ __global__ __launch_bounds__(kExpertWaves * 64, kExpertWavesPerSimd) void expert
     // Row blocks of the classes; every wave writes the same numbers, and reads
     // its own.
     int64_t few = 0, many = 0;
+#pragma unroll 1
     for (int e0 = 0; e0 < p.E; e0 += 64) {
         int64_t b = 0, m = 0;
         if (e0 + lane < p.E) m = expert_rows(p, e0 + lane, b);
