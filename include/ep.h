@@ -499,7 +499,7 @@ ep_status_t ep_route_backward(const void *logits, ep_dtype_t logits_dtype,
  *   expert_offsets NULL (the fixed-capacity layout) rows e*capacity ..
  *   e*capacity + min(num_tokens_per_expert[e], capacity) - 1.  Rows outside
  *   [0, num_rows) are neither read nor written; rows of no expert are left
- *   untouched in y.
+ *   untouched in y.  Runs of different experts do not overlap.
  *   x: x_dtype EP_DTYPE_BF16, bf16 [num_rows*I], x_scales ignored; or
  *   EP_DTYPE_FP8_E4M3, codes [num_rows*I] and x_scales fp32 [num_rows*I/128],
  *   as dispatch writes them (I % 128 == 0).
