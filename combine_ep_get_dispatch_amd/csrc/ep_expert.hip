@@ -176,10 +176,12 @@ struct Lane {
 template <bool FP8, int G, bool ZP, int RT, int CT>
 __device__ __forceinline__ void load_weights(Block<FP8, G, ZP, RT, CT>& k,
                                              const Lane<RT, CT>& a, int ct, int b) {
-    uint32_t at = b * 64;
-    // in a short last block the lane groups past it load codes that meet zeros
-    if (kTail<FP8, G>) at = min(at, a.I / 2 - 16 - a.lg * 16);
-    k.w[ct] = *reinterpret_cast<const i32x4*>(a.w + (a.woff[ct] + at));
+    int at = b * 64;
+    // In a short last block the lane groups past it load the row's last codes,
+    // which meet zeros.  (Below 128 channels that is ahead of the lane's own
+    // place, woff, which holds its 16 lg: a negative step.)
+    if (kTail<FP8, G>) at = min(at, (int)(a.I / 2) - 16 - (int)a.lg * 16);
+    k.w[ct] = *reinterpret_cast<const i32x4*>(a.w + (a.woff[ct] + (uint32_t)at));
 }
 
 template <bool FP8, int G, bool ZP, int RT, int CT>

@@ -501,6 +501,33 @@ def test_expert_linear_with_exact_numbers():
     assert torch.equal(got.cpu().double()[held], want[held])
 
 
+def at_the_end(t):
+    """t's copy in the last bytes of a device allocation of its own."""
+    if t is None:
+        return None
+    whole = torch.empty(32 << 20, dtype=torch.uint8, device="cuda")
+    v = whole[whole.numel() - t.numel() * t.element_size():].view(t.dtype).view(t.shape)
+    return v.copy_(t)
+
+
+@pytest.mark.parametrize("I,G,fp8,zeros", [(32, 32, False, True), (64, 32, False, False),
+                                           (64, 64, False, True), (96, 32, False, True),
+                                           (192, 64, False, False), (128, 128, False, True),
+                                           (128, 32, True, True), (256, 128, True, False)])
+@pytest.mark.parametrize("n", [3, 20])
+def test_expert_linear_with_operands_at_the_ends_of_their_memory(I, G, fp8, zeros, n):
+    announce("expert_linear_w4 at the ends of memory: I=%d G=%d fp8=%s n=%d" % (I, G, fp8, n))
+    E, N = 2, 24
+    x, xs, w, s, z = expert_inputs(E, n, I, N, G, fp8, zeros, False, I + n)
+    cnt = torch.tensor([n, n], dtype=torch.int32)
+    y = at_the_end(torch.zeros((E * n, N), dtype=torch.bfloat16))
+    got = ep.expert_linear_w4(at_the_end(x), at_the_end(w), at_the_end(s), at_the_end(cnt),
+                              capacity=n, x_scales=at_the_end(xs), zeros=at_the_end(z), out=y)
+    torch.cuda.synchronize()
+    want, err = ref.expert_linear(x, xs, w, s, z, [(0, n), (n, n)], N, False)
+    within(got, want, err * (1 + ref.UBF) + ref.UBF * want.abs() + ref.TINY, "y")
+
+
 def test_expert_linear_of_no_rows():
     _, _, w, s, _ = expert_inputs(2, 1, 64, 8, 32, False, False, False, 1)
     x = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
