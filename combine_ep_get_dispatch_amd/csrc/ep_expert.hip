@@ -690,10 +690,10 @@ __device__ __forceinline__ void run_tasks(const ExpertArgs& p, ExpertLds<G, ZP>&
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[i] = v[i] / (1.0f + expf(-v[i])) * u[i];
             }
-            const int row = done.r0 + rt * 16 + lr, c = done.n0 + ct * 16 + lg * 4;
-            if (row < done.n && c < N) {
+            const int row = rt * 16 + lr, c = done.n0 + ct * 16 + lg * 4;
+            if (row < done.n - done.r0 && c < N) {
                 const uint2 o2 = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-                *reinterpret_cast<uint2*>(p.y + (done.begin + row) * N + c) = o2;
+                *reinterpret_cast<uint2*>(p.y + (done.begin + done.r0 + row) * N + c) = o2;
             }
         }
         if (!more) break;
@@ -787,7 +787,8 @@ hipError_t launch_expert_linear_w4(const void* x, const float* xs, bool fp8, int
                           E, I, N, w, scales, zeros, y};
     const int tile = kExpertTiles * 16 / (swiglu ? 2 : 1);
     // at most one workgroup per task, and no more than the GPU holds at once
-    const int64_t blocks = offsets ? E + num_rows / 16 : (int64_t)E * ((capacity + 15) / 16);
+    const int64_t blocks =
+        offsets ? E + num_rows / 16 : (int64_t)E * (((int64_t)capacity + 15) / 16);
     const int64_t tasks = blocks * ((N + tile - 1) / tile);
     const int64_t held = kExpertWavesPerSimd * 4 / kExpertWaves * kCus;
     const dim3 grid((unsigned)(((tasks < held ? tasks : held) + kXcds - 1) / kXcds * kXcds));

@@ -501,6 +501,20 @@ def test_expert_linear_with_exact_numbers():
     assert torch.equal(got.cpu().double()[held], want[held])
 
 
+def test_expert_linear_of_the_largest_capacity():
+    """A capacity of almost 2^31 rows, of which a few hold a token (the others
+    need no memory: they are neither read nor written)."""
+    I, N, G, n = 64, 16, 32, 5
+    x, _, w, s, _ = expert_inputs(1, n, I, N, G, False, False, False, 9)
+    x, w, s = x.cuda(), w.cuda(), s.cuda()
+    cnt = torch.tensor([n], dtype=torch.int32, device="cuda")
+    y = torch.zeros((n, N), dtype=torch.bfloat16, device="cuda")
+    ep._launch("ep_expert_linear_w4", x, x.data_ptr(), None, ep.EP_DTYPE_BF16, 2**31 - 1, None,
+               cnt.data_ptr(), 2**31 - 1, 1, I, N, G, w.data_ptr(), s.data_ptr(), None, 0,
+               y.data_ptr())
+    assert torch.equal(y, ep.expert_linear_w4(x, w, s, cnt, capacity=n))
+
+
 def at_the_end(t):
     """t's copy in the last bytes of a device allocation of its own."""
     if t is None:
