@@ -366,7 +366,8 @@ ep_status_t ep_combine_backward(const void* grad_out, const void* y, int64_t num
     if (K > EP_MAX_TOPK) return EP_ERR_UNSUPPORTED;
     if (T > 0) {
         // without rows every slot is skipped: grad_y and y may then be empty
-        if (!grad_out || !dst_row || (!grad_weights && !grad_y)) return EP_ERR_INVALID_ARG;
+        if (!grad_out || !dst_row) return EP_ERR_INVALID_ARG;
+        if (!grad_weights && !grad_y && num_rows > 0) return EP_ERR_INVALID_ARG;
         if (grad_y && !topk_weights) return EP_ERR_INVALID_ARG;
         if (grad_weights && num_rows > 0 && !y) return EP_ERR_INVALID_ARG;
         if (!aligned16(grad_out) || (y && !aligned16(y)) || (grad_y && !aligned16(grad_y)))

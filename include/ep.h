@@ -404,8 +404,9 @@ ep_status_t ep_combine_cu(const void *y, int64_t num_rows, const int32_t *dst_ro
  * slots name it, which one's gradient it holds is unspecified).
  *   grad_y NULL: only grad_weights (topk_weights may then be NULL).
  *   grad_weights NULL: only grad_y (y may then be NULL).
- * Both NULL is EP_ERR_INVALID_ARG.  Types, shapes, limits and errors as
- * ep_combine: grad_out bf16 [T*H], y and grad_y bf16 [num_rows*H],
+ * Both NULL is EP_ERR_INVALID_ARG, unless num_rows is 0 (grad_y is then empty).
+ * Types, shapes, limits and errors as ep_combine: grad_out bf16 [T*H], y and
+ * grad_y bf16 [num_rows*H],
  * topk_weights and grad_weights fp32 [T*K]; grad_out, y and grad_y 16-byte
  * aligned.  T may be 0.
  */

@@ -321,6 +321,10 @@ def test_backward_without_rows_or_tokens():
     gy, gw = ep.combine_backward(go, none, dst, torch.ones((3, 2), device="cuda"))
     assert gy.shape == (0, 16) and bool((gw == 0).all())
     assert bool((ep.dispatch_backward(none, dst) == 0).all())
+    gy, gw = ep.combine_backward(go, None, dst, torch.ones((3, 2), device="cuda"), num_rows=0)
+    assert gy.shape == (0, 16) and gw is None
+    gy, gw = ep.combine_backward(go, none, dst, None)
+    assert gy is None and bool((gw == 0).all())
     empty = dst[:0]
     gy, gw = ep.combine_backward(go[:0], go, empty, torch.ones((0, 2), device="cuda"))
     assert gw.shape == (0, 2) and ep.dispatch_backward(go, empty).shape == (0, 16)
