@@ -24,6 +24,7 @@
 // but the instructions per token -- about 1000 with a bias and groups, most of
 // them the fp64 scores and the K maxima -- and, in a decode batch, their chain:
 // 7.0 us per launch at 128 tokens, 2 us of them the launch itself.
+#include "ep.h"
 #include "ep_internal.h"
 #include "ep_device.h"
 
@@ -416,120 +417,157 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(
 }
 
 // Gradient.  With c_k = scale * grad_weights[k] over the token's valid slots:
-//   softmax, not normalised:  d_i = p_i (c_i - sum_k c_k p_k), every expert;
+//   softmax, not normalised:  d_i = p_i (c_i - sum_k c_k p_k), every expert, c_i
+//                             the sum of the c of i's slots;
 //   softmax, normalised:      d_k = q_k (c_k - sum_j c_j q_j), q the softmax
 //                             over the slots;
 //   sigmoid, not normalised:  d_k = c_k s_k (1 - s_k);
 //   sigmoid, normalised:      d_k = q_k (c_k - sum_j c_j q_j) (1 - s_k),
 //                             q_k = s_k / sum_j s_j;
-// 0 for every other expert.  Slots of one token that name the same expert add
-// up in slot order.  Dynamic LDS: per token K expert ids (int), K values.
+// 0 for every other expert.
+//
+// Where one expert holds nearly all of the mass, c_k and the sum are nearly the
+// same number and their difference is rounding.  The shares add up to 1, so the
+// c may all be taken relative to that of the expert with the largest share, a:
+//   c_k - sum_j c_j q_j = (c_k - c_a) - sum_j q_j (c_j - c_a).
+// The large share then meets an exact 0, and what is left is off by at most
+// 2 + 2 / q_a roundings of sum_j q_j |c_k - c_j|.  All in fp64, rounded once to
+// the logits' type (to bf16 by way of fp32).
+// Dynamic LDS, per token: a value for every expert (double; the lanes' j-th
+// experts next to each other, so that their accesses meet no bank twice), then K
+// slots' values (double) and experts (int).
 template <typename LT, int VPL, int L>
 __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(
     const LT* __restrict__ logits, const int64_t* __restrict__ topk_idx,
     const float* __restrict__ grad_weights, int T, int E, int K, bool softmax, bool normalize,
     float scale, LT* __restrict__ grad_logits, bool vec) {
     constexpr int kTokens = kRouteThreads / L;
+    // slot k of a token belongs to lane k % L of its segment
+    constexpr int kRounds = L == 8 ? 1 : EP_MAX_TOPK / L;       // (K <= E <= 8 with 8 lanes)
     extern __shared__ EP_LDS_ALIGN unsigned char s_raw[];
     const int sl = threadIdx.x & (L - 1);
     const int tok = threadIdx.x / L;
     const int64_t t = (int64_t)blockIdx.x * kTokens + tok;
     const bool live = t < T;
-    int* s_idx = reinterpret_cast<int*>(s_raw) + tok * K;
-    float* s_val = reinterpret_cast<float*>(s_raw) + kTokens * K + tok * K;
+    double* s_expert = reinterpret_cast<double*>(s_raw) + tok * (VPL * L);
+    double* s_slot = reinterpret_cast<double*>(s_raw) + kTokens * (VPL * L) + tok * K;
+    int* s_idx =
+        reinterpret_cast<int*>(s_raw + (size_t)kTokens * (VPL * L + K) * 8) + tok * K;
 
     const int e0 = sl * VPL;
     const LT* row = logits + t * E;
     const bool dense = softmax && !normalize;
-    float p[VPL];
-    float m = -kFltMax;
-    float inv = 0.0f;
-    if (dense) {
-        if (live) {
-            load_row<VPL>(p, row, e0, E, vec);
-        } else {
+    float l[VPL];
+    if (dense && live) {
+        load_row<VPL>(l, row, e0, E, vec);
+    } else {
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) p[j] = -INFINITY;
-        }
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-            p[j] = clean_logit(p[j]);
-            m = fmaxf(m, p[j]);
-        }
-        m = seg_max<L>(m);
-        float a = 0.0f;
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-            p[j] = expf(p[j] - m);
-            a += p[j];
-        }
-        a = seg_sum<L>(a);
-        inv = a > 0.0f ? 1.0f / a : 0.0f;
+        for (int j = 0; j < VPL; ++j) l[j] = -INFINITY;
     }
+    int e[kRounds];
+    double c[kRounds];
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+        const int k = sl + i * L;
+        const bool held = live && k < K;
+        const int64_t e64 = held ? topk_idx[t * K + k] : -1;
+        e[i] = e64 >= 0 && e64 < E ? (int)e64 : -1;
+        c[i] = e[i] >= 0 ? (double)scale * (double)grad_weights[t * K + k] : 0.0;
+        if (k < K) s_idx[k] = e[i];
+    }
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) s_expert[j * L + sl] = 0.0;
 
-    if (normalize && softmax) {
-        for (int k = sl; k < K; k += L) {
-            const int64_t e = live ? topk_idx[t * K + k] : -1;
-            if (e >= 0 && e < E) m = fmaxf(m, clean_logit(load_logit(row + e)));
+    if (!dense) {
+        // c becomes the slot's gradient
+        float v[kRounds];
+        double u[kRounds];
+        float m = -kFltMax;
+#pragma unroll
+        for (int i = 0; i < kRounds; ++i) {
+            v[i] = e[i] >= 0 ? clean_logit(load_logit(row + e[i])) : -INFINITY;
+            m = fmaxf(m, v[i]);
         }
-        m = seg_max<L>(m);
-    }
-    // sums over the slots: of the unnormalised shares v, and of c * v
-    double sv = 0.0, scv = 0.0;
-    for (int k = sl; k < K; k += L) {
-        const int64_t e64 = live ? topk_idx[t * K + k] : -1;
-        const int e = e64 >= 0 && e64 < E ? (int)e64 : -1;
-        s_idx[k] = e;
-        if (e >= 0 && (dense || normalize)) {
-            const double v = (double)clean_logit(load_logit(row + e));
-            const double u = softmax ? exp(v - (double)m) : sigmoid64(v);
-            sv += u;
-            scv += u * (double)grad_weights[t * K + k];
+        double ca = 0.0, total = 1.0, mean = 0.0;
+        if (normalize) {
+            m = seg_max<L>(m);
+            ca = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kRounds; ++i) ca = larger(ca, v[i] == m ? c[i] : -INFINITY);
+            ca = seg_max<L>(ca);
+            ca = ca > -INFINITY ? ca : 0.0;
+            total = 0.0;
         }
-    }
-    sv = seg_sum<L>(sv);
-    scv = seg_sum<L>(scv) * (double)scale;
-    const double norm = dense ? (double)inv : (sv > 0.0 ? 1.0 / sv : 0.0);
-    const double mean = scv * norm;                 // sum_k c_k times the share of k
-    for (int k = sl; k < K; k += L) {
-        const int e = s_idx[k];
-        double d = 0.0;
-        if (e >= 0) {
-            const double c = (double)scale * (double)grad_weights[t * K + k];
-            if (dense) {
-                d = c;
-            } else {
-                const double v = (double)clean_logit(load_logit(row + e));
-                if (softmax) {
-                    d = exp(v - (double)m) * norm * (c - mean);
-                } else {
-                    const double s = sigmoid64(v);
-                    d = normalize ? s * norm * (c - mean) : c * s;
-                    d *= sigmoid64(-v);
-                }
+#pragma unroll
+        for (int i = 0; i < kRounds; ++i) {
+            u[i] = 0.0;
+            if (e[i] >= 0)
+                u[i] = softmax ? exp((double)v[i] - (double)m) : sigmoid64((double)v[i]);
+            c[i] -= ca;
+            if (normalize) {
+                total += u[i];
+                mean += u[i] * c[i];
             }
         }
-        s_val[k] = (float)d;
-    }
-    wave_sync();
-    float o[VPL];
+        if (normalize) {
+            total = seg_sum<L>(total);
+            mean = seg_sum<L>(mean);
+            mean = total > 0.0 ? mean / total : 0.0;
+        }
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) o[j] = 0.0f;
-    for (int k = 0; k < K; ++k) {
-        const int at = s_idx[k] - e0;
-        const float d = s_val[k];
-        if (at >= 0 && at < VPL) {
-#pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                if (j == at) o[j] += d;
+        for (int i = 0; i < kRounds; ++i) {
+            double d = total > 0.0 ? u[i] / total * (c[i] - mean) : 0.0;
+            if (!softmax && e[i] >= 0) d *= sigmoid64(-(double)v[i]);
+            c[i] = e[i] >= 0 ? d : 0.0;
         }
     }
-    if (dense) {
-        const float mf = (float)mean;
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) o[j] = p[j] * inv * (o[j] - mf);
+    for (int i = 0; i < kRounds; ++i)
+        if (sl + i * L < K) s_slot[sl + i * L] = c[i];
+    wave_sync();
+    // slots of one expert add up in slot order
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+        if (i * L >= K) break;
+        double v = 0.0;
+        for (int k = 0; k < K; ++k) v += s_idx[k] == e[i] ? s_slot[k] : 0.0;
+        if (e[i] >= 0) s_expert[e[i] % VPL * L + e[i] / VPL] = v;
     }
-    if (live) store_row<VPL>(o, grad_logits + t * E, e0, E, vec);
+    wave_sync();
+    double o[VPL];
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) o[j] = s_expert[j * L + sl];
+    if (dense) {
+        float m = -kFltMax;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            l[j] = clean_logit(l[j]);
+            m = fmaxf(m, l[j]);
+        }
+        m = seg_max<L>(m);
+        double ca = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) ca = larger(ca, l[j] == m ? o[j] : -INFINITY);
+        ca = seg_max<L>(ca);
+        ca = ca > -INFINITY ? ca : 0.0;
+        double p[VPL], total = 0.0, mean = 0.0;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            p[j] = exp((double)l[j] - (double)m);
+            o[j] -= ca;
+            total += p[j];
+            mean += p[j] * o[j];
+        }
+        total = seg_sum<L>(total);
+        const double inv = total > 0.0 ? 1.0 / total : 0.0;
+        mean = seg_sum<L>(mean) * inv;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) o[j] = p[j] * inv * (o[j] - mean);
+    }
+    float of[VPL];
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) of[j] = (float)o[j];
+    if (live) store_row<VPL>(of, grad_logits + t * E, e0, E, vec);
 }
 
 bool rows_vectorised(const void* p, size_t elem, int E) {
@@ -563,7 +601,7 @@ hipError_t launch_route_backward_l(const LT* logits, const int64_t* topk_idx, co
     const dim3 grid((unsigned)((T + kTokens - 1) / kTokens)), block(kRouteThreads);
     const bool vec = rows_vectorised(logits, sizeof(LT), E) &&
                      rows_vectorised(grad_logits, sizeof(LT), E);
-    const size_t lds = (size_t)kTokens * K * 8;
+    const size_t lds = (size_t)kTokens * (VPL * L * 8 + K * 12);
     hipLaunchKernelGGL((route_backward_kernel<LT, VPL, L>), grid, block, lds, s, logits, topk_idx,
                        gw, T, E, K, softmax, normalize, scale, grad_logits, vec);
     return hipGetLastError();

@@ -475,9 +475,10 @@ ep_status_t ep_route(const void *logits, ep_dtype_t logits_dtype, const float *e
  *   softmax, normalize:  d l_e = q_k * (c_k - sum_j c_j q_j), q = p / sum of the slots' p
  *   sigmoid:             d l_e = c_k * s_k * (1 - s_k)
  *   sigmoid, normalize:  d l_e = q_k * (c_k - sum_j c_j q_j) * (1 - s_k), q = s / sum of the slots' s
- * and 0 for every other expert; every element of grad_logits is written, in
- * logits' type, rounded once.  Slots of one token that name the same expert
- * add up.  The arguments are those of the ep_route call; topk_idx is its
+ * and 0 for every other expert; every element of grad_logits is written,
+ * computed in fp64 and rounded once to logits' type (to bf16 by way of fp32),
+ * and keeps its digits where one expert holds nearly all of the weight.  Slots
+ * of one token that name the same expert add up.  The arguments are those of the ep_route call; topk_idx is its
  * output, grad_weights fp32 [T*K].  No gradient reaches the bias.
  */
 ep_status_t ep_route_backward(const void *logits, ep_dtype_t logits_dtype,

@@ -1,0 +1,120 @@
+"""The router, its gradient, the gradients of combine and the experts' 4-bit
+products where results are small differences of large numbers, where inputs are
+large, and where the same numbers are summed by another variant of a kernel.
+"""
+import math
+from decimal import Decimal, getcontext
+
+import pytest
+import torch
+
+import operator_refs as ref
+from combine_ep_get_dispatch_amd import binding as ep
+from parity import announce
+
+pytestmark = pytest.mark.gpu
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+# ---------------------------------------------------------------------------
+# the router's gradient of confident tokens
+# ---------------------------------------------------------------------------
+
+def decimal_route_backward(logits, topk_idx, gw, score, normalize, scale):
+    """(gradient, size of what it is added up from) with 60 digits, from
+    d_i = share_i (c_i - sum of the shares' c) [(1 - s_i) for sigmoid scores];
+    size = share_i sum_j share_j |c_i - c_j|."""
+    getcontext().prec = 60
+    T, E = logits.shape
+    K = topk_idx.shape[1]
+    grad = torch.zeros((T, E), dtype=torch.float64)
+    size = torch.zeros((T, E), dtype=torch.float64)
+    for t in range(T):
+        l = [Decimal(float(v)) for v in logits[t]]
+        e = [int(i) for i in topk_idx[t]]
+        c = [Decimal(float(gw[t, k])) * Decimal(float(scale)) for k in range(K)]
+        sig = [1 / (1 + (-v).exp()) for v in l]
+        if score == "softmax" and not normalize:
+            u = [v.exp() for v in l]
+            total = sum(u)
+            ci = [sum((c[k] for k in range(K) if e[k] == i), Decimal(0)) for i in range(E)]
+            for i in range(E):
+                mean = sum(u[j] / total * ci[j] for j in set(e))
+                grad[t, i] = float(u[i] / total * (ci[i] - mean))
+                size[t, i] = float(u[i] / total * sum(u[j] / total * abs(ci[i] - ci[j])
+                                                      for j in range(E)))
+            continue
+        u = [l[i].exp() if score == "softmax" else sig[i] for i in e]
+        total = sum(u)
+        for k in range(K):
+            one = 1 - sig[e[k]] if score == "sigmoid" else Decimal(1)
+            if normalize:
+                mean = sum(u[j] / total * c[j] for j in range(K))
+                grad[t, e[k]] += float(u[k] / total * (c[k] - mean) * one)
+                size[t, e[k]] += float(u[k] / total * one * sum(u[j] / total * abs(c[k] - c[j])
+                                                               for j in range(K)))
+            else:
+                grad[t, e[k]] += float(c[k] * u[k] * one)
+                size[t, e[k]] += float(abs(c[k] * u[k] * one))
+    return grad, size
+
+
+@pytest.mark.parametrize("score,norm", [("softmax", False), ("softmax", True),
+                                        ("sigmoid", False), ("sigmoid", True)])
+@pytest.mark.parametrize("K", [1, 3])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("E,many", [(64, False), (256, False), (256, True)])
+def test_gradient_of_confident_tokens(score, norm, K, dtype, E, many):
+    """The top logit leads by 10 to 60: its expert's gradient is its share times
+    what the others hold, down to 1e-26 of c, and right relative to itself.
+
+    fp64 throughout: a share is off by exp's 2 units and the rounding of its
+    argument, at most 2^-53 * 128, and by at most 1100 additions, so each term
+    is off by less than 2^-42 of itself; taking the c relative to that of the
+    largest share, at least 1/256, adds 2 + 2 * 256 roundings of 2^-53 of the
+    size.  Together less than 2^-41 of the size.
+    Then one rounding to fp32, and for bf16 one more."""
+    announce("confident tokens E=%d K=%d %s %s %s many=%s" % (E, K, dtype, score, norm, many))
+    leads = [10.0, 15.0, 18.0, 20.0, 25.0, 30.0, 60.0]
+    T = len(leads)
+    l = torch.randn((T, E), generator=gen(E + K)) * 1.5
+    top = torch.randint(0, E, (T,), generator=gen(3))
+    for t, lead in enumerate(leads):
+        l[t, top[t]] = float(l[t].max()) + lead
+    if score == "sigmoid":
+        l -= 12.0                                 # shares that are far apart
+    l = l.to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    gw = torch.randn((T, K), generator=gen(K))
+    idx = l.float().sort(dim=1, descending=True, stable=True).indices[:, :K].contiguous()
+    # with a large batch a token has fewer lanes
+    n = 2100 // T + 1 if many else 1
+    got = ep.route_backward(l.repeat(n, 1).cuda(), idx.repeat(n, 1).cuda(), gw.repeat(n, 1).cuda(),
+                            score=score, normalize=norm, scale=2.5)
+    torch.cuda.synchronize()
+    want, size = decimal_route_backward(l, idx, gw, score, norm, 2.5)
+    tol = 2.0 ** -41 * size + ref.U32 * want.abs() * (1 + ref.UBF) + ref.TINY
+    if dtype == "bf16":
+        tol = tol + ref.UBF * want.abs()
+    got = got.cpu().double().view(n, T, E)
+    assert bool((got == got[0]).all())
+    off = (got[0] - want).abs()
+    assert bool((off <= tol).all()), "worst %.3g of the result" % float(
+        (off / want.abs().clamp(min=1e-37)).max())
+
+
+def test_gradient_of_repeated_and_tied_slots():
+    """Slots that name one expert together, and equal c: the sums are exact zeros
+    or the formula's, not what their roundings leave."""
+    l = torch.tensor([[30.0, 1.0, 0.0, -1.0], [4.0, 4.0, 4.0, 4.0], [25.0, 2.0, 1.0, 0.0]])
+    idx = torch.tensor([[0, 0, 1], [0, 1, 2], [0, 1, 0]])
+    gw = torch.tensor([[0.3, -0.7, 0.2], [0.25, 0.25, 0.25], [1e-3, 1e-3, 1e-3]])
+    for score, norm in (("softmax", False), ("softmax", True), ("sigmoid", True)):
+        got = ep.route_backward(l.cuda(), idx.cuda(), gw.cuda(), score=score, normalize=norm).cpu()
+        want, size = decimal_route_backward(l, idx, gw, score, norm, 1.0)
+        tol = 2.0 ** -41 * size + 2 * ref.U32 * want.abs() + ref.TINY
+        assert bool(((got.double() - want).abs() <= tol).all()), (score, norm)
+        if norm:
+            assert bool((got[1:] == 0).all()), (score, norm)
