@@ -118,3 +118,29 @@ def test_gradient_of_repeated_and_tied_slots():
         assert bool(((got.double() - want).abs() <= tol).all()), (score, norm)
         if norm:
             assert bool((got[1:] == 0).all()), (score, norm)
+
+
+@pytest.mark.parametrize("T,E,K,dtype", [(2100, 5, 2, "fp32"), (4097, 40, 40, "fp32"),
+                                         (2200, 100, 8, "bf16"), (3000, 160, 6, "bf16"),
+                                         (2049, 256, 8, "fp32"), (2100, 400, 64, "fp32"),
+                                         (2060, 512, 12, "bf16")])
+def test_softmax_weights_are_the_same_bits_in_batches_of_any_size(T, E, K, dtype):
+    """A token's softmax weights in a large batch (few lanes a token) and in
+    small ones (a wave a token), without normalisation: the same bits, and within
+    the roundings of the exponents' arguments (at most ln E half steps on average
+    over the shares), expf's (4) and the result's (1): their sum adds none."""
+    announce("softmax weights T=%d E=%d K=%d %s" % (T, E, K, dtype))
+    l = torch.randn((T, E), generator=gen(T + E)) * 3
+    l[::7, :: 3] = -math.inf
+    l[11] = -math.inf
+    l[12] += 30000.0
+    l = l.to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    idx, w = ep.route(l.cuda(), K, scale=2.5)
+    parts = [ep.route(p.cuda(), K, scale=2.5) for p in l.split(701)]
+    torch.cuda.synchronize()
+    assert torch.equal(idx, torch.cat([p[0] for p in parts]))
+    assert torch.equal(w, torch.cat([p[1] for p in parts]))
+    s = ref.scores(l, "softmax")
+    want = torch.where(idx.cpu() >= 0, s.gather(1, idx.cpu().clamp(min=0)), 0.0) * 2.5
+    tol = (math.log(E) + 4 + 1 + 1) * ref.U32 * want + ref.TINY
+    assert bool(((w.cpu().double() - want).abs() <= tol).all())
