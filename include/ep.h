@@ -516,7 +516,9 @@ ep_status_t ep_route_backward(const void *logits, ep_dtype_t logits_dtype,
  * E*capacity <= num_rows; num_rows < 2^31.  EP_ERR_UNSUPPORTED for
  * E > EP_MAX_EXPERTS, I > EP_MAX_EXPERT_IN or W * I/2 >= 2^31.  x and the scales are expected
  * finite, |x| < 2^119.  No workspace; the order of the sums is fixed by the
- * arguments' shapes.  (No page describes the experts themselves; format and
+ * arguments' shapes and, for E4M3 rows, by whether the row's expert has more
+ * than 16 rows: below and above, a row's result is the same bits whatever rows
+ * stand beside it, and for bf16 rows it always is.  (No page describes the experts themselves; format and
  * definition are this library's.)
  */
 ep_status_t ep_expert_linear_w4(const void *x, const float *x_scales, ep_dtype_t x_dtype,

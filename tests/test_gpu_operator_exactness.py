@@ -144,3 +144,59 @@ def test_softmax_weights_are_the_same_bits_in_batches_of_any_size(T, E, K, dtype
     want = torch.where(idx.cpu() >= 0, s.gather(1, idx.cpu().clamp(min=0)), 0.0) * 2.5
     tol = (math.log(E) + 4 + 1 + 1) * ref.U32 * want + ref.TINY
     assert bool(((w.cpu().double() - want).abs() <= tol).all())
+
+
+# ---------------------------------------------------------------------------
+# experts
+# ---------------------------------------------------------------------------
+
+def expert_inputs(R, I, N, G, fp8, zeros, swiglu, seed, mean=0.0):
+    """One expert's rows, weights, scales and zero points."""
+    g = gen(seed)
+    W = 2 * N if swiglu else N
+    x = torch.randn((R, I), generator=g) + mean
+    xs = None
+    if fp8:
+        a = x.view(R, I // 128, 128).abs().amax(2)
+        xs = a / 448.0
+        x = (x.view(R, I // 128, 128) * (448.0 / a)[..., None]).to(torch.float8_e4m3fn)
+        x = x.view(torch.uint8).view(R, I)
+    else:
+        x = x.bfloat16()
+    w = torch.randint(0, 256, (1, W, I // 2), dtype=torch.uint8, generator=g)
+    s = ((torch.rand((1, I // G, W), generator=g) + 0.5) * (0.3 / math.sqrt(I))).bfloat16()
+    z = torch.randint(0, 16, (1, I // G, W), dtype=torch.uint8, generator=g) if zeros else None
+    return x, xs, w, s, z
+
+
+def expert(x, xs, w, s, z, n, swiglu=False, out=None):
+    cu = lambda t: None if t is None else t.cuda()
+    return ep.expert_linear_w4(cu(x), cu(w), cu(s), torch.tensor([n], dtype=torch.int32).cuda(),
+                               capacity=x.shape[0], x_scales=cu(xs), zeros=cu(z), swiglu=swiglu,
+                               out=out)
+
+
+@pytest.mark.parametrize("fp8,G,zeros,swiglu", [
+    (True, 128, False, True), (True, 128, True, False), (True, 64, True, False),
+    (True, 32, False, False), (False, 128, False, False), (False, 128, True, True),
+    (False, 64, False, False), (False, 32, True, False)])
+@pytest.mark.parametrize("blocks", [1, 3, 4, 5, 7, 8, 9, 12, 13, 16, 56, 65, 77])
+def test_a_rows_bits_do_not_depend_on_the_rows_beside_it(fp8, G, zeros, swiglu, blocks):
+    """A row's result is the same bits however many rows stand beside it: of bf16
+    rows always, of E4M3 rows among experts of up to 16 rows and among larger
+    ones (whose blocks of input channels are added up in another order)."""
+    announce("bits by rows: fp8=%s G=%d blocks=%d" % (fp8, G, blocks))
+    R, N = 40, 40
+    args = expert_inputs(R, blocks * 128, N, G, fp8, zeros, swiglu, blocks)
+    full = expert(*args, R, swiglu).cpu()
+    want, err = ref.expert_linear(*args[:5], [(0, R)], N, swiglu)
+    off = (full.double() - want).abs()
+    assert bool((off <= err * (1 + ref.UBF) + ref.UBF * want.abs() + ref.TINY).all())
+    few = expert(*args, 16, swiglu).cpu()
+    assert bool(((few[:16].double() - want[:16]).abs() <= (err * (1 + ref.UBF) + ref.UBF * want.abs()
+                                                           + ref.TINY)[:16]).all())
+    for n in (1, 7, 16, 17, 32, 33):
+        part = expert(*args, n, swiglu).cpu()
+        assert torch.equal(part[:n], (few if n <= 16 else full)[:n]), n
+    if not fp8:
+        assert torch.equal(few[:16], full[:16])
