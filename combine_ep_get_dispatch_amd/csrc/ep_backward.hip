@@ -108,15 +108,22 @@ __device__ __forceinline__ void load_grad(float (&g)[8], const uint16_t* __restr
     unpack8(g, v);
 }
 
-// Workgroup of nw waves per token; wave i takes chunks i, i + nw, ...  The
-// waves' partial dot products of a group of KN slots meet in LDS and are added
-// in wave order.
+// The sums of a token's weight gradients, in both kernels: parts of the chunks
+// i, i + kBackwardParts, ..., added up channel by channel in a lane, then over
+// the lanes, then over the parts in order.
+constexpr int kBackwardParts = kBackwardMaxThreads / 64;
+__host__ __device__ __forceinline__ int num_parts(int nchunk) {
+    return nchunk < kBackwardParts ? nchunk : kBackwardParts;
+}
+
+// Workgroup of nw waves per token, a wave for each part.  The parts of a group
+// of KN slots meet in LDS.
 template <int KN>
 __global__ __launch_bounds__(kBackwardMaxThreads) void combine_backward_kernel(
     const uint16_t* __restrict__ gout, const uint16_t* __restrict__ y, int64_t nrows,
     const int32_t* __restrict__ dst_row, const float* __restrict__ w, int K, int H,
     uint16_t* __restrict__ gy, float* __restrict__ gw) {
-    __shared__ float s_part[kBackwardMaxThreads / 64][KN];
+    __shared__ float s_part[kBackwardParts][KN];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int nw = blockDim.x >> 6;
@@ -153,33 +160,35 @@ __global__ __launch_bounds__(kBackwardMaxThreads) void combine_backward_kernel(
 }
 
 // Large batches: a workgroup owns a tile of consecutive tokens and first reads
-// all their rows (dot products of every (token, chunk) to LDS), then writes all
+// all their rows (dot products of every (token, part) to LDS), then writes all
 // their gradient rows.  g is read again for the second phase, from a cache.
 template <int KN>
 __global__ __launch_bounds__(kBackwardTileThreads) void combine_backward_tile_kernel(
     const uint16_t* __restrict__ gout, const uint16_t* __restrict__ y, int64_t nrows,
     const int32_t* __restrict__ dst_row, const float* __restrict__ w, int T, int K, int H,
     int tile, uint16_t* __restrict__ gy, float* __restrict__ gw) {
-    extern __shared__ EP_LDS_ALIGN float s_dot[];       // [tile * nchunk][K]
+    extern __shared__ EP_LDS_ALIGN float s_dot[];       // [tile * parts][K]
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     constexpr int kWaves = kBackwardTileThreads / 64;
     const int64_t t0 = (int64_t)blockIdx.x * tile;
     const int nt = (int)min((int64_t)tile, T - t0);
     const int nchunk = (H + kCombineChunk - 1) / kCombineChunk;
-    const int ntask = nt * nchunk;
-    for (int task = wave; task < ntask; task += kWaves) {
-        const int tt = task / nchunk;
-        const int h0 = (task - tt * nchunk) * kCombineChunk + lane * 8;
-        const bool act = h0 < H;
+    const int npart = num_parts(nchunk);
+    for (int task = wave; task < nt * npart; task += kWaves) {
+        const int tt = task / npart;
         const Slots s = load_slots(dst_row, nullptr, nrows, t0 + tt, K);
-        float g[8];
-        load_grad(g, gout, t0 + tt, H, h0, act);
         for (int k0 = 0; k0 < K; k0 += KN) {
             float dot[KN];
 #pragma unroll
             for (int i = 0; i < KN; ++i) dot[i] = 0.0f;
-            dot_rows<KN>(dot, g, y, s, k0, H, h0, act);
+            for (int c = task - tt * npart; c < nchunk; c += kBackwardParts) {
+                const int h0 = c * kCombineChunk + lane * 8;
+                const bool act = h0 < H;
+                float g[8];
+                load_grad(g, gout, t0 + tt, H, h0, act);
+                dot_rows<KN>(dot, g, y, s, k0, H, h0, act);
+            }
 #pragma unroll
             for (int i = 0; i < KN; ++i) {
                 const float v = seg_sum<64>(dot[i]);
@@ -188,7 +197,7 @@ __global__ __launch_bounds__(kBackwardTileThreads) void combine_backward_tile_ke
         }
     }
     __syncthreads();
-    for (int task = wave; task < ntask; task += kWaves) {
+    for (int task = wave; task < nt * nchunk; task += kWaves) {
         const int tt = task / nchunk;
         const int h0 = (task - tt * nchunk) * kCombineChunk + lane * 8;
         const bool act = h0 < H;
@@ -200,7 +209,7 @@ __global__ __launch_bounds__(kBackwardTileThreads) void combine_backward_tile_ke
     for (int i = threadIdx.x; i < nt * K; i += kBackwardTileThreads) {
         const int tt = i / K, k = i - tt * K;
         float v = 0.0f;
-        for (int c = 0; c < nchunk; ++c) v += s_dot[(tt * nchunk + c) * K + k];
+        for (int c = 0; c < npart; ++c) v += s_dot[(tt * npart + c) * K + k];
         gw[t0 * K + i] = v;
     }
 }
@@ -211,20 +220,19 @@ hipError_t launch_backward_k(const uint16_t* gout, const uint16_t* y, int64_t nr
                              uint16_t* gy, float* gw, hipStream_t s) {
     const int nchunk = (H + kCombineChunk - 1) / kCombineChunk;
     // Tiles of as many slots as keep 8 per wave, while the batch still gives
-    // every CU of a 256-CU part two tiles, where both gradients are asked for
-    // and a tile's sums fit its LDS.
+    // every CU of a 256-CU part two tiles, where both gradients are asked for.
     int tile = kBackwardTileSlots / K;
     if (tile > T / kBackwardMinTiles) tile = T / kBackwardMinTiles;
-    const size_t lds = (size_t)tile * nchunk * K * sizeof(float);
+    const int npart = num_parts(nchunk);
+    const size_t lds = (size_t)tile * npart * K * sizeof(float);
     if (y && gy && gw && K >= kBackwardTileMinK && H >= kBackwardTileMinH &&
-        2 * tile * K >= kBackwardTileSlots && lds <= 64 * 1024) {
+        2 * tile * K >= kBackwardTileSlots) {
         hipLaunchKernelGGL(combine_backward_tile_kernel<KN>,
                            dim3((unsigned)(((int64_t)T + tile - 1) / tile)),
                            dim3(kBackwardTileThreads), lds, s, gout, y, nrows, dst_row, w, T, K, H,
                            tile, gy, gw);
     } else {
-        const int nw = nchunk < kBackwardMaxThreads / 64 ? nchunk : kBackwardMaxThreads / 64;
-        hipLaunchKernelGGL(combine_backward_kernel<KN>, dim3((unsigned)T), dim3(nw * 64), 0, s,
+        hipLaunchKernelGGL(combine_backward_kernel<KN>, dim3((unsigned)T), dim3(npart * 64), 0, s,
                            gout, y, nrows, dst_row, w, K, H, gy, gw);
     }
     return hipGetLastError();

@@ -200,3 +200,34 @@ def test_a_rows_bits_do_not_depend_on_the_rows_beside_it(fp8, G, zeros, swiglu, 
         assert torch.equal(part[:n], (few if n <= 16 else full)[:n]), n
     if not fp8:
         assert torch.equal(few[:16], full[:16])
+
+
+# ---------------------------------------------------------------------------
+# combine's gradient
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("T,H,K", [(2050, 4104, 8), (2100, 8192, 8), (1100, 8200, 17), (2048, 9224, 8),
+                                   (4100, 16896, 4), (520, 20000, 33), (600, 9224, 8)])
+def test_weight_gradients_are_the_same_bits_with_and_without_row_gradients(T, H, K):
+    """Large batches write both gradients in tiles, the weights' alone in a
+    workgroup per token: the sums are added up in the same order."""
+    announce("weight gradients T=%d H=%d K=%d" % (T, H, K))
+    g = torch.Generator(device="cuda").manual_seed(T)
+    go = torch.randn((T, H), device="cuda", generator=g).bfloat16()
+    R = 3000                                       # (every row once: T * K rows are much memory)
+    y = torch.randn((R, H), device="cuda", generator=g).bfloat16()
+    dst = torch.full((T * K,), -1, dtype=torch.int32)
+    at = torch.randperm(T * K, generator=gen(K))[:R]
+    dst[at] = torch.arange(R, dtype=torch.int32)
+    dst = dst.view(T, K).cuda()
+    w = torch.rand((T, K), device="cuda", generator=g)
+    _, both = ep.combine_backward(go, y, dst, w)
+    _, alone = ep.combine_backward(go, y, dst, None)
+    torch.cuda.synchronize()
+    assert torch.equal(both, alone)
+    ok = dst >= 0
+    t = ok.nonzero()[:, 0]
+    terms = go[t].double() * y[dst[ok].long()].double()
+    assert bool(((both[ok].double() - terms.sum(1)).abs()
+                 <= 64 * ref.U32 * terms.abs().sum(1) + ref.TINY).all())
+    assert bool((both[~ok] == 0).all())
