@@ -515,7 +515,9 @@ ep_status_t ep_route_backward(const void *logits, ep_dtype_t logits_dtype,
  * zeros 4-byte.  capacity is ignored with expert_offsets, else >= 1 with
  * E*capacity <= num_rows; num_rows < 2^31.  EP_ERR_UNSUPPORTED for
  * E > EP_MAX_EXPERTS, I > EP_MAX_EXPERT_IN or W * I/2 >= 2^31.  x and the scales are expected
- * finite, |x| < 2^119.  No workspace; the order of the sums is fixed by the
+ * finite, |x| < 2^113 (of E4M3 rows: x_scales < 2^104, which gives that), and
+ * 143 * sum over i of |x[r,i]| * s below fp32's largest value.  (Sums of bf16
+ * rows pass through 128 channels of up to 143 |x|.)  No workspace; the order of the sums is fixed by the
  * arguments' shapes and, for E4M3 rows, by whether the row's expert has more
  * than 16 rows: below and above, a row's result is the same bits whatever rows
  * stand beside it, and for bf16 rows it always is.  (No page describes the experts themselves; format and

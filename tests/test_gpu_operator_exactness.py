@@ -231,3 +231,64 @@ def test_weight_gradients_are_the_same_bits_with_and_without_row_gradients(T, H,
     assert bool(((both[ok].double() - terms.sum(1)).abs()
                  <= 64 * ref.U32 * terms.abs().sum(1) + ref.TINY).all())
     assert bool((both[~ok] == 0).all())
+
+
+# ---------------------------------------------------------------------------
+# experts: large rows, rows with a common mean
+# ---------------------------------------------------------------------------
+
+def close(got, want, err, what):
+    """Within the sums' bound and the result's one rounding; over the whole, a
+    rounding error is uniform, at most 2^-8 / sqrt(3) of the power of two below
+    the value, so 0.6 half steps of the 2-norm leave the sums 0.16 of them."""
+    got = got.cpu().double()
+    off = (got - want).abs()
+    bad = ~(off <= err * (1 + ref.UBF) + ref.UBF * want.abs() + ref.TINY)
+    assert not bool(bad.any()), "%s: %d of %d off" % (what, int(bad.sum()), bad.numel())
+    scale = float(want.abs().max())
+    if want.numel() >= 1000:
+        assert float((off / scale).norm()) <= 0.6 * ref.UBF * float((want / scale).norm()), what
+
+
+@pytest.mark.parametrize("G,zeros", [(32, False), (32, True), (64, True), (128, False), (128, True)])
+@pytest.mark.parametrize("n", [5, 20])
+def test_rows_of_one_sign_just_below_the_largest(G, zeros, n):
+    """bf16 rows of up to 2^113, all of one sign: a group's sums come up to
+    143 * 128 * 2^113 < 2^128 and stay finite."""
+    announce("large rows G=%d n=%d" % (G, n))
+    x, _, w, s, z = expert_inputs(20, 512, 64, G, False, zeros, False, G + n)
+    x = ((x.float().abs() / 8).clamp(0.5, 0.998) * 2.0 ** 112).bfloat16() * 2
+    x[1] = -x[1]
+    x[2] = 255 * 2.0 ** 105                          # the largest bf16 number below 2^113
+    s = (s.float() * 2.0 ** -20).bfloat16()
+    got = expert(x, None, w, s, z, n)
+    torch.cuda.synchronize()
+    assert float(x.float().abs().max()) < 2.0 ** 113
+    want, err = ref.expert_linear(x, None, w, s, z, [(0, n)], 64, False)
+    off = (got.cpu().double() - want).abs()[:n]
+    assert bool((off <= (err * (1 + ref.UBF) + ref.UBF * want.abs() + ref.TINY)[:n]).all())
+
+
+@pytest.mark.parametrize("G", [32, 128])
+def test_e4m3_rows_of_the_largest_scales(G):
+    announce("large E4M3 rows G=%d" % G)
+    n, I, N = 18, 512, 64
+    x, xs, w, s, z = expert_inputs(n, I, N, G, True, True, False, G)
+    x[0] = 0x7e                                      # 448 everywhere
+    xs = torch.full_like(xs, 2.0 ** 103)
+    s = (s.float() * 2.0 ** -20).bfloat16()
+    want, err = ref.expert_linear(x, xs, w, s, z, [(0, n)], N, False)
+    close(expert(x, xs, w, s, z, n), want, err, "y")
+
+
+@pytest.mark.parametrize("fp8,G,zeros", [(False, 128, False), (False, 128, True), (False, 32, True),
+                                         (True, 128, True), (True, 32, False)])
+@pytest.mark.parametrize("mean", [1.0, -30.0, 1000.0])
+@pytest.mark.parametrize("n", [10, 24])
+def test_rows_with_a_common_mean(fp8, G, zeros, mean, n):
+    """Rows far from zero: what the codes' offset adds and the zero points take
+    off again is then much larger than the result."""
+    announce("common mean %g fp8=%s G=%d n=%d" % (mean, fp8, G, n))
+    x, xs, w, s, z = expert_inputs(n, 2048, 128, G, fp8, zeros, False, G + n, mean)
+    want, err = ref.expert_linear(x, xs, w, s, z, [(0, n)], 128, False)
+    close(expert(x, xs, w, s, z, n), want, err, "y")
