@@ -292,3 +292,44 @@ def test_rows_with_a_common_mean(fp8, G, zeros, mean, n):
     x, xs, w, s, z = expert_inputs(n, 2048, 128, G, fp8, zeros, False, G + n, mean)
     want, err = ref.expert_linear(x, xs, w, s, z, [(0, n)], 128, False)
     close(expert(x, xs, w, s, z, n), want, err, "y")
+
+
+def e4m3_bound(x, xs, s, zeros, G):
+    """Bound on a row's E4M3 sums.  Of eight neighbouring channels the matrix
+    instruction cuts what lies below 2^-13 of the largest product's exponents'
+    power of two: with codes of up to 15 below 2^-10 of the largest |x|'s power,
+    which a code's last place reaches where |x| is under 2^-7 of that; in the
+    sum of x (by ones, times a zero point of up to 15) below 2^-13, reached
+    under 2^-10.  Then the eights' sums are added in fp32, in at most G / 8 + 8
+    steps a group at a full step of at most 30 |x| each, and the groups."""
+    R, I = x.shape
+    v = ref.e4m3_values()[x.long()].abs()
+    eight = v.view(R, I // 8, 8)
+    top = torch.exp2(torch.floor(torch.log2(eight.amax(2, keepdim=True).clamp(min=2.0 ** -6))))
+    # E4M3's last place stops at 2^-9: exponents below -6 count as -6
+    power = torch.exp2(torch.floor(torch.log2(eight.clamp(min=2.0 ** -6))))
+    cut = ((eight > 0) & (power < top * 2.0 ** -7)) * top * 2.0 ** -10
+    cut = cut + ((eight > 0) & (power < top * 2.0 ** -10)) * top * 2.0 ** -13 * 15
+    each = cut.view(R, I) + (G / 8 + 8) * 2 * ref.U32 * 30 * v
+    return (each * xs.double().repeat_interleave(128, 1)) @ \
+        s[0].t().double().repeat_interleave(G, 1).t().abs()
+
+
+@pytest.mark.parametrize("G,zeros", [(32, False), (32, True), (64, False), (128, False), (128, True)])
+@pytest.mark.parametrize("n", [1, 13, 30])
+@pytest.mark.parametrize("I", [128, 1024, 7168])
+@pytest.mark.parametrize("spread", [0.0, 2.0])
+def test_e4m3_sums_within_what_their_codes_leave(G, zeros, n, I, spread):
+    """E4M3 rows against a bound made for them; spread: channels of sizes far
+    apart, so that small codes stand beside large ones."""
+    announce("E4M3 bound G=%d n=%d I=%d spread=%g" % (G, n, I, spread))
+    N = 128
+    x, xs, w, s, z = expert_inputs(n, I, N, G, True, zeros, False, I + n)
+    if spread:
+        size = torch.exp(torch.randn((n, I), generator=gen(n)) * spread).clamp(max=40.0)
+        v = (ref.e4m3_values()[x.long()] * size / 40.0).float()
+        x = v.to(torch.float8_e4m3fn).view(torch.uint8)
+    want, _ = ref.expert_linear(x, xs, w, s, z, [(0, n)], N, False)
+    size = ref.e4m3_values()[x.long()].abs() * xs.double().repeat_interleave(128, 1)
+    groups = (I / G + 64) * ref.U32 * 15 * size @ s[0].t().double().repeat_interleave(G, 1).t()
+    close(expert(x, xs, w, s, z, n), want, e4m3_bound(x, xs, s, z, G) + groups, "y")
