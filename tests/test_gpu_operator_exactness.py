@@ -333,3 +333,21 @@ def test_e4m3_sums_within_what_their_codes_leave(G, zeros, n, I, spread):
     size = ref.e4m3_values()[x.long()].abs() * xs.double().repeat_interleave(128, 1)
     groups = (I / G + 64) * ref.U32 * 15 * size @ s[0].t().double().repeat_interleave(G, 1).t()
     close(expert(x, xs, w, s, z, n), want, e4m3_bound(x, xs, s, z, G) + groups, "y")
+
+
+# ---------------------------------------------------------------------------
+# the binding's checks of GPU tensors
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("name", ["gradients", "routers", "experts"])
+def test_binding_refuses_wrong_gpu_tensors(name, monkeypatch):
+    """The refusals of test_operators_cpu.py with tensors on the GPU, which the
+    checks' short way looks at first; nothing is launched."""
+    import test_operators_cpu as cpu
+
+    def called(name, *args):
+        raise AssertionError("the binding called %s" % name)
+    monkeypatch.setattr(ep, "_launch", called)
+    monkeypatch.setattr(ep, "_is_gpu", lambda t: True)      # (of tensors elsewhere: "must be on")
+    with torch.device("cuda"):
+        getattr(cpu, "test_binding_refuses_what_is_wrong_with_the_%s_tensors" % name)(None)

@@ -235,3 +235,124 @@ def test_e4m3_values_are_the_formats():
     v = ref.e4m3_values()
     t = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
     assert torch.equal(torch.nan_to_num(v, nan=1e9), torch.nan_to_num(t, nan=1e9))
+
+
+@pytest.fixture
+def no_call(monkeypatch):
+    """CPU tensors stand in for GPU ones; a call that passes the checks fails
+    the test, on a machine with a GPU and a loaded library too."""
+    def called(name, *args):
+        raise AssertionError("the binding called %s before rejecting its arguments" % name)
+    monkeypatch.setattr(b, "_is_gpu", lambda t: True)
+    monkeypatch.setattr(b, "_launch", called)
+
+
+def refused(why, fn, *args, **kw):
+    with pytest.raises((ValueError, TypeError), match=why):
+        fn(*args, **kw)
+
+
+def test_binding_refuses_what_is_wrong_with_the_gradients_tensors(no_call):
+    T, K, H, R = 4, 2, 16, 8
+    bf = torch.bfloat16
+    go, y = torch.zeros((T, H), dtype=bf), torch.zeros((R, H), dtype=bf)
+    dst, w = torch.zeros((T, K), dtype=torch.int32), torch.zeros((T, K))
+    gy, gw = torch.zeros((R, H), dtype=bf), torch.zeros((T, K))
+    cb = b.combine_backward
+    with pytest.raises(AssertionError, match="ep_combine_backward"):
+        cb(go, y, dst, w, out=(gy, gw))                  # nothing wrong: it is called
+    refused("grad_out must have shape", cb, go[:2], y, dst, w)
+    refused("grad_out must be torch.bfloat16", cb, go.float(), y, dst, w)
+    refused("y must have shape", cb, go, y[:, :8].contiguous(), dst, w)
+    refused("y must be contiguous", cb, go, torch.zeros((R, 2 * H), dtype=bf)[:, ::2], dst, w)
+    refused("y must be on", cb, go, y.to("meta"), dst, w)
+    refused("dst_row must be torch.int32", cb, go, y, dst.long(), w)
+    refused("dst_row must be on", cb, go, y, dst.to("meta"), w)
+    refused("topk_weights must be torch.float32", cb, go, y, dst, w.double())
+    refused("topk_weights must have shape", cb, go, y, dst, w[:2])
+    refused("grad_y must have shape", cb, go, y, dst, w, out=(gy[:4], gw))
+    refused("grad_y must be contiguous", cb, go, y, dst, w,
+            out=(gy.t().contiguous().t(), gw))
+    refused("grad_weights must have shape", cb, go, y, dst, w, out=(gy, gw[:2]))
+    refused("needs y or topk_weights", cb, go, None, dst, None)
+    refused("needs num_rows", cb, go, None, dst, w)
+    refused("grad_weights needs y", cb, go, None, dst, w, out=(gy, gw))
+    refused("grad_y needs topk_weights", cb, go, y, dst, None, out=(gy, gw))
+    db = b.dispatch_backward
+    with pytest.raises(AssertionError, match="ep_dispatch_backward"):
+        db(y, dst, out=go)
+    refused("dst_row must be torch.int32", db, y, dst.long())
+    refused("grad_recv_x must be torch.bfloat16", db, y.float(), dst)
+    refused("grad_recv_x must be .R, H.", db, y[:, 0], dst)
+    refused("grad_recv_x must be contiguous", db, y.t(), dst)
+    refused("out must have shape", db, y, dst, out=go[:2])
+    refused("out must be on", db, y, dst, out=go.to("meta"))
+
+
+def test_binding_refuses_what_is_wrong_with_the_routers_tensors(no_call):
+    T, E, K = 4, 16, 2
+    lg = torch.zeros((T, E))
+    idx, w = torch.zeros((T, K), dtype=torch.int64), torch.zeros((T, K))
+    with pytest.raises(AssertionError, match="ep_route"):
+        b.route(lg, K, expert_bias=torch.zeros(E), out=(idx, w))
+    for bad in (lg.double(), lg.half()):
+        refused("logits must be float32 or bfloat16", b.route, bad, K)
+        refused("logits must be float32 or bfloat16", b.route_backward, bad, idx, w)
+    refused("logits must be .T, E.", b.route, lg[0], K)
+    refused("logits must be contiguous", b.route, lg.t(), K)
+    refused("logits must be contiguous", b.route, lg[:, ::2], K)
+    refused("expert_bias must have shape", b.route, lg, K, expert_bias=torch.zeros(E - 1))
+    refused("expert_bias must be torch.float32", b.route, lg, K, expert_bias=torch.zeros(E).double())
+    refused("expert_bias must be on", b.route, lg, K, expert_bias=torch.zeros(E, device="meta"))
+    refused("score must be one of", b.route, lg, K, score="relu")
+    refused("topk_idx must be torch.int64", b.route, lg, K, out=(idx.int(), w))
+    refused("topk_weights must have shape", b.route, lg, K, out=(idx, w[:, :1].contiguous()))
+    with pytest.raises(AssertionError, match="ep_route_backward"):
+        b.route_backward(lg, idx, w, out=torch.zeros_like(lg))
+    refused("topk_idx must be torch.int64", b.route_backward, lg, idx.int(), w)
+    refused("topk_idx must have shape", b.route_backward, lg, idx[:3], w[:3])
+    refused("topk_idx must be .T, K.", b.route_backward, lg, idx[:, 0], w)
+    refused("grad_weights must have shape", b.route_backward, lg, idx, w[:2])
+    refused("grad_weights must be on", b.route_backward, lg, idx, w.to("meta"))
+    refused("score must be one of", b.route_backward, lg, idx, w, score="max")
+    refused("out must be torch.float32", b.route_backward, lg, idx, w, out=lg.bfloat16())
+
+
+def test_binding_refuses_what_is_wrong_with_the_experts_tensors(no_call):
+    E, C, I, N, G = 3, 4, 256, 16, 64
+    x = torch.zeros((E * C, I), dtype=torch.bfloat16)
+    q = torch.zeros((E * C, I), dtype=torch.uint8)
+    xs = torch.zeros((E * C, I // 128))
+    w = torch.zeros((E, N, I // 2), dtype=torch.uint8)
+    s = torch.zeros((E, I // G, N), dtype=torch.bfloat16)
+    z = torch.zeros((E, I // G, N), dtype=torch.uint8)
+    cnt = torch.zeros(E, dtype=torch.int32)
+    off = torch.zeros(E + 1, dtype=torch.int32)
+    y = torch.zeros((E * C, N), dtype=torch.bfloat16)
+    fn = b.expert_linear_w4
+    for a, kw in (((x, w, s, cnt), dict(capacity=C, zeros=z)),
+                  ((q, w, s, cnt), dict(expert_offsets=off, x_scales=xs))):
+        with pytest.raises(AssertionError, match="ep_expert_linear_w4"):
+            fn(*a, out=y, **kw)
+    refused("x must be torch.bfloat16", fn, x.float(), w, s, cnt, capacity=C)
+    refused("codes need x_scales", fn, q, w, s, cnt, capacity=C)
+    refused("x_scales must have shape", fn, q, w, s, cnt, capacity=C, x_scales=xs[:, :1].contiguous())
+    refused("x_scales must be torch.float32", fn, q, w, s, cnt, capacity=C, x_scales=xs.bfloat16())
+    refused("x_scales belong to E4M3", fn, x, w, s, cnt, capacity=C, x_scales=xs)
+    refused("weight must have shape", fn, x, w[:, :, :64].contiguous(), s, cnt, capacity=C)
+    refused("weight must be contiguous", fn, x, w.transpose(1, 2).contiguous().transpose(1, 2), s, cnt,
+            capacity=C)
+    refused("weight .E, W, I/2.", fn, x, w[0], s, cnt, capacity=C)
+    refused("weight must be on", fn, x, w.to("meta"), s, cnt, capacity=C)
+    refused("I/G groups", fn, x, w, s[:, :3].contiguous(), cnt, capacity=C)
+    refused("scales must be torch.bfloat16", fn, x, w, s.float(), cnt, capacity=C)
+    refused("scales must have shape", fn, x, w, s[:2], cnt, capacity=C)
+    refused("zeros must be torch.uint8", fn, x, w, s, cnt, capacity=C, zeros=z.int())
+    refused("zeros must have shape", fn, x, w, s, cnt, capacity=C, zeros=z[:, :2].contiguous())
+    refused("num_tokens_per_expert must be torch.int32", fn, x, w, s, cnt.long(), capacity=C)
+    refused("num_tokens_per_expert must have shape", fn, x, w, s, cnt[:2], capacity=C)
+    refused("expert_offsets or capacity", fn, x, w, s, cnt, capacity=C, expert_offsets=off)
+    refused("expert_offsets must have shape", fn, x, w, s, cnt, expert_offsets=off[:E])
+    refused("out must have shape", fn, x, w, s, cnt, capacity=C, out=x)
+    refused("even number of weight channels", fn, x, w[:, :15].contiguous(), s[:, :, :15].contiguous(),
+            cnt, capacity=C, swiglu=True)
