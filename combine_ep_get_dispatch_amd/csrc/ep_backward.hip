@@ -238,12 +238,9 @@ hipError_t launch_backward_k(const uint16_t* gout, const uint16_t* y, int64_t nr
     return hipGetLastError();
 }
 
-}  // namespace
-
-hipError_t launch_combine_backward(const uint16_t* gout, const uint16_t* y, int64_t nrows,
-                                   const int32_t* dst_row, const float* w, int T, int K, int H,
-                                   uint16_t* gy, float* gw, hipStream_t s) {
-    if (T == 0) return hipSuccess;
+hipError_t launch_slice(const uint16_t* gout, const uint16_t* y, int64_t nrows,
+                        const int32_t* dst_row, const float* w, int T, int K, int H, uint16_t* gy,
+                        float* gw, hipStream_t s) {
 #define EP_B_ARGS gout, y, nrows, dst_row, w, T, K, H, gy, gw, s
     switch (K) {
         case 1: return launch_backward_k<1>(EP_B_ARGS);
@@ -253,6 +250,22 @@ hipError_t launch_combine_backward(const uint16_t* gout, const uint16_t* y, int6
         default: return launch_backward_k<8>(EP_B_ARGS);
     }
 #undef EP_B_ARGS
+}
+
+}  // namespace
+
+hipError_t launch_combine_backward(const uint16_t* gout, const uint16_t* y, int64_t nrows,
+                                   const int32_t* dst_row, const float* w, int T, int K, int H,
+                                   uint16_t* gy, float* gw, hipStream_t s) {
+    const int64_t slice = max_launch_tokens(kBackwardMaxThreads);
+    for (int64_t t = 0; t < T; t += slice) {
+        const int n = (int)(T - t < slice ? T - t : slice);
+        const hipError_t e = launch_slice(gout + t * H, y, nrows, dst_row + t * K,
+                                          w ? w + t * K : nullptr, n, K, H, gy,
+                                          gw ? gw + t * K : nullptr, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace ep

@@ -210,12 +210,9 @@ hipError_t launch_k(dim3 grid, bool budget, hipStream_t s, const uint16_t* y, in
     return hipGetLastError();
 }
 
-}  // namespace
-
-hipError_t launch_combine(const uint16_t* y, int64_t nrows, const int32_t* dst_row,
-                          const float* w, int T, int K, int H, uint16_t* out, int num_cus,
-                          hipStream_t s) {
-    if (T == 0) return hipSuccess;
+hipError_t launch_slice(const uint16_t* y, int64_t nrows, const int32_t* dst_row,
+                        const float* w, int T, int K, int H, uint16_t* out, int num_cus,
+                        hipStream_t s) {
     const int nchunk = (H + kCombineChunk - 1) / kCombineChunk;
     const int64_t ntask = (int64_t)T * nchunk;
     int64_t nblk = (ntask + kCombineThreads / 64 - 1) / (kCombineThreads / 64);
@@ -245,6 +242,22 @@ hipError_t launch_combine(const uint16_t* y, int64_t nrows, const int32_t* dst_r
         default: return launch_k<0>(EP_C_ARGS);
     }
 #undef EP_C_ARGS
+}
+
+}  // namespace
+
+hipError_t launch_combine(const uint16_t* y, int64_t nrows, const int32_t* dst_row,
+                          const float* w, int T, int K, int H, uint16_t* out, int num_cus,
+                          hipStream_t s) {
+    const int64_t slice = max_launch_tokens((H + kCombineChunk - 1) / kCombineChunk *
+                                            kCombineThreads);
+    for (int64_t t = 0; t < T; t += slice) {
+        const int n = (int)(T - t < slice ? T - t : slice);
+        const hipError_t e = launch_slice(y, nrows, dst_row + t * K, w ? w + t * K : nullptr, n, K,
+                                          H, out + t * H, num_cus, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace ep

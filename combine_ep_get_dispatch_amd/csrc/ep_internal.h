@@ -211,6 +211,13 @@ hipError_t launch_dispatch_dedup(const uint16_t* x, const int64_t* idx, int T, i
                                  int32_t* recv_src, int32_t* recv_topk_idx, int32_t* slot_src,
                                  int32_t* dst_row, hipStream_t s);
 
+// A launch holds fewer than 2^32 threads.  Tokens of one launch where a token
+// takes up to `threads` of them; larger batches are launched in slices.
+inline int64_t max_launch_tokens(int64_t threads) {
+    const int64_t n = ((int64_t)1 << 31) / threads;
+    return n > 0 ? n : 1;
+}
+
 // ---------------------------------------------------------------- combine ---
 // One wave per (token, 512-channel chunk); 8 channels per lane; two waves per
 // workgroup (measured ~3% faster than 4 or 8 and slightly faster than 1).

@@ -652,21 +652,37 @@ hipError_t route_backward_any(const void* logits, const int64_t* topk_idx, const
 hipError_t launch_route(const void* logits, bool bf16, const float* bias, int T, int E, int K,
                         bool softmax, int NG, int TG, bool normalize, float scale,
                         int64_t* topk_idx, float* topk_weights, hipStream_t s) {
-    if (T == 0) return hipSuccess;
-    return bf16 ? route_any<uint16_t>(logits, bias, T, E, K, softmax, NG, TG, normalize, scale,
-                                      topk_idx, topk_weights, s)
-                : route_any<float>(logits, bias, T, E, K, softmax, NG, TG, normalize, scale,
-                                   topk_idx, topk_weights, s);
+    const int64_t slice = max_launch_tokens(64);
+    for (int64_t t = 0; t < T; t += slice) {
+        const int n = (int)(T - t < slice ? T - t : slice);
+        const void* l = static_cast<const char*>(logits) + t * E * (bf16 ? 2 : 4);
+        const hipError_t e =
+            bf16 ? route_any<uint16_t>(l, bias, n, E, K, softmax, NG, TG, normalize, scale,
+                                       topk_idx + t * K, topk_weights + t * K, s)
+                 : route_any<float>(l, bias, n, E, K, softmax, NG, TG, normalize, scale,
+                                    topk_idx + t * K, topk_weights + t * K, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_route_backward(const void* logits, bool bf16, const int64_t* topk_idx,
                                  const float* gw, int T, int E, int K, bool softmax,
                                  bool normalize, float scale, void* grad_logits, hipStream_t s) {
-    if (T == 0) return hipSuccess;
-    return bf16 ? route_backward_any<uint16_t>(logits, topk_idx, gw, T, E, K, softmax, normalize,
-                                               scale, grad_logits, s)
-                : route_backward_any<float>(logits, topk_idx, gw, T, E, K, softmax, normalize,
-                                            scale, grad_logits, s);
+    const int64_t slice = max_launch_tokens(64);
+    for (int64_t t = 0; t < T; t += slice) {
+        const int n = (int)(T - t < slice ? T - t : slice);
+        const int64_t at = t * E * (bf16 ? 2 : 4);
+        const void* l = static_cast<const char*>(logits) + at;
+        void* g = static_cast<char*>(grad_logits) + at;
+        const hipError_t e =
+            bf16 ? route_backward_any<uint16_t>(l, topk_idx + t * K, gw + t * K, n, E, K, softmax,
+                                                normalize, scale, g, s)
+                 : route_backward_any<float>(l, topk_idx + t * K, gw + t * K, n, E, K, softmax,
+                                             normalize, scale, g, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace ep

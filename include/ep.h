@@ -82,6 +82,7 @@ typedef enum EP_ENUM_BASE {
 #define EP_LL_MAX_SLOTS 8192   /* T*K of one ep_low_latency_dispatch call */
 #define EP_MAX_EXPERT_ALIGNMENT 1024   /* of ep_layout_dispatch_aligned */
 #define EP_STATIC_SCRATCH_BYTES (8u << 20)   /* per GPU, of ep_layout_dispatch_static */
+#define EP_MAX_GRAD_HIDDEN (1 << 30)   /* hidden of the gradients of combine and dispatch */
 #define EP_MAX_ROUTE_GROUPS 64   /* expert groups of ep_route */
 #define EP_MAX_EXPERT_IN (1 << 24)   /* input channels of ep_expert_linear_w4 */
 
@@ -408,7 +409,7 @@ ep_status_t ep_combine_cu(const void *y, int64_t num_rows, const int32_t *dst_ro
  * Types, shapes, limits and errors as ep_combine: grad_out bf16 [T*H], y and
  * grad_y bf16 [num_rows*H],
  * topk_weights and grad_weights fp32 [T*K]; grad_out, y and grad_y 16-byte
- * aligned.  T may be 0.
+ * aligned.  T may be 0.  EP_ERR_UNSUPPORTED for H > EP_MAX_GRAD_HIDDEN too.
  */
 ep_status_t ep_combine_backward(const void *grad_out, const void *y, int64_t num_rows,
                                 const int32_t *dst_row, const float *topk_weights,
@@ -425,7 +426,8 @@ ep_status_t ep_combine_backward(const void *grad_out, const void *y, int64_t num
  * like the receive rows (of any dispatch form; for the de-duplicated one like
  * the expert-major rows that dst_row names), the gradient with respect to the
  * values the rows stand for: an FP8 dispatch passes it straight through its
- * quantiser.  Types, shapes, limits and errors as ep_combine without weights.
+ * quantiser.  Types, shapes, limits and errors as ep_combine without weights;
+ * EP_ERR_UNSUPPORTED for H > EP_MAX_GRAD_HIDDEN too.
  */
 ep_status_t ep_dispatch_backward(const void *grad_recv_x, int64_t num_rows,
                                  const int32_t *dst_row, int32_t num_tokens, int32_t num_topk,
@@ -459,7 +461,7 @@ ep_status_t ep_dispatch_backward(const void *grad_recv_x, int64_t num_rows,
  * fp32 [T*K].  E % num_groups == 0, 1 <= topk_groups <= num_groups,
  * K <= topk_groups * (E / num_groups); scale finite.  EP_ERR_UNSUPPORTED for
  * E > EP_MAX_EXPERTS, K > EP_MAX_TOPK or num_groups > EP_MAX_ROUTE_GROUPS.
- * One launch, no workspace.  T may be 0.
+ * One launch (one per 2^25 tokens), no workspace.  T may be 0.
  */
 ep_status_t ep_route(const void *logits, ep_dtype_t logits_dtype, const float *expert_bias,
                      int32_t num_tokens, int32_t num_experts, int32_t num_topk,

@@ -351,3 +351,54 @@ def test_binding_refuses_wrong_gpu_tensors(name, monkeypatch):
     monkeypatch.setattr(ep, "_is_gpu", lambda t: True)      # (of tensors elsewhere: "must be on")
     with torch.device("cuda"):
         getattr(cpu, "test_binding_refuses_what_is_wrong_with_the_%s_tensors" % name)(None)
+
+
+# ---------------------------------------------------------------------------
+# batches of more threads than one launch holds
+# ---------------------------------------------------------------------------
+
+def test_gradients_of_more_tokens_than_one_launch_holds():
+    """2^26 and a few tokens of 8 channels: a wave for each of them would be more
+    than the 2^32 threads of a launch."""
+    T, H = (1 << 26) + 5, 8
+    announce("gradients of %d tokens" % T)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    go = torch.randint(-8, 9, (T, H), device="cuda", generator=g, dtype=torch.int8).bfloat16()
+    y = torch.randint(-8, 9, (T, H), device="cuda", generator=g, dtype=torch.int8).bfloat16()
+    w = torch.randint(-4, 5, (T, 1), device="cuda", generator=g, dtype=torch.int8).float()
+    dst = torch.arange(T - 1, -1, -1, dtype=torch.int32, device="cuda").view(T, 1)
+    gy, gw = ep.combine_backward(go, y, dst, w)
+    for a in range(0, T, 1 << 24):                  # (small whole numbers: every sum is exact)
+        b = min(a + (1 << 24), T)
+        rows = y[T - b:T - a].flip(0).float()
+        assert torch.equal(gw[a:b, 0], (rows * go[a:b].float()).sum(1)), a
+        assert torch.equal(gy[T - b:T - a].flip(0).float(), go[a:b].float() * w[a:b]), a
+    del gy, gw
+    gx = ep.dispatch_backward(y, dst)
+    assert torch.equal(gx, y.flip(0))
+    del gx
+    out = ep.combine(y, dst, w)
+    assert torch.equal(out, (y.flip(0).float() * w).bfloat16())
+
+
+def test_router_of_more_tokens_than_one_launch_holds():
+    """2^29 and a few tokens of one expert, of 8 lanes each."""
+    T = (1 << 29) + 5
+    announce("router of %d tokens" % T)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    l = torch.randn((T, 1), device="cuda", generator=g, dtype=torch.bfloat16)
+    l[::1000003] = -math.inf
+    idx, w = ep.route(l, 1, score="sigmoid")
+    step = 1 << 26
+    for a in range(0, T, step):
+        p = l[a:a + step].double()
+        assert torch.equal(idx[a:a + step], torch.where(p > -math.inf, 0, -1)), a
+        want = torch.sigmoid(p)
+        assert bool(((w[a:a + step].double() - want).abs() <= 2 * ref.U32 * want).all()), a
+    gl = ep.route_backward(l, idx, w, score="sigmoid")
+    for a in range(0, T, step):
+        p = l[a:a + step].double()
+        want = w[a:a + step].double() * torch.sigmoid(p) * torch.sigmoid(-p)
+        want = torch.where(p > -math.inf, want, 0.0)
+        off = (gl[a:a + step].double() - want).abs()
+        assert bool((off <= (ref.UBF + 2 * ref.U32) * want.abs()).all()), a

@@ -356,3 +356,11 @@ def test_binding_refuses_what_is_wrong_with_the_experts_tensors(no_call):
     refused("out must have shape", fn, x, w, s, cnt, capacity=C, out=x)
     refused("even number of weight channels", fn, x, w[:, :15].contiguous(), s[:, :, :15].contiguous(),
             cnt, capacity=C, swiglu=True)
+
+
+def test_gradients_reject_rows_past_the_largest(buf):
+    L = b.lib()
+    go, y, dst, w, gy, gw = (buf() for _ in range(6))
+    for H in ((1 << 30) + 8, 2**31 - 8):
+        assert L.ep_combine_backward(go, y, 1, dst, w, 1, 1, H, gy, gw, None) == UNSUPPORTED
+        assert L.ep_dispatch_backward(go, 1, dst, 1, 1, H, gy, None) == UNSUPPORTED
