@@ -82,7 +82,7 @@ typedef enum EP_ENUM_BASE {
 #define EP_LL_MAX_SLOTS 8192   /* T*K of one ep_low_latency_dispatch call */
 #define EP_MAX_EXPERT_ALIGNMENT 1024   /* of ep_layout_dispatch_aligned */
 #define EP_STATIC_SCRATCH_BYTES (8u << 20)   /* per GPU, of ep_layout_dispatch_static */
-#define EP_MAX_GRAD_HIDDEN (1 << 30)   /* hidden of the gradients of combine and dispatch */
+#define EP_MAX_GRAD_HIDDEN 0x7ffffe00   /* hidden of the gradients of combine and dispatch */
 #define EP_MAX_ROUTE_GROUPS 64   /* expert groups of ep_route */
 #define EP_MAX_EXPERT_IN (1 << 24)   /* input channels of ep_expert_linear_w4 */
 
