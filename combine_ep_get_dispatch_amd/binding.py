@@ -581,6 +581,12 @@ def combine(y: torch.Tensor, dst_row: torch.Tensor, topk_weights: torch.Tensor,
 # gradients of dispatch and combine
 # ---------------------------------------------------------------------------
 
+def _sizes(bits: int):
+    """Refuse sizes (joined by |) that the library's 32-bit arguments would cut."""
+    if bits >> 31 not in (0, -1):
+        raise ValueError("sizes must be below 2^31")
+
+
 def _launch(name: str, t: torch.Tensor, *args):
     """Call ``name`` with ``args`` and torch's current stream on t's device,
     with that device current."""
@@ -608,6 +614,7 @@ def combine_backward(grad_out: torch.Tensor, y: torch.Tensor | None, dst_row: to
         raise ValueError("grad_out must be [T, H], y [R, H] and dst_row [T, K]")
     T, K = dst_row.shape
     H = grad_out.shape[1]
+    _sizes(T | K | H)
     dev = grad_out.device
     _need(grad_out, torch.bfloat16, "grad_out", (T, H), device=dev)
     _need(dst_row, torch.int32, "dst_row", device=dev)
@@ -648,6 +655,7 @@ def dispatch_backward(grad_recv_x: torch.Tensor, dst_row: torch.Tensor,
         raise ValueError("grad_recv_x must be [R, H] and dst_row [T, K]")
     T, K = dst_row.shape
     R, H = grad_recv_x.shape
+    _sizes(T | K | H)
     dev = grad_recv_x.device
     _need(grad_recv_x, torch.bfloat16, "grad_recv_x", device=dev)
     _need(dst_row, torch.int32, "dst_row", device=dev)
@@ -686,7 +694,8 @@ def route(logits: torch.Tensor, num_topk: int, expert_bias: torch.Tensor | None 
     combine.  ``out`` = (topk_idx, topk_weights) may be given."""
     dt = _logits_dtype(logits)
     T, E = logits.shape
-    K = int(num_topk)
+    K, NG, TG = int(num_topk), int(num_groups), int(topk_groups)
+    _sizes(T | E | K | NG | TG)
     dev = logits.device
     if expert_bias is not None:
         _need(expert_bias, torch.float32, "expert_bias", (E,), device=dev)
@@ -697,8 +706,7 @@ def route(logits: torch.Tensor, num_topk: int, expert_bias: torch.Tensor | None 
     _need(idx, torch.int64, "topk_idx", (T, K), device=dev)
     _need(w, torch.float32, "topk_weights", (T, K), device=dev)
     _launch("ep_route", logits, _addr(logits), dt, _addr(expert_bias), T, E, K, _score(score),
-            int(num_groups), int(topk_groups), int(bool(normalize)), float(scale), _addr(idx),
-            _addr(w))
+            NG, TG, int(bool(normalize)), float(scale), _addr(idx), _addr(w))
     return idx, w
 
 
@@ -713,6 +721,7 @@ def route_backward(logits: torch.Tensor, topk_idx: torch.Tensor, grad_weights: t
     if topk_idx.dim() != 2:
         raise ValueError("topk_idx must be [T, K]")
     K = topk_idx.shape[1]
+    _sizes(T | E | K)
     _need(topk_idx, torch.int64, "topk_idx", (T, K), device=dev)
     _need(grad_weights, torch.float32, "grad_weights", (T, K), device=dev)
     if out is None:
@@ -746,6 +755,8 @@ def expert_linear_w4(x: torch.Tensor, weight: torch.Tensor, scales: torch.Tensor
     R, I = x.shape
     E, W = weight.shape[0], weight.shape[1]
     NG = scales.shape[1]
+    C = int(capacity)
+    _sizes(E | I | W | C)
     dev = x.device
     if swiglu and W % 2 != 0:
         raise ValueError("swiglu needs an even number of weight channels, got %d" % W)
@@ -766,7 +777,7 @@ def expert_linear_w4(x: torch.Tensor, weight: torch.Tensor, scales: torch.Tensor
         _need(zeros, torch.uint8, "zeros", (E, NG, W), device=dev)
     _need(num_tokens_per_expert, torch.int32, "num_tokens_per_expert", (E,), device=dev)
     if expert_offsets is not None:
-        if capacity:
+        if C:
             raise ValueError("give expert_offsets or capacity, not both")
         _need(expert_offsets, torch.int32, "expert_offsets", (E + 1,), device=dev)
     if out is None:
@@ -774,7 +785,7 @@ def expert_linear_w4(x: torch.Tensor, weight: torch.Tensor, scales: torch.Tensor
     _need(out, torch.bfloat16, "out", (R, N), device=dev)
     _launch("ep_expert_linear_w4", x, _addr(x), _addr(x_scales),
             EP_DTYPE_FP8_E4M3 if fp8 else EP_DTYPE_BF16, R, _addr(expert_offsets),
-            _addr(num_tokens_per_expert), int(capacity), E, I, N, I // NG, _addr(weight),
+            _addr(num_tokens_per_expert), C, E, I, N, I // NG, _addr(weight),
             _addr(scales), _addr(zeros), int(bool(swiglu)), _addr(out))
     return out
 

@@ -364,3 +364,29 @@ def test_gradients_reject_rows_past_the_largest(buf):
     for H in (2**31 - 504, 2**31 - 8):
         assert L.ep_combine_backward(go, y, 1, dst, w, 1, 1, H, gy, gw, None) == UNSUPPORTED
         assert L.ep_dispatch_backward(go, 1, dst, 1, 1, H, gy, None) == UNSUPPORTED
+
+
+def test_binding_refuses_sizes_that_32_bits_would_cut(no_call):
+    """ctypes cuts an int argument to 32 bits without an error: 2^32 + 1 groups
+    would be 1 group, 2^32 + 3 tokens 3 tokens."""
+    big = (1 << 32) + 1
+    why = "below 2.31"
+    lg = torch.zeros((4, 16))
+    refused(why, b.route, lg, 2, num_groups=big)
+    refused(why, b.route, lg, 2, topk_groups=big)
+    refused(why, b.route, lg[:0], big)
+    row = lambda n, t: torch.empty((n, 1), dtype=t, device="meta")
+    refused(why, b.route, row(big, torch.bfloat16), 1)
+    refused(why, b.route_backward, row(big, torch.float32), row(big, torch.int64),
+            row(big, torch.float32))
+    bf = torch.bfloat16
+    y = torch.empty((8, 16), dtype=bf, device="meta")
+    refused(why, b.combine_backward, torch.empty((big, 16), dtype=bf, device="meta"), y,
+            row(big, torch.int32), row(big, torch.float32))
+    refused(why, b.dispatch_backward, y, row(big, torch.int32))
+    x = torch.zeros((12, 64), dtype=bf)
+    w = torch.zeros((3, 16, 32), dtype=torch.uint8)
+    s = torch.zeros((3, 1, 16), dtype=bf)
+    cnt = torch.zeros(3, dtype=torch.int32)
+    for c in (big, 1 << 31):
+        refused(why, b.expert_linear_w4, x, w, s, cnt, capacity=c)
