@@ -443,12 +443,14 @@ struct RowBlocks {
     int first[kKnown], rows[kKnown], upto[2][kKnown];
 };
 
+// Sums of lanes 0..i, at most 2^30: counts whose runs overlap, all of up to 2^31
+// rows, would pass 32 bits.
 __device__ __forceinline__ int prefix_sum(int v) {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
         const int o = __shfl_up(v, d);
-        if (lane >= d) v += o;
+        if (lane >= d) v = (int)min((unsigned)v + (unsigned)o, 1u << 30);
     }
     return v;
 }
@@ -739,8 +741,8 @@ __global__ __launch_bounds__(kExpertWaves * 64, kExpertWavesPerSimd) void expert
         if (e0 < kKnown) {
             lds.rbs.first[e0 + lane] = (int)b;
             lds.rbs.rows[e0 + lane] = rows;
-            lds.rbs.upto[0][e0 + lane] = (int)few + f;
-            lds.rbs.upto[1][e0 + lane] = (int)many + g;
+            lds.rbs.upto[0][e0 + lane] = (int)(few + f);
+            lds.rbs.upto[1][e0 + lane] = (int)(many + g);
         }
         few += __builtin_amdgcn_readlane(f, 63);
         many += __builtin_amdgcn_readlane(g, 63);

@@ -402,3 +402,21 @@ def test_router_of_more_tokens_than_one_launch_holds():
         want = torch.where(p > -math.inf, want, 0.0)
         off = (gl[a:a + step].double() - want).abs()
         assert bool((off <= (ref.UBF + 2 * ref.U32) * want.abs()).all()), a
+
+
+def test_expert_counts_whose_blocks_pass_32_bits():
+    """128 experts that each claim 2^31 - 1 rows: more tasks than any rows have.
+    Nothing is read or written."""
+    announce("expert counts past 32 bits")
+    E, I, N, G = 128, 32, 8, 32
+    x = torch.zeros((8, I), dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros((E, N, I // 2), dtype=torch.uint8, device="cuda")
+    s = torch.zeros((E, 1, N), dtype=torch.bfloat16, device="cuda")
+    cnt = torch.full((E,), 2**31 - 1, dtype=torch.int32, device="cuda")
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    y = torch.full((8, N), 6.5, dtype=torch.bfloat16, device="cuda")
+    ep._launch("ep_expert_linear_w4", x, x.data_ptr(), None, ep.EP_DTYPE_BF16, 2**31 - 1,
+               off.data_ptr(), cnt.data_ptr(), 0, E, I, N, G, w.data_ptr(), s.data_ptr(), None, 0,
+               y.data_ptr())
+    torch.cuda.synchronize()
+    assert bool((y == 6.5).all())
