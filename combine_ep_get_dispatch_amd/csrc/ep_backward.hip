@@ -81,6 +81,12 @@ __device__ __forceinline__ void dot_rows(float (&dot)[KN], const float (&g)[8],
     }
 }
 
+// Slot k's sum over the lanes; 0 for a slot without a row, whatever stands in g.
+__device__ __forceinline__ float slot_sum(float dot, const Slots& s, int k) {
+    const float v = seg_sum<64>(dot);
+    return __builtin_amdgcn_readlane(s.row, k) >= 0 ? v : 0.0f;
+}
+
 // ... and w * g into their gradient rows.
 template <int KN>
 __device__ __forceinline__ void write_rows(const float (&g)[8], uint16_t* __restrict__ gy,
@@ -145,7 +151,7 @@ __global__ __launch_bounds__(kBackwardMaxThreads) void combine_backward_kernel(
         if (gw) {
 #pragma unroll
             for (int i = 0; i < KN; ++i) {
-                const float v = seg_sum<64>(dot[i]);
+                const float v = slot_sum(dot[i], s, k0 + i);
                 if (lane == i) s_part[wave][i] = v;
             }
             __syncthreads();
@@ -191,7 +197,7 @@ __global__ __launch_bounds__(kBackwardTileThreads) void combine_backward_tile_ke
             }
 #pragma unroll
             for (int i = 0; i < KN; ++i) {
-                const float v = seg_sum<64>(dot[i]);
+                const float v = slot_sum(dot[i], s, k0 + i);
                 if (lane == i && k0 + i < K) s_dot[task * K + k0 + i] = v;
             }
         }

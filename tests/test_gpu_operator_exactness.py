@@ -420,3 +420,36 @@ def test_expert_counts_whose_blocks_pass_32_bits():
                y.data_ptr())
     torch.cuda.synchronize()
     assert bool((y == 6.5).all())
+
+
+@pytest.mark.parametrize("T,H,K", [(30, 264, 3), (9, 9000, 12), (2050, 4104, 8), (1100, 8200, 17)])
+def test_slots_without_a_row_get_0_whatever_their_tokens_gradient_holds(T, H, K):
+    """Infinities and NaN in the gradients of padded tokens, and of tokens that
+    have some of their slots: a slot without a row gets exactly 0."""
+    announce("masked slots T=%d H=%d K=%d" % (T, H, K))
+    g = torch.Generator(device="cuda").manual_seed(T)
+    R = 500
+    go = torch.randn((T, H), device="cuda", generator=g).bfloat16()
+    y = torch.randn((R, H), device="cuda", generator=g).bfloat16()
+    dst = torch.full((T * K,), -1, dtype=torch.int32)
+    at = torch.randperm(T * K, generator=gen(K))
+    n = min(R, T * K // 2)
+    dst[at[:n]] = torch.arange(n, dtype=torch.int32)
+    dst[at[n:n + 5]] = R + 7
+    dst = dst.view(T, K)
+    dst[::3] = -1
+    dst = dst.cuda()
+    go[::2, 5], go[::3], go[1, -1] = math.inf, math.nan, -math.inf
+    w = torch.rand((T, K), device="cuda", generator=g)
+    gy, both = ep.combine_backward(go, y, dst, w, out=(torch.full_like(y, 2.5), None))
+    _, alone = ep.combine_backward(go, y, dst, None)
+    ok = (dst >= 0) & (dst < R)
+    assert bool((~ok).any()) and bool(ok.any())
+    for gw in (both, alone):
+        assert bool((gw[~ok] == 0).all())
+    named = torch.zeros(R, dtype=torch.bool, device="cuda")
+    named[dst[ok].long()] = True
+    assert bool((gy[~named] == 2.5).all())
+    t = ok.nonzero()[:, 0]
+    assert torch.equal(torch.isnan(gy[dst[ok].long()].float()),
+                       torch.isnan(go[t].float() * w[ok][:, None]))
