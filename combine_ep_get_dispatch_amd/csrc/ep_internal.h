@@ -259,7 +259,7 @@ hipError_t launch_combine_backward(const uint16_t* gout, const uint16_t* y, int6
 
 // ----------------------------------------------------------------- router ---
 constexpr int kRouteThreads = 256;
-constexpr int kRouteWideTokens = 2048;   // largest batch with a wave per token
+constexpr int kRouteWideTokens = 2048;   // largest batch with a wave per token (to 256 experts)
 
 // bias null: the logits decide (unless NG > 1).  logits bf16 or fp32.
 hipError_t launch_route(const void* logits, bool bf16, const float* bias, int T, int E, int K,

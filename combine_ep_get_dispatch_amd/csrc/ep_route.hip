@@ -612,10 +612,24 @@ hipError_t launch_route_backward_l(const LT* logits, const int64_t* topk_idx, co
 }
 
 // Experts per lane and lanes per token: a whole wave for a token while the
-// batch is small (short chains), fewer lanes beyond (less work per token).  On
-// MI355X, wave / fewer: router of 256 experts with bias and groups, 128 tokens
-// 7.0 / 8.6 us, 4096 tokens 11.3 / 11.5, 32768 tokens 54 / 50; of 128 experts by
-// logits, 16384 tokens 13.7 / 7.9; of 64, 4096 tokens 5.5 / 4.5.
+// batch is small (short chains) and beyond 256 experts, fewer lanes otherwise
+// (less work per token).  On MI355X, us per launch, wave / fewer lanes, K = 6 or 8:
+//   tokens               128         2048        4096        16384
+//   by logits, fp32
+//     64 experts      3.7 / 3.6   3.9 / 3.7   4.7 / 3.8   10.0 / 5.4
+//    128              3.9 / 4.4   4.5 / 4.6   5.4 / 4.7   12.2 / 8.1
+//    256              4.3 / 4.7   5.0 / 4.8   6.3 / 6.0   14.8 / 13.0
+//    512              5.0 / 6.8   6.3 / 7.0   8.6 / 9.7   21.6 / 24.7
+//   bias, 8 groups, sigmoid, normalised
+//     64              5.3 / 5.7   5.7 / 5.8   7.4 / 6.0   18.0 / 10.0
+//    128              5.9 / 7.9   6.5 / 8.2   8.6 / 8.3   21.6 / 17.0
+//    256              6.7 / 8.3   7.7 / 8.4  10.6 / 10.9  27.9 / 27.7
+//    512              8.7 / 13.0 11.1 / 13.3 17.1 / 19.1  45.7 / 53.4
+//   gradient, softmax over all experts
+//     64              3.2 / 3.6   3.6 / 3.8   4.2 / 3.8    9.1 / 5.5
+//    128              3.3 / 4.1   3.9 / 4.3   4.7 / 4.5   11.1 / 7.7
+//    256              3.5 / 4.0   4.2 / 4.5   5.5 / 5.5   14.2 / 12.4
+//    512              4.0 / 5.2   5.5 / 6.5   7.7 / 8.6   22.4 / 22.5
 #define EP_ROUTE_DISPATCH(FN, LT, ...)                                             \
     do {                                                                           \
         const bool few = T <= kRouteWideTokens;                                    \
@@ -626,8 +640,7 @@ hipError_t launch_route_backward_l(const LT* logits, const int64_t* topk_idx, co
             return few ? FN<LT, 2, 64>(__VA_ARGS__) : FN<LT, 8, 16>(__VA_ARGS__);  \
         if (E <= 256)                                                              \
             return few ? FN<LT, 4, 64>(__VA_ARGS__) : FN<LT, 8, 32>(__VA_ARGS__);  \
-        if (E <= 512)                                                              \
-            return few ? FN<LT, 8, 64>(__VA_ARGS__) : FN<LT, 16, 32>(__VA_ARGS__); \
+        if (E <= 512) return FN<LT, 8, 64>(__VA_ARGS__);                           \
         return FN<LT, 16, 64>(__VA_ARGS__);                                        \
     } while (0)
 
