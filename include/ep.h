@@ -454,7 +454,7 @@ ep_status_t ep_dispatch_backward(const void *grad_recv_x, int64_t num_rows,
  * If fewer than K experts are left the last slots get topk_idx = -1 and
  * weight 0, a masked slot everywhere in this library; so a padded token whose
  * logits are all -inf takes no part.  A logit of +inf counts as fp32's largest
- * value.  Scores that are ordered by the logits and not normalised are summed
+ * value.  With neither a bias nor groups nor normalize the softmax is summed
  * exactly: a token's weights are the same bits in batches of any size.
  * logits [T*E] fp32 (EP_DTYPE_FP32) or bf16 (EP_DTYPE_BF16), aligned to their
  * element; expert_bias fp32 [E] or NULL; topk_idx int64 [T*K]; topk_weights
