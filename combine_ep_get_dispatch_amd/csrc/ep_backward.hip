@@ -6,9 +6,9 @@
 // writes no row.  (The gradient of dispatch is combine with unit weights; it
 // runs combine's kernels, see ep_combine.hip.)
 //
-// What bounds it.  The kernel is HBM-bound: every y row named is read once and every grad_y row
-// written once, about 3 flops per 4 bytes, so the design is combine's: 8
-// channels per lane, the row loads of a group of slots all in flight before
+// What bounds it.  The kernel is HBM-bound: every y row named is read once and
+// every grad_y row written once, about 3 flops per 4 bytes, so the design is
+// combine's: 8 channels per lane, the row loads of a group of slots all in flight before
 // the first product, non-temporal loads and stores for rows touched once.  A
 // row of g is read once and used for all the token's slots.
 //
@@ -17,7 +17,7 @@
 // less often.  On MI355X, tiled against one workgroup per token:
 //   4096 tokens x 7168, top-8   170 / 193 us (5.9 TB/s of 6.1 for plain reads)
 //   2048 x 7168, top-8           88 /  99      4096 x 7168, top-4   89 /  99
-//   8192 x 4096, top-4          101 / 107      4096 x 5120, top-6   93 / 100
+//   8192 x 4096, top-4          102 / 107      4096 x 5120, top-6   93 / 100
 //   4096 x 4096, top-10         127 / 139
 // but 103.4 / 102.9 at 8192 x 2048 top-8, 45 / 43 at 8192 x 1024 top-6 and
 // 262 / 228 at 32768 x 4096 top-2: few channels leave a tile's waves uneven

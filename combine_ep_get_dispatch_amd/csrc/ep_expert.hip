@@ -49,8 +49,9 @@
 // its rows; its four waves take every fourth step along the input channels and
 // their sums meet in LDS, in wave order.  Experts of up to 16 rows run with one
 // row tile, others with two (16 experts x 4096 -> 2 x 2048, E4M3 rows, one / two
-// for all: 4 rows each 35 / 37 us, 16 rows 57 / 42, 64 rows 146 / 106).  Four row
-// tiles do not fit the registers (64 rows: 187 us, 98 now with two).
+// for all, rows of an expert on average: 4 rows 35 / 37 us, 16 rows 57 / 42, 64
+// rows 146 / 106).  Four row tiles do not fit the registers (64 rows: 187 us, 98
+// now with two).
 //
 // What it took on MI355X, 32 experts x 128 rows, 7168 -> 2 x 2048 with SWIGLU,
 // E4M3 rows (484 MB): 3670 us with a wave per channel, 111 on matrix
@@ -58,7 +59,7 @@
 // 91-98 with the two 64-byte halves of a weight line asked for together (5.4
 // TB/s in the kernel; reading the weights alone in this pattern took 81).  bf16
 // rows, which leave registers for one block at a time (20 to 33 of 256 go to
-// scratch where G = 128; a form without took as long): 107-110 us.  One token's
+// scratch where G = 128; a form without took as long): 101-110 us.  One token's
 // eight experts, 2048 -> 7168 (60 MB): 17 us, 10 of them the weights.
 #include "ep_internal.h"
 #include "ep_device.h"

@@ -437,6 +437,13 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(
 // The large share then meets an exact 0, and what is left is off by at most
 // 2 + 2 / q_a roundings of sum_j q_j |c_k - c_j|.  All in fp64, rounded once to
 // the logits' type (to bf16 by way of fp32).
+//
+// What bounds it: latency at 4096 tokens of 256 experts (6.0 us per launch for
+// the dense form, 1.4 of them the bytes; 4.8 for the selected experts'), the
+// instructions beyond (23 us at 32768, the floor 11; 21 with sums in fp32).
+// Slots of one expert are added up once by the lanes that hold them and meet
+// their experts through LDS, in place of a search by every lane (9.7 us).
+//
 // Dynamic LDS, per token: a value for every expert (double; the lanes' j-th
 // experts next to each other, so that their accesses meet no bank twice), then K
 // slots' values (double) and experts (int).
