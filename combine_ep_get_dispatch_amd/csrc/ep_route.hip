@@ -266,13 +266,13 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(
             for (int j = 0; j < VPL; ++j) a += exp((double)l[j] - (double)m);
             total = seg_sum<L>(a);
         } else {
-            // fp32 terms, each cut to a multiple of 2^-42: up to 1024 of them,
+            // fp32 terms, each rounded to a multiple of 2^-41: up to 1024 of them,
             // each at most 1, add up in fp64 without rounding, so that a token's
             // total does not depend on how many lanes its batch size gives it
-            constexpr double kGrain = 1.5 * 1024.0;      // its last place is 2^-42
+            constexpr float kGrain = 0x1.8p-18f;         // its last place is 2^-41
             double a = 0.0;
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) a += ((double)expf(l[j] - m) + kGrain) - kGrain;
+            for (int j = 0; j < VPL; ++j) a += (double)((expf(l[j] - m) + kGrain) - kGrain);
             total = seg_sum<L>(a);
         }
     }
