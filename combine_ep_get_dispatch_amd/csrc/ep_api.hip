@@ -338,7 +338,7 @@ ep_status_t ep_combine_cu(const void* y, int64_t num_rows, const int32_t* dst_ro
     if (T < 0 || K <= 0 || H <= 0 || H % 8 != 0 || num_rows < 0 || num_cus < 0)
         return EP_ERR_INVALID_ARG;
     if ((int64_t)T * K >= kMaxRows) return EP_ERR_INVALID_ARG;
-    if (K > EP_MAX_TOPK) return EP_ERR_UNSUPPORTED;
+    if (K > EP_MAX_TOPK || H > EP_MAX_COMBINE_HIDDEN) return EP_ERR_UNSUPPORTED;
     if (T > 0) {
         if (!dst_row || !topk_weights || !out) return EP_ERR_INVALID_ARG;
         if ((y && !aligned16(y)) || !aligned16(out)) return EP_ERR_INVALID_ARG;
@@ -363,7 +363,7 @@ ep_status_t ep_combine_backward(const void* grad_out, const void* y, int64_t num
     const int32_t T = num_tokens, K = num_topk, H = hidden;
     if (T < 0 || K <= 0 || H <= 0 || H % 8 != 0 || num_rows < 0) return EP_ERR_INVALID_ARG;
     if ((int64_t)T * K >= kMaxRows) return EP_ERR_INVALID_ARG;
-    if (K > EP_MAX_TOPK || H > EP_MAX_GRAD_HIDDEN) return EP_ERR_UNSUPPORTED;
+    if (K > EP_MAX_TOPK || H > EP_MAX_COMBINE_HIDDEN) return EP_ERR_UNSUPPORTED;
     if (T > 0) {
         // without rows every slot is skipped: grad_y and y may then be empty
         if (!grad_out || !dst_row) return EP_ERR_INVALID_ARG;
@@ -386,7 +386,7 @@ ep_status_t ep_dispatch_backward(const void* grad_recv_x, int64_t num_rows,
     const int32_t T = num_tokens, K = num_topk, H = hidden;
     if (T < 0 || K <= 0 || H <= 0 || H % 8 != 0 || num_rows < 0) return EP_ERR_INVALID_ARG;
     if ((int64_t)T * K >= kMaxRows) return EP_ERR_INVALID_ARG;
-    if (K > EP_MAX_TOPK || H > EP_MAX_GRAD_HIDDEN) return EP_ERR_UNSUPPORTED;
+    if (K > EP_MAX_TOPK || H > EP_MAX_COMBINE_HIDDEN) return EP_ERR_UNSUPPORTED;
     if (T > 0) {
         if (!dst_row || !grad_x || (num_rows > 0 && !grad_recv_x)) return EP_ERR_INVALID_ARG;
         if ((grad_recv_x && !aligned16(grad_recv_x)) || !aligned16(grad_x))

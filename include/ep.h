@@ -82,7 +82,7 @@ typedef enum EP_ENUM_BASE {
 #define EP_LL_MAX_SLOTS 8192   /* T*K of one ep_low_latency_dispatch call */
 #define EP_MAX_EXPERT_ALIGNMENT 1024   /* of ep_layout_dispatch_aligned */
 #define EP_STATIC_SCRATCH_BYTES (8u << 20)   /* per GPU, of ep_layout_dispatch_static */
-#define EP_MAX_GRAD_HIDDEN 0x7ffffe00   /* hidden of the gradients of combine and dispatch */
+#define EP_MAX_COMBINE_HIDDEN 0x7ffffe00   /* hidden of combine and the gradients */
 #define EP_MAX_ROUTE_GROUPS 64   /* expert groups of ep_route */
 #define EP_MAX_EXPERT_IN (1 << 24)   /* input channels of ep_expert_linear_w4 */
 
@@ -409,7 +409,7 @@ ep_status_t ep_combine_cu(const void *y, int64_t num_rows, const int32_t *dst_ro
  * Types, shapes, limits and errors as ep_combine: grad_out bf16 [T*H], y and
  * grad_y bf16 [num_rows*H],
  * topk_weights and grad_weights fp32 [T*K]; grad_out, y and grad_y 16-byte
- * aligned.  T may be 0.  EP_ERR_UNSUPPORTED for H > EP_MAX_GRAD_HIDDEN too.
+ * aligned.  T may be 0.
  */
 ep_status_t ep_combine_backward(const void *grad_out, const void *y, int64_t num_rows,
                                 const int32_t *dst_row, const float *topk_weights,
@@ -426,8 +426,7 @@ ep_status_t ep_combine_backward(const void *grad_out, const void *y, int64_t num
  * like the receive rows (of any dispatch form; for the de-duplicated one like
  * the expert-major rows that dst_row names), the gradient with respect to the
  * values the rows stand for: an FP8 dispatch passes it straight through its
- * quantiser.  Types, shapes, limits and errors as ep_combine without weights;
- * EP_ERR_UNSUPPORTED for H > EP_MAX_GRAD_HIDDEN too.
+ * quantiser.  Types, shapes, limits and errors as ep_combine without weights.
  */
 ep_status_t ep_dispatch_backward(const void *grad_recv_x, int64_t num_rows,
                                  const int32_t *dst_row, int32_t num_tokens, int32_t num_topk,
@@ -481,8 +480,9 @@ ep_status_t ep_route(const void *logits, ep_dtype_t logits_dtype, const float *e
  * and 0 for every other expert; every element of grad_logits is written,
  * computed in fp64 and rounded once to logits' type (to bf16 by way of fp32),
  * and keeps its digits where one expert holds nearly all of the weight.  Slots
- * of one token that name the same expert add up.  The arguments are those of the ep_route call; topk_idx is its
- * output, grad_weights fp32 [T*K].  No gradient reaches the bias.
+ * of one token that name the same expert add up.  The arguments are those of
+ * the ep_route call; topk_idx is its output, grad_weights fp32 [T*K].  No
+ * gradient reaches the bias.
  */
 ep_status_t ep_route_backward(const void *logits, ep_dtype_t logits_dtype,
                               const int64_t *topk_idx, const float *grad_weights,
@@ -520,14 +520,17 @@ ep_status_t ep_route_backward(const void *logits, ep_dtype_t logits_dtype,
  * I > 0, N > 0, N % 8 == 0; x, weight, y 16-byte aligned, scales 8-byte,
  * zeros 4-byte.  capacity is ignored with expert_offsets, else >= 1 with
  * E*capacity <= num_rows; num_rows < 2^31.  EP_ERR_UNSUPPORTED for
- * E > EP_MAX_EXPERTS, I > EP_MAX_EXPERT_IN or W * I/2 >= 2^31.  x and the scales are expected
- * finite, |x| < 2^113 (of E4M3 rows: x_scales < 2^104, which gives that), and
- * 143 * sum over i of |x[r,i]| * s below fp32's largest value.  (Sums of bf16
- * rows pass through 128 channels of up to 143 |x|.)  No workspace; the order of the sums is fixed by the
- * arguments' shapes and, for E4M3 rows, by whether the row's expert has more
- * than 16 rows: below and above, a row's result is the same bits whatever rows
- * stand beside it, and for bf16 rows it always is.  (No page describes the experts themselves; format and
- * definition are this library's.)
+ * E > EP_MAX_EXPERTS, I > EP_MAX_EXPERT_IN or W * I/2 >= 2^31.
+ *   x and the scales are expected finite, |x| < 2^113 (of E4M3 rows: x_scales
+ * < 2^104, which gives that), and 143 * sum over i of |x[r,i]| * s below fp32's
+ * largest value.  (Sums of bf16 rows pass through 128 channels of up to 143
+ * |x|.)
+ *   No workspace.  The order of the sums is fixed by the arguments' shapes and,
+ * for E4M3 rows, by whether the row's expert has more than 16 rows: below and
+ * above, a row's result is the same bits whatever rows stand beside it, and for
+ * bf16 rows it always is.
+ *   (No page describes the experts themselves; format and definition are this
+ * library's.)
  */
 ep_status_t ep_expert_linear_w4(const void *x, const float *x_scales, ep_dtype_t x_dtype,
                                 int64_t num_rows, const int32_t *expert_offsets,

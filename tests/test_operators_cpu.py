@@ -358,12 +358,13 @@ def test_binding_refuses_what_is_wrong_with_the_experts_tensors(no_call):
             cnt, capacity=C, swiglu=True)
 
 
-def test_gradients_reject_rows_past_the_largest(buf):
+def test_combine_and_gradients_reject_rows_past_the_largest(buf):
     L = b.lib()
     go, y, dst, w, gy, gw = (buf() for _ in range(6))
     for H in (2**31 - 504, 2**31 - 8):
         assert L.ep_combine_backward(go, y, 1, dst, w, 1, 1, H, gy, gw, None) == UNSUPPORTED
         assert L.ep_dispatch_backward(go, 1, dst, 1, 1, H, gy, None) == UNSUPPORTED
+        assert L.ep_combine(y, 1, dst, w, 1, 1, H, gy, None) == UNSUPPORTED
 
 
 def test_binding_refuses_sizes_that_32_bits_would_cut(no_call):
