@@ -78,6 +78,19 @@ SIGNATURES = {
                                          ctypes.c_int, _i32, _f32, _vp, _vp]),
     "ep_expert_linear_w4": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _i64, _vp, _vp, _i32, _i32,
                                            _i32, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _vp]),
+    "ep_expert_linear": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _i64, _vp, _vp, _i32, _i32, _i32,
+                                        _i32, _vp, _vp, _i32, _vp, _vp]),
+    "ep_expert_linear_backward": (ctypes.c_int, [_vp, _vp, _vp, _i64, _vp, _vp, _i32, _i32, _i32,
+                                                 _i32, _vp, _vp, ctypes.c_int, _i32, _vp]),
+    "ep_expert_swiglu": (ctypes.c_int, [_vp, _i64, _vp, _vp, _i32, _i32, _i32, ctypes.c_int, _vp,
+                                        _vp, _vp]),
+    "ep_expert_swiglu_backward": (ctypes.c_int, [_vp, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _vp,
+                                                 _vp]),
+    "ep_rms_norm": (ctypes.c_int, [_vp, _vp, _vp, ctypes.c_int, _i32, _i32, _f32, _vp, _vp, _vp,
+                                   _vp, _vp, _vp]),
+    "ep_rms_norm_backward_workspace_bytes": (_sz, [_i32, _i32]),
+    "ep_rms_norm_backward": (ctypes.c_int, [_vp, _vp, _vp, ctypes.c_int, _vp, _vp, _i32, _i32,
+                                            _vp, _vp, _vp, _sz, _vp]),
     "ep_get_device_error": (ctypes.c_int, [_vp, _sz, ctypes.POINTER(_i64), _vp]),
     "ep_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "ep_convert_e4m3": (ctypes.c_int, [_vp, _vp, _i64, _i32, _vp]),
@@ -788,6 +801,286 @@ def expert_linear_w4(x: torch.Tensor, weight: torch.Tensor, scales: torch.Tensor
             _addr(num_tokens_per_expert), C, E, I, N, I // NG, _addr(weight),
             _addr(scales), _addr(zeros), int(bool(swiglu)), _addr(out))
     return out
+
+
+def _runs(num_tokens_per_expert: torch.Tensor, expert_offsets: torch.Tensor | None, capacity: int,
+          E: int, device):
+    """Check the tensors that say which rows an expert has."""
+    _need(num_tokens_per_expert, torch.int32, "num_tokens_per_expert", (E,), device=device)
+    if expert_offsets is not None:
+        if capacity:
+            raise ValueError("give expert_offsets or capacity, not both")
+        _need(expert_offsets, torch.int32, "expert_offsets", (E + 1,), device=device)
+
+
+def expert_linear(x: torch.Tensor, weight: torch.Tensor, num_tokens_per_expert: torch.Tensor,
+                  expert_offsets: torch.Tensor | None = None, capacity: int = 0,
+                  x_scales: torch.Tensor | None = None,
+                  weight_scales: torch.Tensor | None = None, swiglu: bool = False,
+                  out: torch.Tensor | None = None) -> torch.Tensor:
+    """ep_expert_linear: the experts' products over the rows of a dispatch.
+
+    x [R, I] and weight [E, W, I] are both bf16, or both uint8 E4M3 codes with
+    x_scales [R, I/128] and weight_scales [E, S, I/128] float32, one scale per
+    128 x 128 block; W = N and S = ceil(N/128), or both doubled with swiglu
+    (gate half first).  The rows are those of a dispatch with offsets
+    (expert_offsets [E+1] and the counts of its Layout) or of a
+    low_latency_dispatch (its counts and ``capacity``).  Returns y [R, N] bf16;
+    rows that hold no token are left as they are (an ``out`` not given is
+    allocated uninitialised)."""
+    if x.dim() != 2 or weight.dim() != 3:
+        raise ValueError("x must be [R, I] and weight [E, W, I]")
+    R, I = x.shape
+    E, W = weight.shape[0], weight.shape[1]
+    C = int(capacity)
+    _sizes(E | I | W | C)
+    dev = x.device
+    if swiglu and W % 2 != 0:
+        raise ValueError("swiglu needs an even number of weight channels, got %d" % W)
+    N = W // 2 if swiglu else W
+    fp8 = x.dtype == torch.uint8
+    dt = torch.uint8 if fp8 else torch.bfloat16
+    _need(x, dt, "x", device=dev)
+    _need(weight, dt, "weight", (E, W, I), device=dev)
+    if fp8:
+        if x_scales is None or weight_scales is None:
+            raise ValueError("E4M3 codes need x_scales and weight_scales")
+        _need(x_scales, torch.float32, "x_scales", (R, I // 128), device=dev)
+        S = (N + 127) // 128 * (2 if swiglu else 1)
+        _need(weight_scales, torch.float32, "weight_scales", (E, S, I // 128), device=dev)
+    elif x_scales is not None or weight_scales is not None:
+        raise ValueError("x_scales and weight_scales belong to E4M3 codes (uint8)")
+    _runs(num_tokens_per_expert, expert_offsets, C, E, dev)
+    if out is None:
+        out = torch.empty((R, N), dtype=torch.bfloat16, device=dev)
+    _need(out, torch.bfloat16, "out", (R, N), device=dev)
+    _launch("ep_expert_linear", x, _addr(x), _addr(x_scales),
+            EP_DTYPE_FP8_E4M3 if fp8 else EP_DTYPE_BF16, R, _addr(expert_offsets),
+            _addr(num_tokens_per_expert), C, E, I, N, _addr(weight), _addr(weight_scales),
+            int(bool(swiglu)), _addr(out))
+    return out
+
+
+def expert_linear_backward(grad_y: torch.Tensor, x: torch.Tensor | None,
+                           weight: torch.Tensor | None, num_tokens_per_expert: torch.Tensor,
+                           expert_offsets: torch.Tensor | None = None, capacity: int = 0,
+                           grad_weight_dtype: torch.dtype = torch.bfloat16,
+                           accumulate: bool = False, out=None):
+    """ep_expert_linear_backward: from grad_y [R, N] bf16 the gradients of
+    expert_linear(x, weight, ...) in bf16 without swiglu: (grad_x [R, I] bf16,
+    grad_weight [E, N, I] bf16 or float32), or the ones given in ``out``.
+    Without ``weight`` only grad_weight is computed, without ``x`` only grad_x;
+    the other one is None.  ``accumulate`` adds to a float32 grad_weight given
+    in ``out``.  Rows of grad_x that hold no token are left as they are (a
+    grad_x not given is allocated uninitialised)."""
+    if x is None and weight is None:
+        raise ValueError("expert_linear_backward needs x or weight")
+    if (grad_y.dim() != 2 or (x is not None and x.dim() != 2)
+            or (weight is not None and weight.dim() != 3)):
+        raise ValueError("grad_y must be [R, N], x [R, I] and weight [E, N, I]")
+    R, N = grad_y.shape
+    E = num_tokens_per_expert.numel() if weight is None else weight.shape[0]
+    I = x.shape[1] if weight is None else weight.shape[2]
+    C = int(capacity)
+    _sizes(E | I | N | C)
+    dev = grad_y.device
+    _need(grad_y, torch.bfloat16, "grad_y", device=dev)
+    grad_x, grad_weight = (None, None) if out is None else out
+    if weight is not None:
+        _need(weight, torch.bfloat16, "weight", (E, N, I), device=dev)
+        if grad_x is None:
+            grad_x = torch.empty((R, I), dtype=torch.bfloat16, device=dev)
+        _need(grad_x, torch.bfloat16, "grad_x", (R, I), device=dev)
+    elif grad_x is not None:
+        raise ValueError("grad_x needs weight")
+    if x is not None:
+        _need(x, torch.bfloat16, "x", (R, I), device=dev)
+        if grad_weight is None:
+            if accumulate:
+                raise ValueError("accumulate needs a grad_weight in out")
+            grad_weight = torch.empty((E, N, I), dtype=grad_weight_dtype, device=dev)
+        dt = grad_weight.dtype
+        if dt != torch.float32 and (dt != torch.bfloat16 or accumulate):
+            raise TypeError("grad_weight must be float32%s, got %s"
+                            % (" to accumulate" if accumulate else " or bfloat16", dt))
+        _need(grad_weight, dt, "grad_weight", (E, N, I), device=dev)
+    elif grad_weight is not None:
+        raise ValueError("grad_weight needs x")
+    _runs(num_tokens_per_expert, expert_offsets, C, E, dev)
+    f32 = grad_weight is not None and grad_weight.dtype == torch.float32
+    _launch("ep_expert_linear_backward", grad_y, _addr(grad_y), _addr(x), _addr(weight), R,
+            _addr(expert_offsets), _addr(num_tokens_per_expert), C, E, I, N, _addr(grad_x),
+            _addr(grad_weight), EP_DTYPE_FP32 if f32 else EP_DTYPE_BF16, int(bool(accumulate)))
+    return grad_x, grad_weight
+
+
+def expert_swiglu(gate_up: torch.Tensor, num_tokens_per_expert: torch.Tensor | None = None,
+                  expert_offsets: torch.Tensor | None = None, capacity: int = 0,
+                  fp8: bool = False, out=None):
+    """ep_expert_swiglu: gate_up [R, 2N] bf16 -> silu(gate) * up, y [R, N] bf16,
+    or with ``fp8`` (codes [R, N] uint8, scales [R, N/128] float32).  The rows
+    are the experts', as expert_linear takes them, or all of them without
+    ``num_tokens_per_expert``; the others are left as they are (an ``out`` not
+    given is allocated uninitialised)."""
+    R, N = _gate_shape(gate_up)
+    dev = gate_up.device
+    E, C = _gate_runs(num_tokens_per_expert, expert_offsets, capacity, N, dev)
+    _need(gate_up, torch.bfloat16, "gate_up", device=dev)
+    if fp8:
+        if out is None:
+            out = (torch.empty((R, N), dtype=torch.uint8, device=dev),
+                   torch.empty((R, N // 128), dtype=torch.float32, device=dev))
+        y, scales = out
+        _need(y, torch.uint8, "codes", (R, N), device=dev)
+        _need(scales, torch.float32, "scales", (R, N // 128), device=dev)
+    else:
+        if out is None:
+            out = torch.empty((R, N), dtype=torch.bfloat16, device=dev)
+        y, scales = out, None
+        _need(y, torch.bfloat16, "out", (R, N), device=dev)
+    _launch("ep_expert_swiglu", gate_up, _addr(gate_up), R, _addr(expert_offsets),
+            _addr(num_tokens_per_expert), C, E, N, EP_DTYPE_FP8_E4M3 if fp8 else EP_DTYPE_BF16,
+            _addr(y), _addr(scales))
+    return out
+
+
+def expert_swiglu_backward(grad_y: torch.Tensor, gate_up: torch.Tensor,
+                           num_tokens_per_expert: torch.Tensor | None = None,
+                           expert_offsets: torch.Tensor | None = None, capacity: int = 0,
+                           out: torch.Tensor | None = None) -> torch.Tensor:
+    """ep_expert_swiglu_backward: from grad_y [R, N] bf16 the gradient of
+    expert_swiglu's gate_up, [R, 2N] bf16."""
+    R, N = _gate_shape(gate_up)
+    dev = gate_up.device
+    E, C = _gate_runs(num_tokens_per_expert, expert_offsets, capacity, N, dev)
+    _need(gate_up, torch.bfloat16, "gate_up", device=dev)
+    _need(grad_y, torch.bfloat16, "grad_y", (R, N), device=dev)
+    if out is None:
+        out = torch.empty((R, 2 * N), dtype=torch.bfloat16, device=dev)
+    _need(out, torch.bfloat16, "out", (R, 2 * N), device=dev)
+    _launch("ep_expert_swiglu_backward", gate_up, _addr(grad_y), _addr(gate_up), R,
+            _addr(expert_offsets), _addr(num_tokens_per_expert), C, E, N, _addr(out))
+    return out
+
+
+def _gate_shape(gate_up: torch.Tensor):
+    if gate_up.dim() != 2 or gate_up.shape[1] % 2 != 0:
+        raise ValueError("gate_up must be [R, 2N]")
+    return gate_up.shape[0], gate_up.shape[1] // 2
+
+
+def _gate_runs(num_tokens_per_expert, expert_offsets, capacity, N, device):
+    C = int(capacity)
+    if num_tokens_per_expert is None:
+        if expert_offsets is not None or C:
+            raise ValueError("expert_offsets and capacity need num_tokens_per_expert")
+        _sizes(N)
+        return 0, 0
+    E = num_tokens_per_expert.numel()
+    _sizes(E | N | C)
+    _runs(num_tokens_per_expert, expert_offsets, C, E, device)
+    return E, C
+
+
+# ---------------------------------------------------------------------------
+# norm
+# ---------------------------------------------------------------------------
+
+@dataclass
+class RmsNormed:
+    y: torch.Tensor | None               # [T, H] bf16
+    codes: torch.Tensor | None           # [T, H] uint8 E4M3 codes of y
+    scales: torch.Tensor | None          # [T, H/128] float32
+    residual: torch.Tensor | None        # [T, H] bf16: x + residual
+    inv_rms: torch.Tensor                # [T] float32
+
+
+def _norm_weight(weight: torch.Tensor, H: int, device) -> int:
+    if weight.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("weight must be float32 or bfloat16, got %s" % weight.dtype)
+    _need(weight, weight.dtype, "weight", (H,), device=device)
+    return EP_DTYPE_FP32 if weight.dtype == torch.float32 else EP_DTYPE_BF16
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+             residual: torch.Tensor | None = None, bf16: bool = True, fp8: bool = False,
+             out: RmsNormed | None = None) -> RmsNormed:
+    """ep_rms_norm: h / rms(h) * weight of h = x [T, H] bf16, or of h = x +
+    residual, which is then the next residual: in bf16 (``bf16``), in E4M3 with a
+    scale per 128 channels (``fp8``), or both."""
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    T, H = x.shape
+    _sizes(T | H)
+    dev = x.device
+    if not bf16 and not fp8:
+        raise ValueError("rms_norm needs bf16 or fp8")
+    _need(x, torch.bfloat16, "x", device=dev)
+    wdt = _norm_weight(weight, H, dev)
+    if residual is not None:
+        _need(residual, torch.bfloat16, "residual", (T, H), device=dev)
+    if out is None:
+        out = RmsNormed(
+            torch.empty((T, H), dtype=torch.bfloat16, device=dev) if bf16 else None,
+            torch.empty((T, H), dtype=torch.uint8, device=dev) if fp8 else None,
+            torch.empty((T, H // 128), dtype=torch.float32, device=dev) if fp8 else None,
+            torch.empty((T, H), dtype=torch.bfloat16, device=dev) if residual is not None
+            else None,
+            torch.empty(T, dtype=torch.float32, device=dev))
+    if bf16:
+        _need(out.y, torch.bfloat16, "y", (T, H), device=dev)
+    if fp8:
+        _need(out.codes, torch.uint8, "codes", (T, H), device=dev)
+        _need(out.scales, torch.float32, "scales", (T, H // 128), device=dev)
+    if residual is not None:
+        _need(out.residual, torch.bfloat16, "out.residual", (T, H), device=dev)
+    _need(out.inv_rms, torch.float32, "inv_rms", (T,), device=dev)
+    _launch("ep_rms_norm", x, _addr(x), _addr(residual), _addr(weight), wdt, T, H, float(eps),
+            _addr(out.y) if bf16 else None, _addr(out.codes) if fp8 else None,
+            _addr(out.scales) if fp8 else None,
+            _addr(out.residual) if residual is not None else None, _addr(out.inv_rms))
+    return out
+
+
+def rms_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
+                      inv_rms: torch.Tensor, grad_residual: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, out=None):
+    """ep_rms_norm_backward: from grad_y [T, H] bf16 the gradients of rms_norm:
+    (grad_x [T, H] bf16, of x and residual alike, grad_weight [H] float32).
+    ``x`` is what was normed, with a residual the call's ``residual`` output, whose
+    own gradient ``grad_residual`` is added.  ``workspace``: uint8, at least
+    rms_norm_backward_workspace_bytes; allocated if not given."""
+    if grad_y.dim() != 2:
+        raise ValueError("grad_y must be [T, H]")
+    T, H = grad_y.shape
+    _sizes(T | H)
+    dev = grad_y.device
+    _need(grad_y, torch.bfloat16, "grad_y", device=dev)
+    _need(x, torch.bfloat16, "x", (T, H), device=dev)
+    wdt = _norm_weight(weight, H, dev)
+    _need(inv_rms, torch.float32, "inv_rms", (T,), device=dev)
+    if grad_residual is not None:
+        _need(grad_residual, torch.bfloat16, "grad_residual", (T, H), device=dev)
+    if out is None:
+        out = (torch.empty((T, H), dtype=torch.bfloat16, device=dev),
+               torch.empty(H, dtype=torch.float32, device=dev))
+    grad_x, grad_weight = out
+    _need(grad_x, torch.bfloat16, "grad_x", (T, H), device=dev)
+    _need(grad_weight, torch.float32, "grad_weight", (H,), device=dev)
+    if workspace is None:
+        workspace = torch.empty(rms_norm_backward_workspace_bytes(T, H), dtype=torch.uint8,
+                                device=dev)
+    _need(workspace, torch.uint8, "workspace", device=dev)
+    _launch("ep_rms_norm_backward", grad_y, _addr(grad_y), _addr(x), _addr(weight), wdt,
+            _addr(inv_rms), _addr(grad_residual), T, H, _addr(grad_x), _addr(grad_weight),
+            _addr(workspace), workspace.numel())
+    return grad_x, grad_weight
+
+
+def rms_norm_backward_workspace_bytes(num_tokens: int, hidden: int) -> int:
+    """Bytes of rms_norm_backward's workspace (0 for an invalid shape)."""
+    _sizes(num_tokens | hidden)
+    return lib().ep_rms_norm_backward_workspace_bytes(num_tokens, hidden)
 
 
 # ---------------------------------------------------------------------------

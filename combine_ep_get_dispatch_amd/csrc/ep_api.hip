@@ -492,6 +492,202 @@ ep_status_t ep_expert_linear_w4(const void* x, const float* x_scales, ep_dtype_t
         static_cast<uint16_t*>(y), static_cast<hipStream_t>(stream)));
 }
 
+}  // extern "C"
+
+namespace {
+
+// The checks that the calls over the experts' rows share.
+ep_status_t check_runs(int64_t num_rows, const int32_t* offsets, const int32_t* counts,
+                       int32_t capacity, int32_t E) {
+    if (E <= 0 || num_rows < 0 || num_rows >= kMaxRows) return EP_ERR_INVALID_ARG;
+    if (!offsets && (capacity < 1 || (int64_t)E * capacity > num_rows)) return EP_ERR_INVALID_ARG;
+    if (!counts) return EP_ERR_INVALID_ARG;
+    return E > EP_MAX_EXPERTS ? EP_ERR_UNSUPPORTED : EP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ep_status_t ep_expert_linear(const void* x, const float* x_scales, ep_dtype_t dtype,
+                             int64_t num_rows, const int32_t* expert_offsets,
+                             const int32_t* num_tokens_per_expert, int32_t capacity,
+                             int32_t num_experts, int32_t in_features, int32_t out_features,
+                             const void* weight, const float* weight_scales, int32_t swiglu,
+                             void* y, void* stream) {
+    const int32_t E = num_experts, I = in_features, N = out_features;
+    if (dtype != EP_DTYPE_BF16 && dtype != EP_DTYPE_FP8_E4M3) return EP_ERR_INVALID_ARG;
+    const bool fp8 = dtype == EP_DTYPE_FP8_E4M3;
+    if (I <= 0 || I % (fp8 ? 128 : 8) != 0 || N <= 0 || N % 8 != 0) return EP_ERR_INVALID_ARG;
+    if (num_rows > 0) {
+        if (!x || !weight || !y || (fp8 && (!x_scales || !weight_scales)))
+            return EP_ERR_INVALID_ARG;
+        if (!aligned16(x) || !aligned16(weight) || !aligned16(y)) return EP_ERR_INVALID_ARG;
+    }
+    ep_status_t st = check_runs(num_rows, expert_offsets, num_tokens_per_expert, capacity, E);
+    if (st != EP_OK) return st;
+    if (I > EP_MAX_LINEAR_CHANNELS || (int64_t)N * (swiglu ? 2 : 1) > EP_MAX_LINEAR_CHANNELS)
+        return EP_ERR_UNSUPPORTED;
+    const ep::RowRuns runs = {expert_offsets, num_tokens_per_expert, capacity, E, num_rows};
+    return from_hip(ep::launch_expert_linear(x, fp8 ? x_scales : nullptr, runs, I, N, weight,
+                                             weight_scales, swiglu != 0,
+                                             static_cast<uint16_t*>(y),
+                                             static_cast<hipStream_t>(stream)));
+}
+
+ep_status_t ep_expert_linear_backward(const void* grad_y, const void* x, const void* weight,
+                                      int64_t num_rows, const int32_t* expert_offsets,
+                                      const int32_t* num_tokens_per_expert, int32_t capacity,
+                                      int32_t num_experts, int32_t in_features,
+                                      int32_t out_features, void* grad_x, void* grad_weight,
+                                      ep_dtype_t grad_weight_dtype, int32_t accumulate,
+                                      void* stream) {
+    const int32_t E = num_experts, I = in_features, N = out_features;
+    if (I <= 0 || I % 8 != 0 || N <= 0 || N % 8 != 0) return EP_ERR_INVALID_ARG;
+    const bool fp32 = grad_weight_dtype == EP_DTYPE_FP32;
+    if (grad_weight && !fp32 && (grad_weight_dtype != EP_DTYPE_BF16 || accumulate))
+        return EP_ERR_INVALID_ARG;
+    if (!grad_x && !grad_weight) return EP_ERR_INVALID_ARG;
+    if (grad_weight && !aligned16(grad_weight)) return EP_ERR_INVALID_ARG;
+    if (num_rows > 0) {
+        if (!grad_y || !aligned16(grad_y)) return EP_ERR_INVALID_ARG;
+        if (grad_x && (!weight || !aligned16(weight) || !aligned16(grad_x)))
+            return EP_ERR_INVALID_ARG;
+        if (grad_weight && (!x || !aligned16(x))) return EP_ERR_INVALID_ARG;
+    }
+    ep_status_t st = check_runs(num_rows, expert_offsets, num_tokens_per_expert, capacity, E);
+    if (st != EP_OK) return st;
+    if (I > EP_MAX_LINEAR_CHANNELS || N > EP_MAX_LINEAR_CHANNELS) return EP_ERR_UNSUPPORTED;
+    const ep::RowRuns runs = {expert_offsets, num_tokens_per_expert, capacity, E, num_rows};
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const uint16_t* gy = static_cast<const uint16_t*>(grad_y);
+    if (grad_x) {
+        st = from_hip(ep::launch_expert_grad_rows(gy, runs, I, N,
+                                                  static_cast<const uint16_t*>(weight),
+                                                  static_cast<uint16_t*>(grad_x), s));
+        if (st != EP_OK) return st;
+    }
+    if (!grad_weight) return EP_OK;
+    return from_hip(ep::launch_expert_grad_weight(gy, static_cast<const uint16_t*>(x), runs, I, N,
+                                                  grad_weight, fp32, accumulate != 0, s));
+}
+
+ep_status_t ep_expert_swiglu(const void* gate_up, int64_t num_rows, const int32_t* expert_offsets,
+                             const int32_t* num_tokens_per_expert, int32_t capacity,
+                             int32_t num_experts, int32_t features, ep_dtype_t out_dtype, void* y,
+                             float* y_scales, void* stream) {
+    const int32_t E = num_experts, N = features;
+    if (out_dtype != EP_DTYPE_BF16 && out_dtype != EP_DTYPE_FP8_E4M3) return EP_ERR_INVALID_ARG;
+    const bool fp8 = out_dtype == EP_DTYPE_FP8_E4M3;
+    if (N <= 0 || N % (fp8 ? 128 : 8) != 0 || num_rows < 0 || num_rows >= kMaxRows)
+        return EP_ERR_INVALID_ARG;
+    if (num_rows > 0) {
+        if (!gate_up || !y || (fp8 && !y_scales)) return EP_ERR_INVALID_ARG;
+        if (!aligned16(gate_up) || !aligned16(y)) return EP_ERR_INVALID_ARG;
+    }
+    if (num_tokens_per_expert) {
+        ep_status_t st = check_runs(num_rows, expert_offsets, num_tokens_per_expert, capacity, E);
+        if (st != EP_OK) return st;
+    }
+    if (N > EP_MAX_LINEAR_CHANNELS) return EP_ERR_UNSUPPORTED;
+    const ep::RowRuns runs = {expert_offsets, num_tokens_per_expert, capacity, E, num_rows};
+    return from_hip(ep::launch_expert_swiglu(
+        static_cast<const uint16_t*>(gate_up), runs, N, fp8 ? nullptr : static_cast<uint16_t*>(y),
+        fp8 ? static_cast<uint8_t*>(y) : nullptr, y_scales, static_cast<hipStream_t>(stream)));
+}
+
+ep_status_t ep_expert_swiglu_backward(const void* grad_y, const void* gate_up, int64_t num_rows,
+                                      const int32_t* expert_offsets,
+                                      const int32_t* num_tokens_per_expert, int32_t capacity,
+                                      int32_t num_experts, int32_t features, void* grad_gate_up,
+                                      void* stream) {
+    const int32_t E = num_experts, N = features;
+    if (N <= 0 || N % 8 != 0 || num_rows < 0 || num_rows >= kMaxRows) return EP_ERR_INVALID_ARG;
+    if (num_rows > 0) {
+        if (!grad_y || !gate_up || !grad_gate_up) return EP_ERR_INVALID_ARG;
+        if (!aligned16(grad_y) || !aligned16(gate_up) || !aligned16(grad_gate_up))
+            return EP_ERR_INVALID_ARG;
+    }
+    if (num_tokens_per_expert) {
+        ep_status_t st = check_runs(num_rows, expert_offsets, num_tokens_per_expert, capacity, E);
+        if (st != EP_OK) return st;
+    }
+    if (N > EP_MAX_LINEAR_CHANNELS) return EP_ERR_UNSUPPORTED;
+    const ep::RowRuns runs = {expert_offsets, num_tokens_per_expert, capacity, E, num_rows};
+    return from_hip(ep::launch_expert_swiglu_backward(
+        static_cast<const uint16_t*>(grad_y), static_cast<const uint16_t*>(gate_up), runs, N,
+        static_cast<uint16_t*>(grad_gate_up), static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// Shape and type checks shared by the norm and its gradient.
+ep_status_t check_norm(ep_dtype_t weight_dtype, const void* weight, int32_t T, int32_t H) {
+    if (T < 0 || H <= 0 || H % 8 != 0) return EP_ERR_INVALID_ARG;
+    if (weight_dtype != EP_DTYPE_BF16 && weight_dtype != EP_DTYPE_FP32) return EP_ERR_INVALID_ARG;
+    if (T > 0 && (!weight || !aligned16(weight))) return EP_ERR_INVALID_ARG;
+    return H > EP_MAX_NORM_HIDDEN ? EP_ERR_UNSUPPORTED : EP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ep_status_t ep_rms_norm(const void* x, const void* residual, const void* weight,
+                        ep_dtype_t weight_dtype, int32_t num_tokens, int32_t hidden, float eps,
+                        void* y, uint8_t* codes, float* scales, void* residual_out,
+                        float* inv_rms, void* stream) {
+    const int32_t T = num_tokens, H = hidden;
+    ep_status_t st = check_norm(weight_dtype, weight, T, H);
+    if (st == EP_ERR_INVALID_ARG) return st;
+    if (!(eps >= 0.0f && eps - eps == 0.0f)) return EP_ERR_INVALID_ARG;
+    if (T > 0) {
+        if (!x || !aligned16(x) || (!y && !codes)) return EP_ERR_INVALID_ARG;
+        if (y && !aligned16(y)) return EP_ERR_INVALID_ARG;
+        if (codes && (!scales || !aligned16(codes))) return EP_ERR_INVALID_ARG;
+        if (!residual != !residual_out) return EP_ERR_INVALID_ARG;
+        if (residual && (!aligned16(residual) || !aligned16(residual_out)))
+            return EP_ERR_INVALID_ARG;
+    }
+    if (codes && H % 128 != 0) return EP_ERR_INVALID_ARG;
+    if (st != EP_OK || T == 0) return st;
+    return from_hip(ep::launch_rms_norm(
+        static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(residual), weight,
+        weight_dtype == EP_DTYPE_FP32, T, H, eps, static_cast<uint16_t*>(y), codes, scales,
+        static_cast<uint16_t*>(residual_out), inv_rms, static_cast<hipStream_t>(stream)));
+}
+
+size_t ep_rms_norm_backward_workspace_bytes(int32_t num_tokens, int32_t hidden) {
+    if (check_norm(EP_DTYPE_FP32, nullptr, 0, hidden) != EP_OK || num_tokens < 0) return 0;
+    return (size_t)(ep::norm_parts(num_tokens) > 0 ? ep::norm_parts(num_tokens) : 1) * hidden *
+           sizeof(float);
+}
+
+ep_status_t ep_rms_norm_backward(const void* grad_y, const void* x, const void* weight,
+                                 ep_dtype_t weight_dtype, const float* inv_rms,
+                                 const void* grad_residual, int32_t num_tokens, int32_t hidden,
+                                 void* grad_x, float* grad_weight, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+    const int32_t T = num_tokens, H = hidden;
+    ep_status_t st = check_norm(weight_dtype, weight, T, H);
+    if (st != EP_OK) return st;
+    if (!grad_weight || !aligned16(grad_weight) || !workspace || !aligned16(workspace))
+        return EP_ERR_INVALID_ARG;
+    if (T > 0) {
+        if (!grad_y || !x || !inv_rms || !grad_x) return EP_ERR_INVALID_ARG;
+        if (!aligned16(grad_y) || !aligned16(x) || !aligned16(grad_x)) return EP_ERR_INVALID_ARG;
+        if (grad_residual && !aligned16(grad_residual)) return EP_ERR_INVALID_ARG;
+    }
+    if (workspace_bytes < ep_rms_norm_backward_workspace_bytes(T, H)) return EP_ERR_WORKSPACE;
+    return from_hip(ep::launch_rms_norm_backward(
+        static_cast<const uint16_t*>(grad_y), static_cast<const uint16_t*>(x), weight,
+        weight_dtype == EP_DTYPE_FP32, inv_rms, static_cast<const uint16_t*>(grad_residual), T, H,
+        static_cast<uint16_t*>(grad_x), grad_weight, static_cast<float*>(workspace),
+        static_cast<hipStream_t>(stream)));
+}
+
 ep_status_t ep_get_device_error(const void* workspace, size_t workspace_bytes,
                                 int64_t* num_invalid, void* stream) {
     if (!workspace || !num_invalid || workspace_bytes < ep::kWsHeaderBytes)

@@ -90,6 +90,23 @@ __device__ __forceinline__ uint32_t e4m3x4_sw(float a, float b, float c, float d
     return e4m3_sw(a) | (e4m3_sw(b) << 8) | (e4m3_sw(c) << 16) | (e4m3_sw(d) << 24);
 }
 
+// Eight neighbouring channels of a bf16 row as fp32, and back (rounded to
+// nearest even).
+__device__ __forceinline__ void unpack8(float (&f)[8], const uint4& v) {
+    f[0] = bf16_lo(v.x);
+    f[1] = bf16_hi(v.x);
+    f[2] = bf16_lo(v.y);
+    f[3] = bf16_hi(v.y);
+    f[4] = bf16_lo(v.z);
+    f[5] = bf16_hi(v.z);
+    f[6] = bf16_lo(v.w);
+    f[7] = bf16_hi(v.w);
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
+
 // Unsigned maximum over the 8 lanes of an aligned group of 8, with three DPP
 // moves (no LDS round trip): swap neighbours (quad_perm 1,0,3,2), swap pairs
 // (quad_perm 2,3,0,1), then mirror each half row of 8 lanes, which pairs the
@@ -108,6 +125,43 @@ __device__ __forceinline__ uint32_t group16_max_u32(uint32_t v) {
     v = group8_max_u32(v);
     v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xf, 0xf, false));
     return v;
+}
+
+// The E4M3 codes of a lane's eight channels and the scale of the 128 that the 16
+// lanes of its DPP row hold, all active, from fp32 values by dispatch's rule:
+// a_c = max(max |v|, 1e-4), scale a_c / 448, codes E4M3(v * (448 / a_c)); NaNs
+// take no part in the maximum, and an infinite or NaN v gets the code S.1111.111
+// with its sign.
+__device__ __forceinline__ uint2 quantise8(const float (&v)[8], float& scale) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    m = group16_max_u32(m);
+    const bool finite = m < 0x7f800000u;
+    if (!finite) {
+        m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t a = __float_as_uint(v[i]) & 0x7fffffffu;
+            m = max(m, a > 0x7f800000u ? 0u : a);
+        }
+        m = group16_max_u32(m);
+    }
+    const float ac = fmaxf(__uint_as_float(m), 1e-4f), inv = 448.0f / ac;
+    scale = ac / 448.0f;
+    uint2 q = make_uint2(e4m3x4_hw(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                         e4m3x4_hw(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+    if (!finite) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t b = __float_as_uint(v[i]);
+            if ((b & 0x7f800000u) != 0x7f800000u) continue;
+            const int sh = 8 * (i & 3);
+            uint32_t& w = i < 4 ? q.x : q.y;
+            w = (w & ~(0xffu << sh)) | ((b >> 24 & 0x80u) | 0x7fu) << sh;
+        }
+    }
+    return q;
 }
 
 // Sum over aligned segments of S lanes (S a power of two, 1..64), every lane

@@ -289,6 +289,59 @@ hipError_t launch_expert_linear_w4(const void* x, const float* xs, bool fp8, int
                                    const uint16_t* scales, const uint8_t* zeros, bool swiglu,
                                    uint16_t* y, hipStream_t s);
 
+// The rows of the experts: expert e's start at offsets[e], or with offsets null
+// at e * capacity; rows outside [0, num_rows) belong to nobody.
+struct RowRuns {
+    const int32_t* offsets;
+    const int32_t* counts;
+    int capacity;
+    int E;
+    int64_t num_rows;
+
+    // Rows of expert e (0 or less: none) and the first one.
+    __device__ __forceinline__ int64_t of(int e, int64_t& begin) const {
+        begin = offsets ? (int64_t)offsets[e] : (int64_t)e * capacity;
+        int64_t end = begin + (offsets ? counts[e] : min(counts[e], capacity));
+        if (begin < 0) begin = 0;
+        if (end > num_rows) end = num_rows;
+        return end - begin;
+    }
+};
+
+// ---------------------------------------------------------------- grouped ---
+// x_scales null: bf16 rows and weights; else E4M3.
+hipError_t launch_expert_linear(const void* x, const float* xs, const RowRuns& runs, int I, int N,
+                                const void* w, const float* ws, bool swiglu, uint16_t* y,
+                                hipStream_t s);
+hipError_t launch_expert_grad_rows(const uint16_t* gy, const RowRuns& runs, int I, int N,
+                                   const uint16_t* w, uint16_t* gx, hipStream_t s);
+hipError_t launch_expert_grad_weight(const uint16_t* gy, const uint16_t* x, const RowRuns& runs,
+                                     int I, int N, void* gw, bool fp32, bool accumulate,
+                                     hipStream_t s);
+
+// ------------------------------------------------------------------- gate ---
+constexpr int kGateThreads = 256;
+constexpr int kGateTileBytes = 32 * 1024;
+
+// codes null: bf16.  runs.counts null: every row.
+hipError_t launch_expert_swiglu(const uint16_t* a, const RowRuns& runs, int N, uint16_t* y,
+                                uint8_t* codes, float* scales, hipStream_t s);
+hipError_t launch_expert_swiglu_backward(const uint16_t* gy, const uint16_t* a, const RowRuns& runs,
+                                         int N, uint16_t* ga, hipStream_t s);
+
+// ------------------------------------------------------------------- norm ---
+constexpr int kNormMaxParts = 512;
+// Workgroups of the norm's gradient, each with a part of the weight's.
+constexpr int norm_parts(int T) { return T < kNormMaxParts ? T : kNormMaxParts; }
+
+// res null: no residual; y, codes, inv null: not asked for.
+hipError_t launch_rms_norm(const uint16_t* x, const uint16_t* res, const void* w, bool w32, int T,
+                           int H, float eps, uint16_t* y, uint8_t* codes, float* scales,
+                           uint16_t* res_out, float* inv, hipStream_t s);
+hipError_t launch_rms_norm_backward(const uint16_t* gy, const uint16_t* x, const void* w, bool w32,
+                                    const float* inv, const uint16_t* gres, int T, int H,
+                                    uint16_t* gx, float* gw, float* ws, hipStream_t s);
+
 // ------------------------------------------------------------ diagnostics ---
 hipError_t launch_convert_e4m3(const float* in, uint8_t* out, int64_t n, int mode, hipStream_t s);
 hipError_t launch_convert_bf16(const float* in, uint16_t* out, int64_t n, hipStream_t s);

@@ -1,0 +1,326 @@
+// Root-mean-square norm of the tokens ahead of the layer, and its gradient, on
+// gfx950.  With h = x, or bf16(x + residual):
+//   inv = 1 / sqrt(mean over channels of h^2 + eps),   y = h * inv * weight,
+// y rounded once, to bf16, or to E4M3 with a scale per 128 channels as dispatch
+// writes its rows, or to both.  h is what the next layer's residual reads and
+// what the gradient is taken from, so the norm sees it as stored.  With
+// n = h * inv and gn = grad_y * weight:
+//   grad_h = inv * (gn - n * mean(gn * n)) + grad_residual,
+//   grad_weight = sum over tokens of grad_y * n.
+//
+// Both are bound by HBM: a row is read once, kept in registers across its sum,
+// and written once.
+#include "ep_internal.h"
+#include "ep_device.h"
+
+#include <type_traits>
+
+namespace ep {
+namespace {
+
+struct NormArgs {
+    const uint16_t* x;
+    const uint16_t* res;
+    const void* w;
+    float eps;
+    int H;
+    uint16_t* y;
+    uint8_t* codes;
+    float* scales;
+    uint16_t* res_out;
+    float* inv;
+};
+
+struct NormBackArgs {
+    const uint16_t* gy;
+    const uint16_t* x;
+    const void* w;
+    const float* inv;
+    const uint16_t* gres;
+    int T, H;
+    uint16_t* gx;
+    float* part;     // [gridDim.x][H]
+};
+
+// A weight of bf16 or fp32, eight channels.
+template <bool W32>
+struct Weight8 {
+    uint4 a, b;
+};
+template <bool W32>
+__device__ __forceinline__ Weight8<W32> load_weight(const void* w, int c) {
+    Weight8<W32> r;
+    if constexpr (W32) {
+        r.a = static_cast<const uint4*>(w)[2 * c];
+        r.b = static_cast<const uint4*>(w)[2 * c + 1];
+    } else {
+        r.a = static_cast<const uint4*>(w)[c];
+    }
+    return r;
+}
+template <bool W32>
+__device__ __forceinline__ void unpack_weight(float (&f)[8], const Weight8<W32>& w) {
+    if constexpr (W32) {
+        const uint32_t u[8] = {w.a.x, w.a.y, w.a.z, w.a.w, w.b.x, w.b.y, w.b.z, w.b.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(u[i]);
+    } else {
+        unpack8(f, w.a);
+    }
+}
+
+// Sum over a workgroup of NW waves, in wave order, the same in every thread.
+// s holds NW floats; the caller sees to it that no wave still reads it.
+template <int NW>
+__device__ __forceinline__ float block_sum(float v, float* s) {
+    v = seg_sum<64>(v);
+    if constexpr (NW == 1) return v;
+    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+    __syncthreads();
+    float t = s[0];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) t += s[i];
+    return t;
+}
+
+// One row per workgroup of NW waves; a thread holds chunks of 8 channels tid,
+// tid + 64 NW, ..., NC of them, so 16 neighbouring lanes hold 128 neighbouring
+// channels, one scale.
+template <int NW, int NC, bool W32>
+__global__ __launch_bounds__(NW * 64) void rms_norm_kernel(const NormArgs p) {
+    constexpr int kThreads = NW * 64;
+    __shared__ float part[NW];
+    const int chunks = p.H / 8;
+    const int64_t row = blockIdx.x;
+    const uint4* x = reinterpret_cast<const uint4*>(p.x + row * p.H);
+    uint4 v[NC];
+    Weight8<W32> w[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+        v[i] = x[min((int)threadIdx.x + i * kThreads, chunks - 1)];
+    if (p.res) {
+        const uint4* res = reinterpret_cast<const uint4*>(p.res + row * p.H);
+        uint4 r[NC];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) r[i] = res[min((int)threadIdx.x + i * kThreads, chunks - 1)];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            float a[8], b[8];
+            unpack8(a, v[i]);
+            unpack8(b, r[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a[j] += b[j];
+            v[i] = pack8(a);
+            const int c = threadIdx.x + i * kThreads;
+            if (c < chunks) reinterpret_cast<uint4*>(p.res_out + row * p.H)[c] = v[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+        w[i] = load_weight<W32>(p.w, min((int)threadIdx.x + i * kThreads, chunks - 1));
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        float a[8], s = 0.0f;
+        unpack8(a, v[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s = __builtin_fmaf(a[j], a[j], s);
+        sum += (int)threadIdx.x + i * kThreads < chunks ? s : 0.0f;
+    }
+    sum = block_sum<NW>(sum, part);
+    const float inv = 1.0f / sqrtf(sum / (float)p.H + p.eps);
+    if (p.inv && threadIdx.x == 0) p.inv[row] = inv;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int c = threadIdx.x + i * kThreads;
+        if (c >= chunks) break;          // whole groups of 16 lanes where codes are written
+        float a[8], f[8];
+        unpack8(a, v[i]);
+        unpack_weight<W32>(f, w[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[j] = a[j] * inv * f[j];
+        if (p.y) reinterpret_cast<uint4*>(p.y + row * p.H)[c] = pack8(a);
+        if (p.codes) {
+            float scale;
+            const uint2 q = quantise8(a, scale);
+            reinterpret_cast<uint2*>(p.codes + row * p.H)[c] = q;
+            if ((threadIdx.x & 15) == 0) p.scales[row * (p.H / 128) + c / 16] = scale;
+        }
+    }
+}
+
+// Rows blockIdx.x, blockIdx.x + gridDim.x, ...; a thread's channels as above.
+// It sums its channels' grad_weight over the workgroup's rows in registers;
+// sum_parts_kernel adds the workgroups' sums up in their order.
+template <int NW, int NC, bool W32>
+__global__ __launch_bounds__(NW * 64) void rms_norm_backward_kernel(const NormBackArgs p) {
+    constexpr int kThreads = NW * 64;
+    __shared__ float part[2][NW];
+    const int chunks = p.H / 8;
+    float gw[NC][8];
+    Weight8<W32> w[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        w[i] = load_weight<W32>(p.w, min((int)threadIdx.x + i * kThreads, chunks - 1));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) gw[i][j] = 0.0f;
+    }
+    const float per = 1.0f / (float)p.H;
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x, turn ^= 1) {
+        const uint4* x = reinterpret_cast<const uint4*>(p.x + row * p.H);
+        const uint4* gy = reinterpret_cast<const uint4*>(p.gy + row * p.H);
+        uint4 v[NC], g[NC], r[NC];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = min((int)threadIdx.x + i * kThreads, chunks - 1);
+            v[i] = x[c];
+            g[i] = gy[c];
+            if (p.gres) r[i] = reinterpret_cast<const uint4*>(p.gres + row * p.H)[c];
+        }
+        const float inv = p.inv[row];
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            float a[8], b[8], f[8], s = 0.0f;
+            unpack8(a, v[i]);
+            unpack8(b, g[i]);
+            unpack_weight<W32>(f, w[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float n = a[j] * inv;
+                gw[i][j] = __builtin_fmaf(b[j], n, gw[i][j]);
+                s = __builtin_fmaf(b[j] * f[j], n, s);
+            }
+            sum += (int)threadIdx.x + i * kThreads < chunks ? s : 0.0f;
+        }
+        const float mean = block_sum<NW>(sum, part[turn]) * per;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = threadIdx.x + i * kThreads;
+            if (c >= chunks) break;
+            float a[8], b[8], f[8], o[8];
+            unpack8(a, v[i]);
+            unpack8(b, g[i]);
+            unpack_weight<W32>(f, w[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = inv * (b[j] * f[j] - a[j] * inv * mean);
+            if (p.gres) {
+                unpack8(f, r[i]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] += f[j];
+            }
+            reinterpret_cast<uint4*>(p.gx + row * p.H)[c] = pack8(o);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int c = threadIdx.x + i * kThreads;
+        if (c >= chunks) break;
+        float4* o = reinterpret_cast<float4*>(p.part + (int64_t)blockIdx.x * p.H + c * 8);
+        o[0] = make_float4(gw[i][0], gw[i][1], gw[i][2], gw[i][3]);
+        o[1] = make_float4(gw[i][4], gw[i][5], gw[i][6], gw[i][7]);
+    }
+}
+
+// out[c] = sum over the parts, four channels a thread; 16 threads share a
+// channel's parts, each every 16th of them, and add up in a fixed order.
+constexpr int kPartThreads = 16;
+__global__ __launch_bounds__(256) void sum_parts_kernel(const float* part, int parts, int H,
+                                                        float* out) {
+    __shared__ float4 s[256];
+    const int c = (blockIdx.x * (256 / kPartThreads) + threadIdx.x % (256 / kPartThreads)) * 4;
+    float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (c < H) {
+        for (int i = threadIdx.x / (256 / kPartThreads); i < parts; i += kPartThreads) {
+            const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)i * H + c);
+            t.x += v.x;
+            t.y += v.y;
+            t.z += v.z;
+            t.w += v.w;
+        }
+    }
+    s[threadIdx.x] = t;
+    __syncthreads();
+    if (threadIdx.x < 256 / kPartThreads && c < H) {
+        for (int i = 1; i < kPartThreads; ++i) {
+            const float4 v = s[threadIdx.x + i * (256 / kPartThreads)];
+            t.x += v.x;
+            t.y += v.y;
+            t.z += v.z;
+            t.w += v.w;
+        }
+        *reinterpret_cast<float4*>(out + c) = t;
+    }
+}
+
+// Waves and chunks per thread for rows of `chunks` chunks.
+template <typename F>
+void by_width(int chunks, F&& f) {
+    if (chunks <= 64)
+        f(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
+    else if (chunks <= 256)
+        f(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
+    else if (chunks <= 512)
+        f(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
+    else if (chunks <= 1024)
+        f(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
+    else if (chunks <= 2048)
+        f(std::integral_constant<int, 8>{}, std::integral_constant<int, 4>{});
+    else
+        f(std::integral_constant<int, 16>{}, std::integral_constant<int, 4>{});
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm(const uint16_t* x, const uint16_t* res, const void* w, bool w32, int T,
+                           int H, float eps, uint16_t* y, uint8_t* codes, float* scales,
+                           uint16_t* res_out, float* inv, hipStream_t s) {
+    by_width(H / 8, [&](auto nw, auto nc) {
+        constexpr int NW = decltype(nw)::value, NC = decltype(nc)::value;
+        const int64_t most = max_launch_tokens(NW * 64);
+        for (int64_t t = 0; t < T; t += most) {
+            const int64_t at = t * H;
+            const NormArgs p = {x + at,
+                                res ? res + at : nullptr,
+                                w,
+                                eps,
+                                H,
+                                y ? y + at : nullptr,
+                                codes ? codes + at : nullptr,
+                                codes ? scales + t * (H / 128) : nullptr,
+                                res ? res_out + at : nullptr,
+                                inv ? inv + t : nullptr};
+            const dim3 grid((unsigned)(T - t < most ? T - t : most));
+            if (w32)
+                hipLaunchKernelGGL((rms_norm_kernel<NW, NC, true>), grid, dim3(NW * 64), 0, s, p);
+            else
+                hipLaunchKernelGGL((rms_norm_kernel<NW, NC, false>), grid, dim3(NW * 64), 0, s, p);
+        }
+    });
+    return hipGetLastError();
+}
+
+hipError_t launch_rms_norm_backward(const uint16_t* gy, const uint16_t* x, const void* w, bool w32,
+                                    const float* inv, const uint16_t* gres, int T, int H,
+                                    uint16_t* gx, float* gw, float* ws, hipStream_t s) {
+    const int parts = norm_parts(T);
+    if (T > 0) {
+        const NormBackArgs p = {gy, x, w, inv, gres, T, H, gx, ws};
+        by_width(H / 8, [&](auto nw, auto nc) {
+            constexpr int NW = decltype(nw)::value, NC = decltype(nc)::value;
+            if (w32)
+                hipLaunchKernelGGL((rms_norm_backward_kernel<NW, NC, true>), dim3(parts),
+                                   dim3(NW * 64), 0, s, p);
+            else
+                hipLaunchKernelGGL((rms_norm_backward_kernel<NW, NC, false>), dim3(parts),
+                                   dim3(NW * 64), 0, s, p);
+        });
+    }
+    const int per = 256 / kPartThreads * 4;
+    hipLaunchKernelGGL(sum_parts_kernel, dim3((H + per - 1) / per), dim3(256), 0, s, ws, parts, H,
+                       gw);
+    return hipGetLastError();
+}
+
+}  // namespace ep

@@ -68,7 +68,7 @@ typedef enum EP_ENUM_BASE {
 typedef enum EP_ENUM_BASE {
     EP_DTYPE_BF16 = 0,       /* receive rows are bf16 copies of the tokens  */
     EP_DTYPE_FP8_E4M3 = 1,   /* receive rows are OCP E4M3 codes + scales    */
-    EP_DTYPE_FP32 = 2        /* router logits only                          */
+    EP_DTYPE_FP32 = 2        /* logits, norm weights, weight gradients      */
 } ep_dtype_t;
 
 typedef enum EP_ENUM_BASE {
@@ -85,6 +85,8 @@ typedef enum EP_ENUM_BASE {
 #define EP_MAX_COMBINE_HIDDEN 0x7ffffe00   /* hidden of combine and the gradients */
 #define EP_MAX_ROUTE_GROUPS 64   /* expert groups of ep_route */
 #define EP_MAX_EXPERT_IN (1 << 24)   /* input channels of ep_expert_linear_w4 */
+#define EP_MAX_LINEAR_CHANNELS (1 << 22)   /* channels of ep_expert_linear's rows */
+#define EP_MAX_NORM_HIDDEN 32768   /* hidden of ep_rms_norm */
 
 /*
  * Bytes of device workspace that ep_get_dispatch_layout and ep_dispatch need
@@ -539,6 +541,143 @@ ep_status_t ep_expert_linear_w4(const void *x, const float *x_scales, ep_dtype_t
                                 int32_t out_features, int32_t group_size,
                                 const uint8_t *weight, const void *scales,
                                 const uint8_t *zeros, int32_t swiglu, void *y, void *stream);
+
+/*
+ * The experts' linear layer over the rows that a dispatch wrote, for prefill
+ * and training (and for decode with weights of 8 or 16 bits), with an optional
+ * gated activation.  For every row r of expert e, and channel n:
+ *   a[n]    = sum over i of x[r,i] * w[e,n,i]
+ *   y[r,n]  = bf16(a[n]),                          n < N        (swiglu == 0)
+ *   y[r,n]  = bf16(silu(a[n]) * a[N + n]),         n < N        (swiglu != 0)
+ * accumulated in fp32, silu(v) = v / (1 + exp(-v)), rounded once.
+ *   Rows of expert e, num_rows, expert_offsets, num_tokens_per_expert and
+ *   capacity: as ep_expert_linear_w4.  Rows of no expert are left untouched in
+ *   y, and nothing that they hold reaches another row.
+ *   dtype EP_DTYPE_BF16: x bf16 [num_rows*I], weight bf16 [E, W, I], W = N, or
+ *   2N with swiglu (gate channels first); x_scales and weight_scales ignored.
+ *   I % 8 == 0.
+ *   dtype EP_DTYPE_FP8_E4M3 (I % 128 == 0): x E4M3 codes [num_rows*I] with
+ *   x_scales fp32 [num_rows*I/128], as dispatch writes them; weight E4M3 codes
+ *   [E, W, I] with weight_scales fp32 [E, S, I/128], one scale per block of
+ *   128 x 128: channel n of the first N uses block n/128, channel N + n of the
+ *   other half block ceil(N/128) + n/128; S = ceil(N/128), twice that with
+ *   swiglu.  The codes' products are summed over 128 channels, then scaled.
+ *   (As in ep_expert_linear_w4 the matrix instructions align the products of
+ *   neighbouring channels to the largest and cut them at 2^-13 of its power of
+ *   two, ahead of the fp32 sums.)
+ *   N > 0, N % 8 == 0; x, weight, y 16-byte aligned.  EP_ERR_UNSUPPORTED for
+ * E > EP_MAX_EXPERTS, I or W > EP_MAX_LINEAR_CHANNELS.
+ *   No workspace, one launch.  Equal arguments give equal bits.
+ *   (No page describes the experts themselves; the definitions of this call and
+ * the next ones are this library's.)
+ */
+ep_status_t ep_expert_linear(const void *x, const float *x_scales, ep_dtype_t dtype,
+                             int64_t num_rows, const int32_t *expert_offsets,
+                             const int32_t *num_tokens_per_expert, int32_t capacity,
+                             int32_t num_experts, int32_t in_features, int32_t out_features,
+                             const void *weight, const float *weight_scales, int32_t swiglu,
+                             void *y, void *stream);
+
+/*
+ * Gradients of ep_expert_linear in bf16 without the activation (whose own
+ * gradient is ep_expert_swiglu_backward): for the rows r of every expert e
+ *   grad_x[r,i]        = bf16(sum over n of grad_y[r,n] * w[e,n,i])
+ *   grad_weight[e,n,i] = sum over e's rows r of grad_y[r,n] * x[r,i]
+ * accumulated in fp32, rounded once to grad_weight's type, EP_DTYPE_BF16 or
+ * EP_DTYPE_FP32; with accumulate (fp32 only) the sum is added to what
+ * grad_weight holds.  An expert without rows has the gradient 0 (with
+ * accumulate: is left as it is).  Rows of no expert are left untouched in
+ * grad_x, and nothing that they hold in grad_y or x reaches a gradient.
+ *   grad_x NULL: only grad_weight (weight may then be NULL); grad_weight NULL:
+ * only grad_x (x may then be NULL); not both.  Shapes, limits and errors as
+ * ep_expert_linear, with N the channels of grad_y bf16 [num_rows*N]; x and
+ * grad_x bf16 [num_rows*I], weight and grad_weight [E, N, I]; all 16-byte
+ * aligned.  No workspace, a launch for each gradient.
+ */
+ep_status_t ep_expert_linear_backward(const void *grad_y, const void *x, const void *weight,
+                                      int64_t num_rows, const int32_t *expert_offsets,
+                                      const int32_t *num_tokens_per_expert, int32_t capacity,
+                                      int32_t num_experts, int32_t in_features,
+                                      int32_t out_features, void *grad_x, void *grad_weight,
+                                      ep_dtype_t grad_weight_dtype, int32_t accumulate,
+                                      void *stream);
+
+/*
+ * The gated activation by itself, between two products whose first one's output
+ * a training step keeps, or whose second one takes E4M3 rows:
+ *   y[r,n] = silu(a[r,n]) * a[r,N+n],   n < N,
+ * computed in fp32 from a = gate_up bf16 [num_rows*2N], for the rows of the
+ * experts (as ep_expert_linear_w4 describes them), or for all num_rows rows if
+ * num_tokens_per_expert is NULL (the arguments about experts are then ignored).
+ * Other rows are left untouched.
+ *   out_dtype EP_DTYPE_BF16 (N % 8 == 0): y bf16 [num_rows*N], rounded once.
+ *   out_dtype EP_DTYPE_FP8_E4M3 (N % 128 == 0): y codes [num_rows*N] and
+ *   y_scales fp32 [num_rows*N/128] by ep_dispatch's rule, of the fp32 results.
+ * gate_up and y 16-byte aligned.  EP_ERR_UNSUPPORTED for E > EP_MAX_EXPERTS or
+ * N > EP_MAX_LINEAR_CHANNELS.
+ */
+ep_status_t ep_expert_swiglu(const void *gate_up, int64_t num_rows, const int32_t *expert_offsets,
+                             const int32_t *num_tokens_per_expert, int32_t capacity,
+                             int32_t num_experts, int32_t features, ep_dtype_t out_dtype, void *y,
+                             float *y_scales, void *stream);
+
+/*
+ * Gradient of ep_expert_swiglu (with E4M3 rows: straight through the
+ * quantiser), with g = a[r,n], u = a[r,N+n] and s = 1 / (1 + exp(-g)):
+ *   grad_gate_up[r,n]   = bf16(grad_y[r,n] * u * (s + g * s * (1 - s)))
+ *   grad_gate_up[r,N+n] = bf16(grad_y[r,n] * g * s)
+ * grad_y bf16 [num_rows*N], gate_up and grad_gate_up bf16 [num_rows*2N], 16-byte
+ * aligned; N % 8 == 0.  Rows, limits and errors as there.
+ */
+ep_status_t ep_expert_swiglu_backward(const void *grad_y, const void *gate_up, int64_t num_rows,
+                                      const int32_t *expert_offsets,
+                                      const int32_t *num_tokens_per_expert, int32_t capacity,
+                                      int32_t num_experts, int32_t features, void *grad_gate_up,
+                                      void *stream);
+
+/*
+ * Root-mean-square norm of the tokens ahead of the layer, with the residual's
+ * addition ahead of it and E4M3 rows behind it: for every token t
+ *   h[t,i]  = x[t,i], or with a residual bf16(x[t,i] + residual[t,i])
+ *   inv[t]  = 1 / sqrt(mean over i of h[t,i]^2 + eps)
+ *   y[t,i]  = h[t,i] * inv[t] * weight[i]
+ * computed in fp32.  Written are
+ *   y bf16 [T*H] (NULL: not asked for), rounded once;
+ *   codes uint8 [T*H] and scales fp32 [T*H/128] (NULL: not asked for;
+ *   H % 128 == 0), y in E4M3 by ep_dispatch's rule, from the fp32 results;
+ *   residual_out bf16 [T*H], h, with a residual (NULL without);
+ *   inv_rms fp32 [T] (NULL: not asked for), for the gradient.
+ * y or codes has to be given.  x and residual bf16 [T*H]; weight [H] bf16 or
+ * fp32 by weight_dtype; H % 8 == 0; eps >= 0 and finite.  Arrays of rows and
+ * weight 16-byte aligned.  EP_ERR_UNSUPPORTED for H > EP_MAX_NORM_HIDDEN.  T may
+ * be 0.
+ */
+ep_status_t ep_rms_norm(const void *x, const void *residual, const void *weight,
+                        ep_dtype_t weight_dtype, int32_t num_tokens, int32_t hidden, float eps,
+                        void *y, uint8_t *codes, float *scales, void *residual_out,
+                        float *inv_rms, void *stream);
+
+/* Bytes of workspace that ep_rms_norm_backward needs; 0 if the shape is invalid. */
+size_t ep_rms_norm_backward_workspace_bytes(int32_t num_tokens, int32_t hidden);
+
+/*
+ * Gradients of ep_rms_norm: with h (the x of the call, or its residual_out) as
+ * x, inv its inv_rms, n[t,i] = h[t,i] * inv[t] and gn[t,i] = grad_y[t,i] * weight[i],
+ *   grad_x[t,i]    = bf16(inv[t] * (gn[t,i] - n[t,i] * mean over j of gn[t,j] * n[t,j])
+ *                         + grad_residual[t,i])
+ *   grad_weight[i] = sum over t of grad_y[t,i] * n[t,i]
+ * in fp32; grad_x is the gradient of both x and residual, grad_residual bf16
+ * [T*H] what reaches residual_out (or NULL).  E4M3 rows: straight through the
+ * quantiser.  grad_weight fp32 [H], its sum's order fixed by the shape (0 if T
+ * is 0).  workspace: ep_rms_norm_backward_workspace_bytes() bytes, 16-byte aligned,
+ * needs no initialisation; calls that overlap need one each.  Other arguments,
+ * limits and errors as ep_rms_norm.
+ */
+ep_status_t ep_rms_norm_backward(const void *grad_y, const void *x, const void *weight,
+                                 ep_dtype_t weight_dtype, const float *inv_rms,
+                                 const void *grad_residual, int32_t num_tokens, int32_t hidden,
+                                 void *grad_x, float *grad_weight, void *workspace,
+                                 size_t workspace_bytes, void *stream);
 
 /*
  * Waits for `stream`, then stores in *num_invalid the number of invalid
