@@ -59,9 +59,11 @@ __device__ __forceinline__ void dma4(uint32_t at, const i32x4& buffer, uint32_t 
 }
 constexpr uint32_t kNowhere = 0x80000000u;   // past every buffer's end
 
-__device__ __forceinline__ i32x4 make_buffer(uint64_t base, int64_t left) {
-    const int64_t n = left < 0 ? 0 : left > 0x7fffffff ? 0x7fffffff : left;
-    return i32x4{(int)(uint32_t)base, (int)(uint32_t)(base >> 32) & 0xffff, (int)n, 0x00020000};
+// `left` bytes from `base`, less the first `col` (0 or less: none).
+__device__ __forceinline__ i32x4 make_buffer(uint64_t base, int left, int col) {
+    return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)base),
+                 __builtin_amdgcn_readfirstlane((int)(uint32_t)(base >> 32) & 0xffff),
+                 __builtin_amdgcn_readfirstlane(max(0, left - col)), 0x00020000};
 }
 
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
@@ -175,12 +177,22 @@ __device__ __forceinline__ bool find_task(Task& t, const ProductArgs& p, const B
     return false;
 }
 
+constexpr int kRing = 4;    // tasks on their way from the waves that fetch to all
+
 template <bool FP8>
 struct ProductLds {
     uint8_t stage[2][kStage];
     float scales[2][FP8 ? 256 : 1];
     Blocks known;
+    int ring[kRing][8];
 };
+
+// A value that the compiler recomputes from where it is needed rather than hold
+// in registers all along.
+__device__ __forceinline__ uint32_t opaque(uint32_t v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
 
 // 16 rows by 128 bytes as matrix operands, from rows of 128 bytes in LDS.  The
 // 16-byte chunk c of row r lies at place c ^ (r / 2 % 8), so that the 16 lanes
@@ -203,180 +215,165 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>&
     constexpr int kRowsB = 2 * RT * 16;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int group = wave >> 2;
+    const int group = wave >> 2, w4 = wave & 3;
     const int lg = lane >> 4, lr = lane & 15;
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(&lds.stage[0][0]));
     const uint32_t lds_s = FP8 ? __builtin_amdgcn_readfirstlane(lds_offset(&lds.scales[0][0])) : 0;
-    const int64_t a_row = (int64_t)(OP == kRows ? p.K : p.M) * kElem;     // bytes
-    const int64_t b_row = (int64_t)(OP == kGradWeight ? p.B : p.K) * kElem;
+    const uint32_t a_row = (OP == kRows ? p.K : p.M) * kElem;     // bytes
+    const uint32_t b_row = (OP == kGradWeight ? p.B : p.K) * kElem;
+    const int steps_k = (p.K + kStepK - 1) / kStepK;
 
-    // --- what this wave fetches of a step: 1/8 of a's and of b's part ---
-    constexpr int kLoadsA = 4;
-    constexpr int kLoadsB = RT >= 2 ? RT / 2 : 1;
-    uint32_t a_at[kLoadsA], b_at[kLoadsB];
-    int a_col, b_col[2];           // by rows: byte of the step, for the last step's end
-    (void)a_col;
-    (void)b_col;
-#pragma unroll
-    for (int i = 0; i < kLoadsA; ++i) {
-        if constexpr (kAT) {
-            const int k = wave * 8 + i * 2 + (lane >> 5), pos = lane & 31;
-            const int c = (((pos >> 1) ^ column_turn(k)) << 1) | (pos & 1);
-            a_at[i] = (uint32_t)((i * 2 + (lane >> 5)) * a_row) + c * 16;
-        } else {
-            const int r = i * 8 + (lane >> 3), c = (lane & 7) ^ (r >> 1 & 7);
-            a_at[i] = (uint32_t)(r * a_row) + c * 16;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kLoadsB; ++i) {
-        if constexpr (kBT) {
-            const int k = wave * 8 + i * 2 + (lane >> 5), pos = lane & 31;
-            const int c = (((pos >> 1) ^ column_turn(k)) << 1) | (pos & 1);
-            b_at[i] = (uint32_t)((i * 2 + (lane >> 5)) * b_row) + c * 16;
-        } else {
-            const int r = wave * kLoadsB * 8 + i * 8 + (lane >> 3), c = (lane & 7) ^ (r >> 1 & 7);
-            b_at[i] = (uint32_t)((r - wave * kLoadsB * 8) * b_row) + c * 16;
-        }
-    }
+    // --- fetching: the first half's waves, a quarter of a's and of b's part each.
+    // A load takes 1 KiB: 8 rows' 128 bytes, or 2 steps' 256 columns.
+    constexpr int kLoadsA = 8, kLoadsB = RT;
+    // The lane's row (or step) of the first load, and its 16-byte chunk there; in
+    // load i it is chunk ^ chunk_turn(i).
+    auto lane_row = [](bool columns, uint32_t l) { return columns ? l >> 5 : l >> 3; };
+    auto lane_chunk = [](bool columns, uint32_t l) {
+        return columns ? (((l >> 1 & 15) ^ column_turn(l >> 5)) << 5) | (l & 1) << 4
+                       : ((l & 7) ^ l >> 4) << 4;
+    };
+    auto chunk_turn = [](bool columns, int i) {
+        return (uint32_t)((i & 1) * 64 | (columns ? (i >> 2) * 128 : 0));
+    };
 
     struct {
-        bool live;
         int task, step, steps;
         uint64_t a, b, s;
-        int64_t a_left, b_left, s_left;
+        int a_left, b_left, s_left;     // bytes, or by columns steps of k
+        int a_col, b_col;               // by columns: first byte of the row
     } next;
-    auto steps_of = [&](const Task& t) {
-        return OP == kGradWeight ? (t.n + kStepK - 1) / kStepK : (p.K + kStepK - 1) / kStepK;
-    };
-    auto aim = [&](const Task& t) {
-        next.step = 0;
-        next.steps = steps_of(t);
-        if constexpr (OP == kRows) {
-            const int half = SWIGLU ? wave >> 2 : 0;
-            const int c = SWIGLU ? (wave & 3) * 32 : wave * 32;
-            const int64_t w0 = ((int64_t)t.e * (SWIGLU ? 2 : 1) + half) * p.M + t.m0 + c;
-            next.a = (uint64_t)(p.a + w0 * a_row);
-            next.a_left = min((int64_t)32, (int64_t)p.M - t.m0 - c) * a_row;
-        } else if constexpr (OP == kGradRows) {
-            next.a = (uint64_t)(p.a + (((int64_t)t.e * p.K + wave * 8) * a_row + t.m0 * kElem));
-            next.a_left = (int64_t)(p.K - wave * 8) * a_row - t.m0 * kElem;
-        } else {
-            next.a = (uint64_t)(p.a + ((t.begin + wave * 8) * a_row + t.m0 * kElem));
-            next.a_left = (int64_t)(t.n - wave * 8) * a_row - t.m0 * kElem;
-        }
-        if constexpr (OP == kGradWeight) {
-            next.b = (uint64_t)(p.b + ((t.begin + wave * 8) * b_row + t.r0 * kElem));
-            next.b_left = (int64_t)(t.n - wave * 8) * b_row - t.r0 * kElem;
-        } else {
-            const int r = wave * kLoadsB * 8;
-            next.b = (uint64_t)(p.b + (t.begin + t.r0 + r) * b_row);
-            next.b_left = min((int64_t)kLoadsB * 8, (int64_t)t.n - t.r0 - r) * b_row;
-        }
-        if constexpr (FP8) {
-            const int64_t s_row = (int64_t)(p.K / 128) * 4;
-            next.s = (uint64_t)p.bs + (t.begin + t.r0 + wave * 64) * s_row;
-            next.s_left = min((int64_t)64, (int64_t)t.n - t.r0 - wave * 64) * s_row;
-        }
-    };
-    // The first task from next.task on that has steps.
+    int pushed = 0;
+    // Takes the next task up, and tells the others.
     auto seek = [&]() {
         Task t;
-        while (true) {
-            next.live = find_task<OP, RT>(t, p, lds.known, next.task, end, nt, kTile);
-            if (!next.live) return;
-            if (OP != kGradWeight || t.n > 0) break;
-            next.task += stride;
+        const bool live = find_task<OP, RT>(t, p, lds.known, next.task, end, nt, kTile);
+        next.task += stride;
+        if (!live) t.e = -1;
+        if (lane == 0) {
+            int* q = lds.ring[pushed & (kRing - 1)];
+            q[0] = t.e;
+            q[1] = t.m0;
+            q[2] = t.r0;
+            q[3] = t.n;
+            q[4] = (int)t.begin;
         }
-        aim(t);
-    };
-    auto issue = [&](int buf) {
-        if (!next.live) return;
-        const i32x4 ab = make_buffer(next.a, next.a_left), bb = make_buffer(next.b, next.b_left);
-        const uint32_t at = lds0 + buf * kStage;
-        const bool last = next.step == next.steps - 1;
-        // by rows: what of the last step lies past the row's end
-        const int over = last ? p.K * kElem - next.step * kStepBytes : kStepBytes;
-        if (!kBT && over < kStepBytes) {
-#pragma unroll
-            for (int i = 0; i < kLoadsA; ++i) {
-                if constexpr (kAT) {
-                    dma16(a_at[i], ab, at + (wave * kLoadsA + i) * 1024);
-                } else {
-                    const int r = i * 8 + (lane >> 3), c = ((lane & 7) ^ (r >> 1 & 7)) << 4;
-                    dma16(c < over ? a_at[i] : kNowhere, ab, at + (wave * kLoadsA + i) * 1024);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kLoadsB; ++i) {
-                const int r = wave * kLoadsB * 8 + i * 8 + (lane >> 3);
-                const int c = ((lane & 7) ^ (r >> 1 & 7)) << 4;
-                dma16(c < over ? b_at[i] : kNowhere, bb,
-                      at + kABytes + (wave * kLoadsB + i) * 1024);
-            }
+        ++pushed;
+        next.steps = 0;
+        if (!live) return;
+        next.step = 0;
+        next.steps = OP == kGradWeight ? max(1, (t.n + kStepK - 1) / kStepK) : steps_k;
+        if constexpr (OP == kRows) {
+            const int half = SWIGLU ? w4 >> 1 : 0;
+            const int c = SWIGLU ? (w4 & 1) * 64 : w4 * 64;
+            const int64_t w0 = ((int64_t)t.e * (SWIGLU ? 2 : 1) + half) * p.M + t.m0 + c;
+            next.a = (uint64_t)(p.a + w0 * a_row);
+            next.a_left = max(0, min(64, p.M - t.m0 - c)) * (int)a_row;
         } else {
-#pragma unroll
-            for (int i = 0; i < kLoadsA; ++i)
-                dma16(a_at[i], ab, at + (wave * kLoadsA + i) * 1024);
-#pragma unroll
-            for (int i = 0; i < kLoadsB; ++i)
-                dma16(b_at[i], bb, at + kABytes + (wave * kLoadsB + i) * 1024);
+            const int64_t k0 = (OP == kGradRows ? (int64_t)t.e * p.K : t.begin) + w4 * 16;
+            next.a_col = t.m0 * kElem;
+            next.a = (uint64_t)(p.a + k0 * a_row + next.a_col);
+            next.a_left = (OP == kGradRows ? p.K : t.n) - w4 * 16;
+        }
+        if constexpr (OP == kGradWeight) {
+            next.b_col = t.r0 * kElem;
+            next.b = (uint64_t)(p.b + (t.begin + w4 * 16) * b_row + next.b_col);
+            next.b_left = t.n - w4 * 16;
+        } else {
+            const int r = w4 * kLoadsB * 8;
+            next.b = (uint64_t)(p.b + (t.begin + t.r0 + r) * b_row);
+            next.b_left = max(0, min(kLoadsB * 8, t.n - t.r0 - r)) * (int)b_row;
         }
         if constexpr (FP8) {
-            if (wave < (kRowsB + 63) / 64)
-                dma4((uint32_t)(lane * (p.K / 128) * 4), make_buffer(next.s, next.s_left),
-                     lds_s + buf * 1024 + wave * 256);
-            next.s += 4;
-            next.s_left -= 4;
+            const int s_row = p.K / 128 * 4;
+            next.s = (uint64_t)p.bs + (t.begin + t.r0 + w4 * 64) * s_row;
+            next.s_left = max(0, min(64, t.n - t.r0 - w4 * 64)) * s_row;
         }
-        if (last) {
-            next.task += stride;
+    };
+    auto issue = [&](int buf) {
+        if (next.steps == 0) return;
+        auto by_rows = [&](uint64_t base, int left, int col) {
+            return make_buffer(base, left, col);
+        };
+        auto by_steps = [&](uint64_t base, int steps, uint32_t row, int col) {
+            return make_buffer(base, max(0, min(16, steps)) * (int)row, col);
+        };
+        const i32x4 ab = kAT ? by_steps(next.a, next.a_left, a_row, next.a_col)
+                             : by_rows(next.a, next.a_left, 0);
+        const i32x4 bb = kBT ? by_steps(next.b, next.b_left, b_row, next.b_col)
+                             : by_rows(next.b, next.b_left, 0);
+        const uint32_t at = lds0 + buf * kStage;
+        // by rows: what of the last step lies past the row's end
+        const int over = (p.K * kElem) - next.step * kStepBytes;
+        const bool cut = !kBT && over < kStepBytes;
+        const uint32_t l = opaque(lane);
+        const uint32_t ar = __umul24(lane_row(kAT, l), a_row), ac = lane_chunk(kAT, l);
+        const uint32_t br = __umul24(lane_row(kBT, l), b_row), bc = lane_chunk(kBT, l);
+#pragma unroll
+        for (int i = 0; i < kLoadsA; ++i) {
+            const uint32_t c = ac ^ chunk_turn(kAT, i);
+            uint32_t v = ar + c + (uint32_t)i * (kAT ? 2 : 8) * a_row;
+            if (!kAT && cut) v = (int)c < over ? v : kNowhere;
+            dma16(v, ab, at + (w4 * kLoadsA + i) * 1024);
+        }
+#pragma unroll
+        for (int i = 0; i < kLoadsB; ++i) {
+            const uint32_t c = bc ^ chunk_turn(kBT, i);
+            uint32_t v = br + c + (uint32_t)i * (kBT ? 2 : 8) * b_row;
+            if (!kBT && cut) v = (int)c < over ? v : kNowhere;
+            dma16(v, bb, at + kABytes + (w4 * kLoadsB + i) * 1024);
+        }
+        if constexpr (FP8) {
+            if (w4 < (kRowsB + 63) / 64)
+                dma4((uint32_t)(lane * (p.K / 128) * 4), make_buffer(next.s, next.s_left, 0),
+                     lds_s + buf * 1024 + w4 * 256);
+            next.s += 4;
+            next.s_left = max(0, next.s_left - 4);
+        }
+        ++next.step;
+        if (next.step == next.steps) {
             seek();
             return;
         }
-        ++next.step;
-        const int64_t da = kAT ? a_row * kStepK : kStepBytes;
-        const int64_t db = kBT ? b_row * kStepK : kStepBytes;
-        next.a += da;
-        next.a_left -= da;
-        next.b += db;
-        next.b_left -= db;
+        next.a += kAT ? (int64_t)a_row * kStepK : kStepBytes;
+        next.a_left -= kAT ? kStepK : min(kStepBytes, next.a_left);
+        next.b += kBT ? (int64_t)b_row * kStepK : kStepBytes;
+        next.b_left -= kBT ? kStepK : min(kStepBytes, next.b_left);
     };
 
     // --- this wave's results: 64 channels (4 tiles) by RT tiles of rows ---
-    const int wm = wave & 3;
-    const int wr = group;
+    const int wm = w4, wr = group;
     f32x4 acc[4][RT];
     i32x4 af[4][2], bf[RT][2];
     float sx[FP8 ? RT : 1];
-    auto a_tile = [&](int ct) {      // first of the tile's 16 channels in LDS
-        return SWIGLU ? (ct >> 1) * 128 + wm * 32 + (ct & 1) * 16 : wm * 64 + ct * 16;
-    };
-    const uint32_t a_read = row_place((SWIGLU ? wm * 32 : wm * 64) + lr, lg);
-    const uint32_t b_read = row_place(wr * RT * 16 + lr, lg);
-    auto by_columns = [&](const uint8_t* s, int col0, int ks) {
-        // 16 columns from col0 (a multiple of 16), 32 steps of k
-        const int k = lg * 8 + (lr >> 2);
-        const uint32_t at =
-            k * 512 + (((col0 >> 4) ^ column_turn(k)) << 5) + ((lr & 3) << 3) + ks * 32 * 512;
+    // 16 columns of 32 steps of k: lane (lg, lr) holds steps 8 lg .. 8 lg + 7 of
+    // column lr
+    const int k0 = lg * 8 + (lr >> 2);
+    const uint32_t t_read = k0 * 512 + (column_turn(k0) << 5) + ((lr & 3) << 3);
+    const uint32_t r_read = row_place(lr, lg);
+    auto by_columns = [&](const uint8_t* s, uint32_t at, int tile, int ks) {
         typedef __attribute__((address_space(3))) s16x4 L;
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L*)(s + at));
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L*)(s + at + 4 * 512));
+        const uint8_t* q = s + (at ^ tile << 5) + ks * 32 * 512;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L*)q);
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L*)(q + 4 * 512));
         const uint64_t l = __builtin_bit_cast(uint64_t, lo), h = __builtin_bit_cast(uint64_t, hi);
         return i32x4{(int)(uint32_t)l, (int)(uint32_t)(l >> 32), (int)(uint32_t)h,
                      (int)(uint32_t)(h >> 32)};
     };
     auto read = [&](int buf) {
         const uint8_t* s = lds.stage[buf];
+        const uint32_t ta = opaque(t_read), ra = opaque(r_read);
+        const uint8_t* sa = s + (SWIGLU ? wm * 32 : wm * 64) * kStepBytes;
+        const uint8_t* sb = s + kABytes + wr * RT * 16 * kStepBytes;
 #pragma unroll
         for (int ct = 0; ct < 4; ++ct)
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
                 if constexpr (kAT)
-                    af[ct][ks] = by_columns(s, a_tile(ct), ks);
+                    af[ct][ks] = by_columns(s, ta, wm * 4 + ct, ks);
                 else
                     af[ct][ks] = *reinterpret_cast<const i32x4*>(
-                        s + (a_read ^ ks * 64) +
+                        sa + (ra ^ ks * 64) +
                         (SWIGLU ? (ct >> 1) * 128 + (ct & 1) * 16 : ct * 16) * kStepBytes);
             }
 #pragma unroll
@@ -384,24 +381,22 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>&
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
                 if constexpr (kBT)
-                    bf[rt][ks] = by_columns(s + kABytes, (wr * RT + rt) * 16, ks);
+                    bf[rt][ks] = by_columns(s + kABytes, ta, wr * RT + rt, ks);
                 else
-                    bf[rt][ks] = *reinterpret_cast<const i32x4*>(
-                        s + kABytes + (b_read ^ ks * 64) + rt * 16 * kStepBytes);
+                    bf[rt][ks] = *reinterpret_cast<const i32x4*>(sb + (ra ^ ks * 64) +
+                                                                 rt * 16 * kStepBytes);
             }
         if constexpr (FP8) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) sx[rt] = lds.scales[buf][(wr * RT + rt) * 16 + lr];
         }
     };
-    auto multiply = [&](const float* as, int step) {
+    auto multiply = [&](float s0, float s1) {
         if constexpr (FP8) {
-            const int KB = p.K / 128, NB = (p.M + 127) / 128;
-            const float s0 = as[step], s1 = SWIGLU ? as[(int64_t)NB * KB + step] : s0;
             const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                const float g = sx[rt] * s0, u = sx[rt] * s1;
+                const float g = sx[rt] * s0, u = SWIGLU ? sx[rt] * s1 : g;
                 i32x8 b;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) b[i] = bf[rt][i / 4][i % 4];
@@ -464,24 +459,35 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>&
     // Waves 0..3 and 4..7, one of each on a SIMD, take turns: while one half
     // multiplies a step, the other reads its operands.  A step's bytes are asked
     // for as soon as every wave has read the step that lay there before.
-    next.task = task;
-    seek();
     int buf = 0;
-    issue(0);
-    EP_WAIT_DMA();
-    barrier();
-    if (group == 1) {
-        issue(1);
-        barrier();
+    if (group == 0) {
+        next.task = task;
+        seek();
+        issue(0);
+        EP_WAIT_DMA();
+        EP_WAIT_LDS();
     }
-    Task t;
-    for (; find_task<OP, RT>(t, p, lds.known, task, end, nt, kTile); task += stride) {
-        const int steps = steps_of(t);
-        const float* as = nullptr;
+    barrier();
+    if (group == 1) barrier();
+#pragma unroll 1
+    for (int taken = 0;; ++taken) {
+        const int* q = lds.ring[taken & (kRing - 1)];
+        Task t;
+        t.e = __builtin_amdgcn_readfirstlane(q[0]);
+        if (t.e < 0) break;
+        t.m0 = __builtin_amdgcn_readfirstlane(q[1]);
+        t.r0 = __builtin_amdgcn_readfirstlane(q[2]);
+        t.n = __builtin_amdgcn_readfirstlane(q[3]);
+        t.begin = __builtin_amdgcn_readfirstlane(q[4]);
+        const int steps = OP == kGradWeight ? max(1, (t.n + kStepK - 1) / kStepK) : steps_k;
+        typedef const __attribute__((address_space(4))) float* Scalars;
+        Scalars as0 = nullptr, as1 = nullptr;
         if constexpr (FP8) {
             const int KB = p.K / 128, NB = (p.M + 127) / 128;
             const int c = t.m0 + (SWIGLU ? wm * 32 : wm * 64);
-            as = p.as + ((int64_t)t.e * (SWIGLU ? 2 : 1) * NB + min(c / 128, NB - 1)) * KB;
+            as0 = (Scalars)(uint64_t)(p.as + ((int64_t)t.e * (SWIGLU ? 2 : 1) * NB +
+                                              min(c / 128, NB - 1)) * KB);
+            as1 = as0 + (int64_t)NB * KB;
         }
 #pragma unroll
         for (int ct = 0; ct < 4; ++ct)
@@ -489,15 +495,12 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>&
             for (int rt = 0; rt < RT; ++rt) acc[ct][rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
         for (int step = 0; step < steps; ++step, buf ^= 1) {
+            const float s0 = FP8 ? as0[step] : 0.0f, s1 = FP8 && SWIGLU ? as1[step] : 0.0f;
             read(buf);
-            if (group == 0)
-                issue(buf ^ 1);
-            else
-                EP_WAIT_DMA();
+            if (group == 0) issue(buf ^ 1);
             EP_WAIT_LDS();
             barrier();
-            if (group == 1) issue(buf);
-            multiply(as, step);
+            multiply(s0, s1);
             if (group == 0) EP_WAIT_DMA();
             barrier();
         }
