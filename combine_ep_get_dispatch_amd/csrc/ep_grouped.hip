@@ -39,8 +39,7 @@ constexpr int kTileM = 256;
 constexpr int kStepBytes = 128;
 constexpr int kWaves = 8;
 constexpr int kABytes = kTileM * kStepBytes;
-constexpr int kStage = 2 * kABytes;
-
+constexpr int kBHalf = kABytes / 2;
 
 // 16 (or 4) bytes per lane from a bounded buffer to LDS, lane after lane; what
 // lies past the buffer's end arrives as zeros.  Waited for by vmcnt; the
@@ -71,7 +70,11 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 }
 
 #define EP_WAIT_LDS() asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory")
-#define EP_WAIT_DMA() asm volatile("s_waitcnt vmcnt(0)" ::: "memory")
+// Waits until at most N loads to LDS (and stores) are still on their way.
+template <int N>
+__device__ __forceinline__ void wait_dma() {
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
 
 __device__ __forceinline__ void barrier() {
     __builtin_amdgcn_sched_barrier(0);
@@ -177,14 +180,15 @@ __device__ __forceinline__ bool find_task(Task& t, const ProductArgs& p, const B
     return false;
 }
 
-constexpr int kRing = 4;    // tasks on their way from the waves that fetch to all
+constexpr int kRing = 4;    // tasks that a wave's fetching is ahead of its sums, at most
 
 template <bool FP8>
 struct ProductLds {
-    uint8_t stage[2][kStage];
-    float scales[2][FP8 ? 256 : 1];
+    uint8_t a[2][kABytes];
+    uint8_t b[2][2][kBHalf];      // of a step: each half of the waves' first and second tiles
+    float scales[4][FP8 ? 256 : 1];
     Blocks known;
-    int ring[kRing][8];
+    int ring[2][kRing][8];
 };
 
 // A value that the compiler recomputes from where it is needed rather than hold
@@ -212,218 +216,275 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>&
     constexpr bool kBT = OP == kGradWeight;
     constexpr int kElem = FP8 ? 1 : 2;
     constexpr int kStepK = kStepBytes / kElem;
-    constexpr int kRowsB = 2 * RT * 16;
+    constexpr int HT = RT / 2;                             // row tiles of a half
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int group = wave >> 2, w4 = wave & 3;
     const int lg = lane >> 4, lr = lane & 15;
-    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(&lds.stage[0][0]));
+    const uint32_t lds_a = __builtin_amdgcn_readfirstlane(lds_offset(&lds.a[0][0]));
+    const uint32_t lds_b = __builtin_amdgcn_readfirstlane(lds_offset(&lds.b[0][0][0]));
     const uint32_t lds_s = FP8 ? __builtin_amdgcn_readfirstlane(lds_offset(&lds.scales[0][0])) : 0;
     const uint32_t a_row = (OP == kRows ? p.K : p.M) * kElem;     // bytes
     const uint32_t b_row = (OP == kGradWeight ? p.B : p.K) * kElem;
     const int steps_k = (p.K + kStepK - 1) / kStepK;
 
-    // --- fetching: the first half's waves, a quarter of a's and of b's part each.
-    // A load takes 1 KiB: 8 rows' 128 bytes, or 2 steps' 256 columns.
-    constexpr int kLoadsA = 8, kLoadsB = RT;
-    // The lane's row (or step) of the first load, and its 16-byte chunk there; in
-    // load i it is chunk ^ chunk_turn(i).
-    auto lane_row = [](bool columns, uint32_t l) { return columns ? l >> 5 : l >> 3; };
-    auto lane_chunk = [](bool columns, uint32_t l) {
-        return columns ? (((l >> 1 & 15) ^ column_turn(l >> 5)) << 5) | (l & 1) << 4
-                       : ((l & 7) ^ l >> 4) << 4;
-    };
-    auto chunk_turn = [](bool columns, int i) {
-        return (uint32_t)((i & 1) * 64 | (columns ? (i >> 2) * 128 : 0));
-    };
-
+    // --- fetching: waves 0..3 a quarter of a's part of a step each, waves 4..7
+    // of b's.  A load takes 1 KiB: 8 rows' 128 bytes, 2 steps' 256 or 4 steps' 128
+    // columns.
+    constexpr int kLoadsA = 8, kLoadsB = HT;      // of b: a half
     struct {
         int task, step, steps;
-        uint64_t a, b, s;
-        int a_left, b_left, s_left;     // bytes, or by columns steps of k
-        int a_col, b_col;               // by columns: first byte of the row
+        uint64_t at, s;
+        int left, s_left;       // bytes of the rows, or by columns steps of k
+        int col;                // by columns: first byte of the row
     } next;
-    int pushed = 0;
-    // Takes the next task up, and tells the others.
+    int pushed = 0, fetched = 0;                  // tasks; steps whose fetching has begun
     auto seek = [&]() {
         Task t;
         const bool live = find_task<OP, RT>(t, p, lds.known, next.task, end, nt, kTile);
         next.task += stride;
-        if (!live) t.e = -1;
         if (lane == 0) {
-            int* q = lds.ring[pushed & (kRing - 1)];
-            q[0] = t.e;
+            int* q = lds.ring[group][pushed & (kRing - 1)];
+            q[0] = live ? t.e : -1;
             q[1] = t.m0;
             q[2] = t.r0;
             q[3] = t.n;
             q[4] = (int)t.begin;
         }
         ++pushed;
-        next.steps = 0;
-        if (!live) return;
         next.step = 0;
+        next.steps = 0x7fffffff;                  // after the last task: nothing, for good
+        next.left = next.s_left = 0;
+        next.col = 0;
+        next.at = next.s = (uint64_t)p.a;
+        if (!live) return;
         next.steps = OP == kGradWeight ? max(1, (t.n + kStepK - 1) / kStepK) : steps_k;
-        if constexpr (OP == kRows) {
-            const int half = SWIGLU ? w4 >> 1 : 0;
-            const int c = SWIGLU ? (w4 & 1) * 64 : w4 * 64;
-            const int64_t w0 = ((int64_t)t.e * (SWIGLU ? 2 : 1) + half) * p.M + t.m0 + c;
-            next.a = (uint64_t)(p.a + w0 * a_row);
-            next.a_left = max(0, min(64, p.M - t.m0 - c)) * (int)a_row;
+        if (group == 0) {
+            if constexpr (OP == kRows) {
+                const int half = SWIGLU ? w4 >> 1 : 0;
+                const int c = SWIGLU ? (w4 & 1) * 64 : w4 * 64;
+                const int64_t w0 = ((int64_t)t.e * (SWIGLU ? 2 : 1) + half) * p.M + t.m0 + c;
+                next.at = (uint64_t)(p.a + w0 * a_row);
+                next.left = max(0, min(64, p.M - t.m0 - c)) * (int)a_row;
+            } else {
+                const int64_t k0 = (OP == kGradRows ? (int64_t)t.e * p.K : t.begin) + w4 * 16;
+                next.col = t.m0 * kElem;
+                next.at = (uint64_t)(p.a + k0 * a_row + next.col);
+                next.left = (OP == kGradRows ? p.K : t.n) - w4 * 16;
+            }
+        } else if constexpr (kBT) {
+            next.col = t.r0 * kElem;
+            next.at = (uint64_t)(p.b + (t.begin + w4 * 16) * b_row + next.col);
+            next.left = t.n - w4 * 16;
         } else {
-            const int64_t k0 = (OP == kGradRows ? (int64_t)t.e * p.K : t.begin) + w4 * 16;
-            next.a_col = t.m0 * kElem;
-            next.a = (uint64_t)(p.a + k0 * a_row + next.a_col);
-            next.a_left = (OP == kGradRows ? p.K : t.n) - w4 * 16;
-        }
-        if constexpr (OP == kGradWeight) {
-            next.b_col = t.r0 * kElem;
-            next.b = (uint64_t)(p.b + (t.begin + w4 * 16) * b_row + next.b_col);
-            next.b_left = t.n - w4 * 16;
-        } else {
-            const int r = w4 * kLoadsB * 8;
-            next.b = (uint64_t)(p.b + (t.begin + t.r0 + r) * b_row);
-            next.b_left = max(0, min(kLoadsB * 8, t.n - t.r0 - r)) * (int)b_row;
-        }
-        if constexpr (FP8) {
-            const int s_row = p.K / 128 * 4;
-            next.s = (uint64_t)p.bs + (t.begin + t.r0 + w4 * 64) * s_row;
-            next.s_left = max(0, min(64, t.n - t.r0 - w4 * 64)) * s_row;
+            // rows of this wave's part of the first half; those of the second lie 16 HT on
+            const int r = t.r0 + (w4 >> 1) * RT * 16 + (w4 & 1) * HT * 8;
+            next.at = (uint64_t)(p.b + (t.begin + r) * b_row);
+            next.left = (t.n - r) * (int64_t)b_row > 0x7fffffff ? 0x7fffffff
+                                                                : max(0, t.n - r) * (int)b_row;
+            if constexpr (FP8) {
+                const int s_row = p.K / 128 * 4;
+                next.s = (uint64_t)p.bs + (t.begin + t.r0 + w4 * 64) * s_row;
+                next.s_left = max(0, min(64, t.n - t.r0 - w4 * 64)) * s_row;
+            }
         }
     };
-    auto issue = [&](int buf) {
-        if (next.steps == 0) return;
-        auto by_rows = [&](uint64_t base, int left, int col) {
-            return make_buffer(base, left, col);
-        };
-        auto by_steps = [&](uint64_t base, int steps, uint32_t row, int col) {
-            return make_buffer(base, max(0, min(16, steps)) * (int)row, col);
-        };
-        const i32x4 ab = kAT ? by_steps(next.a, next.a_left, a_row, next.a_col)
-                             : by_rows(next.a, next.a_left, 0);
-        const i32x4 bb = kBT ? by_steps(next.b, next.b_left, b_row, next.b_col)
-                             : by_rows(next.b, next.b_left, 0);
-        const uint32_t at = lds0 + buf * kStage;
-        // by rows: what of the last step lies past the row's end
-        const int over = (p.K * kElem) - next.step * kStepBytes;
-        const bool cut = !kBT && over < kStepBytes;
-        const uint32_t l = opaque(lane);
-        const uint32_t ar = __umul24(lane_row(kAT, l), a_row), ac = lane_chunk(kAT, l);
-        const uint32_t br = __umul24(lane_row(kBT, l), b_row), bc = lane_chunk(kBT, l);
-#pragma unroll
-        for (int i = 0; i < kLoadsA; ++i) {
-            const uint32_t c = ac ^ chunk_turn(kAT, i);
-            uint32_t v = ar + c + (uint32_t)i * (kAT ? 2 : 8) * a_row;
-            if (!kAT && cut) v = (int)c < over ? v : kNowhere;
-            dma16(v, ab, at + (w4 * kLoadsA + i) * 1024);
-        }
-#pragma unroll
-        for (int i = 0; i < kLoadsB; ++i) {
-            const uint32_t c = bc ^ chunk_turn(kBT, i);
-            uint32_t v = br + c + (uint32_t)i * (kBT ? 2 : 8) * b_row;
-            if (!kBT && cut) v = (int)c < over ? v : kNowhere;
-            dma16(v, bb, at + kABytes + (w4 * kLoadsB + i) * 1024);
-        }
-        if constexpr (FP8) {
-            if (w4 < (kRowsB + 63) / 64)
-                dma4((uint32_t)(lane * (p.K / 128) * 4), make_buffer(next.s, next.s_left, 0),
-                     lds_s + buf * 1024 + w4 * 256);
-            next.s += 4;
-            next.s_left = max(0, next.s_left - 4);
-        }
-        ++next.step;
-        if (next.step == next.steps) {
+    auto advance = [&](bool columns, uint32_t row) {
+        if (++next.step == next.steps) {
             seek();
             return;
         }
-        next.a += kAT ? (int64_t)a_row * kStepK : kStepBytes;
-        next.a_left -= kAT ? kStepK : min(kStepBytes, next.a_left);
-        next.b += kBT ? (int64_t)b_row * kStepK : kStepBytes;
-        next.b_left -= kBT ? kStepK : min(kStepBytes, next.b_left);
+        next.at += columns ? (int64_t)row * kStepK : kStepBytes;
+        next.left -= columns ? kStepK : min(kStepBytes, next.left);
     };
+    // 1 KiB loads of one operand, `loads` of them; `turn` is what the LDS row of the
+    // first one adds to the places of its chunks.
+    auto fetch = [&](auto columns_, auto loads_, int cols, uint32_t row, const i32x4& buffer,
+                     uint32_t at, uint32_t turn) {
+        constexpr bool columns = decltype(columns_)::value;
+        constexpr int loads = decltype(loads_)::value;
+        const uint32_t l = opaque(lane);
+        const int over = columns ? kStepBytes : p.K * kElem - next.step * kStepBytes;
+        uint32_t r, c, per;
+        if (columns) {
+            // a step's columns: 16 chunks of 32 bytes (256 columns) or 8
+            const uint32_t lanes = cols == 256 ? 5 : 4, pos = l & ((1u << lanes) - 1);
+            r = l >> lanes;
+            per = cols == 256 ? 2 : 4;
+            c = (((pos >> 1) ^ column_turn(r)) << 5) | (pos & 1) << 4;
+        } else {
+            r = l >> 3;
+            per = 8;
+            c = (((l & 7) ^ l >> 4) << 4) ^ turn;
+        }
+        r = __umul24(r, row);
+#pragma unroll
+        for (int i = 0; i < loads; ++i) {
+            // load i's rows are `per` i further: their turns, in bytes
+            const uint32_t k = i * per;
+            const uint32_t ci = c ^ (columns ? column_turn(k) << 5 : (k >> 1 & 7) << 4);
+            // 128 of 256 columns: the second wave row's lie 128 columns on
+            uint32_t v = r + ci + k * row;
+            if (columns && cols == 128) v += ci & 128;
+            if (!columns && over < kStepBytes) v = (int)ci < over ? v : kNowhere;
+            dma16(v, buffer, at + i * 1024);
+        }
+    };
+    auto issue_a = [&]() {
+        const i32x4 buffer =
+            kAT ? make_buffer(next.at, max(0, min(16, next.left)) * (int)a_row, next.col)
+                : make_buffer(next.at, next.left, 0);
+        fetch(std::integral_constant<bool, kAT>{}, std::integral_constant<int, kLoadsA>{}, 256,
+              a_row, buffer, lds_a + (fetched & 1) * kABytes + w4 * kLoadsA * 1024, 0);
+        ++fetched;
+        advance(kAT, a_row);
+    };
+    auto issue_b = [&](int half) {
+        i32x4 buffer;
+        if constexpr (kBT) {
+            const int more = half * 128;         // bytes: 64 columns
+            buffer = make_buffer(next.at + more, max(0, min(16, next.left)) * (int)b_row,
+                                 next.col + more);
+        } else {
+            const int more = half * HT * 16 * (int)b_row;
+            buffer = make_buffer(next.at + more, min(next.left - more, HT * 8 * (int)b_row), 0);
+        }
+        fetch(std::integral_constant<bool, kBT>{}, std::integral_constant<int, kLoadsB>{}, 128,
+              b_row, buffer, lds_b + ((fetched & 1) * 2 + half) * kBHalf + w4 * kLoadsB * 1024,
+              HT == 1 ? (w4 & 1) * 64 : 0);
+        if constexpr (FP8) {
+            if (half == 0) {
+                dma4((uint32_t)(lane * (p.K / 128) * 4), make_buffer(next.s, next.s_left, 0),
+                     lds_s + (fetched & 3) * 1024 + w4 * 256);
+                next.s += 4;
+                next.s_left = max(0, next.s_left - 4);
+            }
+        }
+        if (half == 1) {
+            ++fetched;
+            advance(kBT, b_row);
+        }
+    };
+    // loads of a step that may be on their way while an older part has to be there
+    constexpr int kAheadA = kLoadsA, kAheadB = 2 * kLoadsB + (FP8 ? 1 : 0);
 
     // --- this wave's results: 64 channels (4 tiles) by RT tiles of rows ---
     const int wm = w4, wr = group;
     f32x4 acc[4][RT];
-    i32x4 af[4][2], bf[RT][2];
-    float sx[FP8 ? RT : 1];
+    i32x4 af[4][2], bf[HT][2];
+    float sx[FP8 ? HT : 1];
     // 16 columns of 32 steps of k: lane (lg, lr) holds steps 8 lg .. 8 lg + 7 of
     // column lr
-    const int k0 = lg * 8 + (lr >> 2);
-    const uint32_t t_read = k0 * 512 + (column_turn(k0) << 5) + ((lr & 3) << 3);
-    const uint32_t r_read = row_place(lr, lg);
-    auto by_columns = [&](const uint8_t* s, uint32_t at, int tile, int ks) {
+    auto by_columns = [&](const uint8_t* s, int row, uint32_t at, int tile, int ks) {
         typedef __attribute__((address_space(3))) s16x4 L;
-        const uint8_t* q = s + (at ^ tile << 5) + ks * 32 * 512;
+        const uint8_t* q = s + (at ^ tile << 5) + ks * 32 * row;
         const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L*)q);
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L*)(q + 4 * 512));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L*)(q + 4 * row));
         const uint64_t l = __builtin_bit_cast(uint64_t, lo), h = __builtin_bit_cast(uint64_t, hi);
         return i32x4{(int)(uint32_t)l, (int)(uint32_t)(l >> 32), (int)(uint32_t)h,
                      (int)(uint32_t)(h >> 32)};
     };
-    auto read = [&](int buf) {
-        const uint8_t* s = lds.stage[buf];
-        const uint32_t ta = opaque(t_read), ra = opaque(r_read);
-        const uint8_t* sa = s + (SWIGLU ? wm * 32 : wm * 64) * kStepBytes;
-        const uint8_t* sb = s + kABytes + wr * RT * 16 * kStepBytes;
+    auto lane_columns = [&](int row) {
+        const uint32_t l = opaque(lane), k = (l >> 4) * 8 + (l >> 2 & 3);
+        return k * row + (column_turn(k) << 5) + ((l & 3) << 3);
+    };
+    auto lane_rows = [&]() {
+        const uint32_t l = opaque(lane);
+        return row_place(l & 15, l >> 4);
+    };
+    auto read_a = [&](int buf) {
+        const uint8_t* s = lds.a[buf];
+        if constexpr (kAT) {
+            const uint32_t at = lane_columns(512);
 #pragma unroll
-        for (int ct = 0; ct < 4; ++ct)
+            for (int ct = 0; ct < 4; ++ct)
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                if constexpr (kAT)
-                    af[ct][ks] = by_columns(s, ta, wm * 4 + ct, ks);
-                else
+                for (int ks = 0; ks < 2; ++ks)
+                    af[ct][ks] = by_columns(s, 512, at, wm * 4 + ct, ks);
+        } else {
+            const uint32_t at = lane_rows();
+            s += (SWIGLU ? wm * 32 : wm * 64) * kStepBytes;
+#pragma unroll
+            for (int ct = 0; ct < 4; ++ct)
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks)
                     af[ct][ks] = *reinterpret_cast<const i32x4*>(
-                        sa + (ra ^ ks * 64) +
+                        s + (at ^ ks * 64) +
                         (SWIGLU ? (ct >> 1) * 128 + (ct & 1) * 16 : ct * 16) * kStepBytes);
-            }
+        }
+    };
+    auto read_b = [&](int buf, int half, int step) {
+        const uint8_t* s = lds.b[buf][half];
+        const uint32_t at = kBT ? lane_columns(256) : lane_rows();
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
+        for (int rt = 0; rt < HT; ++rt)
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
                 if constexpr (kBT)
-                    bf[rt][ks] = by_columns(s + kABytes, ta, wr * RT + rt, ks);
+                    bf[rt][ks] = by_columns(s, 256, at, wr * HT + rt, ks);
                 else
-                    bf[rt][ks] = *reinterpret_cast<const i32x4*>(sb + (ra ^ ks * 64) +
-                                                                 rt * 16 * kStepBytes);
+                    bf[rt][ks] = *reinterpret_cast<const i32x4*>(
+                        s + (at ^ ks * 64) + (wr * HT + rt) * 16 * kStepBytes);
             }
         if constexpr (FP8) {
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) sx[rt] = lds.scales[buf][(wr * RT + rt) * 16 + lr];
+            for (int rt = 0; rt < HT; ++rt)
+                sx[rt] = lds.scales[step & 3][(wr * RT + half * HT + rt) * 16 + lr];
         }
     };
-    auto multiply = [&](float s0, float s1) {
+    auto multiply = [&](auto half_, float s0, float s1) {
+        constexpr int r0 = decltype(half_)::value * HT;
         if constexpr (FP8) {
             const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+            // a tile's 128 channels are scaled into its sums while the next tiles are
+            // multiplied
+            constexpr int kLate = 2;
+            f32x4 part[kLate + 1];
+            float g[HT], u[HT];
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                const float g = sx[rt] * s0, u = SWIGLU ? sx[rt] * s1 : g;
-                i32x8 b;
+            for (int rt = 0; rt < HT; ++rt) {
+                g[rt] = sx[rt] * s0;
+                u[rt] = SWIGLU ? sx[rt] * s1 : g[rt];
+            }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) b[i] = bf[rt][i / 4][i % 4];
+            for (int i = 0; i < 4 * HT + kLate; ++i) {
+                if (i < 4 * HT) {
+                    const int rt = i / 4, ct = i % 4;
+                    i32x8 a, b;
 #pragma unroll
-                for (int ct = 0; ct < 4; ++ct) {
-                    i32x8 a;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) a[i] = af[ct][i / 4][i % 4];
-                    const f32x4 t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    for (int j = 0; j < 8; ++j) {
+                        a[j] = af[ct][j / 4][j % 4];
+                        b[j] = bf[rt][j / 4][j % 4];
+                    }
+                    part[i % (kLate + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                         a, b, zero, 0, 0, 0, 127, 0, 127);
-                    const float sc = SWIGLU && ct >= 2 ? u : g;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc[ct][rt][i] = __builtin_fmaf(t[i], sc, acc[ct][rt][i]);
                 }
+                if (i >= kLate) {
+                    const int rt = (i - kLate) / 4, ct = (i - kLate) % 4;
+                    const f32x4 t = part[(i - kLate) % (kLate + 1)];
+                    const float sc = SWIGLU && ct >= 2 ? u[rt] : g[rt];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        acc[ct][r0 + rt][j] = __builtin_fmaf(t[j], sc, acc[ct][r0 + rt][j]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
         } else {
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
+                for (int rt = 0; rt < HT; ++rt)
 #pragma unroll
                     for (int ct = 0; ct < 4; ++ct)
-                        acc[ct][rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        acc[ct][r0 + rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                             __builtin_bit_cast(bf16x8, af[ct][ks]),
-                            __builtin_bit_cast(bf16x8, bf[rt][ks]), acc[ct][rt], 0, 0, 0);
+                            __builtin_bit_cast(bf16x8, bf[rt][ks]), acc[ct][r0 + rt], 0, 0, 0);
         }
+        // done here, not where the sums are next used
+#pragma unroll
+        for (int rt = 0; rt < HT; ++rt)
+#pragma unroll
+            for (int ct = 0; ct < 4; ++ct) asm volatile("" : "+v"(acc[ct][r0 + rt]));
     };
     auto store = [&](const Task& t) {
         const int rows = OP == kGradWeight ? p.B : t.n;
@@ -457,21 +518,33 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>&
 
     // --- the steps ---
     // Waves 0..3 and 4..7, one of each on a SIMD, take turns: while one half
-    // multiplies a step, the other reads its operands.  A step's bytes are asked
-    // for as soon as every wave has read the step that lay there before.
-    int buf = 0;
+    // multiplies, the other reads its next operands, a's and half of b's tiles,
+    // then the other half of b's.  Phases of step t, four to each half of the
+    // waves, the second half's one later: read a and b's first tiles, multiply,
+    // read b's second tiles, multiply.  What lay in a place is asked for anew once
+    // all waves have read it:
+    //   a(t + 2)           in the first half's phase 3 of t,  needed six phases later;
+    //   b's first (t + 2)  in the second half's phase 3 of t, needed five later;
+    //   b's second (t + 1) in the second half's phase 1 of t, needed five later.
+    next.task = task;
+    seek();
     if (group == 0) {
-        next.task = task;
-        seek();
-        issue(0);
-        EP_WAIT_DMA();
-        EP_WAIT_LDS();
+        issue_a();
+        issue_a();
+        wait_dma<kAheadA>();
+    } else {
+        issue_b(0);
+        issue_b(1);
+        issue_b(0);
+        wait_dma<kAheadB>();
     }
+    EP_WAIT_LDS();
     barrier();
     if (group == 1) barrier();
+    int turn = 0;
 #pragma unroll 1
     for (int taken = 0;; ++taken) {
-        const int* q = lds.ring[taken & (kRing - 1)];
+        const int* q = lds.ring[group][taken & (kRing - 1)];
         Task t;
         t.e = __builtin_amdgcn_readfirstlane(q[0]);
         if (t.e < 0) break;
@@ -494,20 +567,36 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>&
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) acc[ct][rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
-        for (int step = 0; step < steps; ++step, buf ^= 1) {
+        for (int step = 0; step < steps; ++step, ++turn) {
             const float s0 = FP8 ? as0[step] : 0.0f, s1 = FP8 && SWIGLU ? as1[step] : 0.0f;
-            read(buf);
-            if (group == 0) issue(buf ^ 1);
+            read_a(turn & 1);
+            read_b(turn & 1, 0, turn);
+            if (group == 1) {
+                issue_b(1);
+                wait_dma<kAheadB>();
+            }
             EP_WAIT_LDS();
             barrier();
-            multiply(s0, s1);
-            if (group == 0) EP_WAIT_DMA();
+            multiply(std::integral_constant<int, 0>{}, s0, s1);
+            barrier();
+            read_b(turn & 1, 1, turn);
+            if (group == 0) {
+                issue_a();
+            } else {
+                issue_b(0);
+                wait_dma<kAheadB>();
+            }
+            EP_WAIT_LDS();
+            barrier();
+            multiply(std::integral_constant<int, 1>{}, s0, s1);
+            if (group == 0) wait_dma<kAheadA>();
             barrier();
         }
         if (OP == kGradWeight && ADD && t.n == 0) continue;
         store(t);
     }
     if (group == 0) barrier();
+    wait_dma<0>();
     barrier();
 }
 
