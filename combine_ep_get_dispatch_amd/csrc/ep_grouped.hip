@@ -41,14 +41,37 @@ constexpr int kWaves = 8;
 constexpr int kABytes = kTileM * kStepBytes;
 constexpr int kBHalf = kABytes / 2;
 
-// 16 (or 4) bytes per lane from a bounded buffer to LDS, lane after lane; what
-// lies past the buffer's end arrives as zeros.  Waited for by vmcnt; the
-// compiler does not count it.
-__device__ __forceinline__ void dma16(uint32_t at, const i32x4& buffer, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-                 :
-                 : "v"(at), "s"(buffer), "s"(lds)
-                 : "memory");
+// 16 (or 4) bytes per lane from a bounded buffer to LDS, lane after lane, N loads
+// one after the other; what lies past the buffer's end arrives as zeros.  A load's
+// place i * 1024 counts in both memories, so `at` holds what is missing from
+// kShift, which the buffer's base makes up for.  Waited for by vmcnt; the compiler
+// does not count it.
+constexpr int kShift = 3072;
+template <int N>
+__device__ __forceinline__ void dma16(const uint32_t* at, const i32x4& buffer, uint32_t lds) {
+    if constexpr (N == 4)
+        asm volatile(
+            "s_mov_b32 m0, %5\n\ts_nop 0\n\t"
+            "buffer_load_dwordx4 %0, %4, 0 offen lds\n\t"
+            "buffer_load_dwordx4 %1, %4, 0 offen offset:1024 lds\n\t"
+            "buffer_load_dwordx4 %2, %4, 0 offen offset:2048 lds\n\t"
+            "buffer_load_dwordx4 %3, %4, 0 offen offset:3072 lds"
+            :
+            : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "s"(buffer), "s"(lds)
+            : "memory");
+    else if constexpr (N == 2)
+        asm volatile(
+            "s_mov_b32 m0, %3\n\ts_nop 0\n\t"
+            "buffer_load_dwordx4 %0, %2, 0 offen lds\n\t"
+            "buffer_load_dwordx4 %1, %2, 0 offen offset:1024 lds"
+            :
+            : "v"(at[0]), "v"(at[1]), "s"(buffer), "s"(lds)
+            : "memory");
+    else
+        asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+                     :
+                     : "v"(at[0]), "s"(buffer), "s"(lds)
+                     : "memory");
 }
 __device__ __forceinline__ void dma4(uint32_t at, const i32x4& buffer, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
@@ -58,11 +81,12 @@ __device__ __forceinline__ void dma4(uint32_t at, const i32x4& buffer, uint32_t 
 }
 constexpr uint32_t kNowhere = 0x80000000u;   // past every buffer's end
 
-// `left` bytes from `base`, less the first `col` (0 or less: none).
-__device__ __forceinline__ i32x4 make_buffer(uint64_t base, int left, int col) {
+// `size` bytes (0 or less: none) from `base`, which the loads reach at kShift.
+__device__ __forceinline__ i32x4 make_buffer(uint64_t base, int size, int shift = kShift) {
+    base -= shift;
     return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)base),
                  __builtin_amdgcn_readfirstlane((int)(uint32_t)(base >> 32) & 0xffff),
-                 __builtin_amdgcn_readfirstlane(max(0, left - col)), 0x00020000};
+                 __builtin_amdgcn_readfirstlane(max(0, size) + shift), 0x00020000};
 }
 
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
@@ -280,8 +304,7 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>&
             // rows of this wave's part of the first half; those of the second lie 16 HT on
             const int r = t.r0 + (w4 >> 1) * RT * 16 + (w4 & 1) * HT * 8;
             next.at = (uint64_t)(p.b + (t.begin + r) * b_row);
-            next.left = (t.n - r) * (int64_t)b_row > 0x7fffffff ? 0x7fffffff
-                                                                : max(0, t.n - r) * (int)b_row;
+            next.left = (int)min((int64_t)max(0, t.n - r) * b_row, (int64_t)0x7fff0000);
             if constexpr (FP8) {
                 const int s_row = p.K / 128 * 4;
                 next.s = (uint64_t)p.bs + (t.begin + t.r0 + w4 * 64) * s_row;
@@ -297,61 +320,77 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>&
         next.at += columns ? (int64_t)row * kStepK : kStepBytes;
         next.left -= columns ? kStepK : min(kStepBytes, next.left);
     };
-    // 1 KiB loads of one operand, `loads` of them; `turn` is what the LDS row of the
-    // first one adds to the places of its chunks.
-    auto fetch = [&](auto columns_, auto loads_, int cols, uint32_t row, const i32x4& buffer,
-                     uint32_t at, uint32_t turn) {
-        constexpr bool columns = decltype(columns_)::value;
-        constexpr int loads = decltype(loads_)::value;
-        const uint32_t l = opaque(lane);
-        const int over = columns ? kStepBytes : p.K * kElem - next.step * kStepBytes;
-        uint32_t r, c, per;
+    // The lane's places of a part's loads (a's or of a half of b's), less their kShift.
+    uint32_t at[kLoadsA];
+    auto chunk = [&](bool columns, int lanes, int i) {
+        const uint32_t l = lane;
         if (columns) {
-            // a step's columns: 16 chunks of 32 bytes (256 columns) or 8
-            const uint32_t lanes = cols == 256 ? 5 : 4, pos = l & ((1u << lanes) - 1);
-            r = l >> lanes;
-            per = cols == 256 ? 2 : 4;
-            c = (((pos >> 1) ^ column_turn(r)) << 5) | (pos & 1) << 4;
-        } else {
-            r = l >> 3;
-            per = 8;
-            c = (((l & 7) ^ l >> 4) << 4) ^ turn;
+            // 16 places of 32 bytes (256 columns) or 8 for a step of k
+            const uint32_t pos = l & ((1u << lanes) - 1), k = (l >> lanes) + i * (64 >> lanes);
+            return (((pos >> 1) ^ column_turn(k)) << 5) | (pos & 1) << 4;
         }
-        r = __umul24(r, row);
+        const uint32_t r = (HT == 1 ? w4 * 8 : 0) + i * 8 + (l >> 3);    // of b's part
+        return ((l & 7) ^ (r >> 1 & 7)) << 4;
+    };
 #pragma unroll
-        for (int i = 0; i < loads; ++i) {
-            // load i's rows are `per` i further: their turns, in bytes
-            const uint32_t k = i * per;
-            const uint32_t ci = c ^ (columns ? column_turn(k) << 5 : (k >> 1 & 7) << 4);
+    for (int i = 0; i < kLoadsA; ++i) {
+        const int shift = kShift - i % 4 * 1024;
+        if (group == 0) {
+            if constexpr (kAT)
+                at[i] = ((lane >> 5) + i * 2) * a_row + chunk(true, 5, i) + shift;
+            else
+                at[i] = ((lane >> 3) + i * 8) * a_row +
+                        (((lane & 7) ^ (((lane >> 3) + i * 8) >> 1 & 7)) << 4) + shift;
+        } else if constexpr (kBT) {
             // 128 of 256 columns: the second wave row's lie 128 columns on
-            uint32_t v = r + ci + k * row;
-            if (columns && cols == 128) v += ci & 128;
-            if (!columns && over < kStepBytes) v = (int)ci < over ? v : kNowhere;
-            dma16(v, buffer, at + i * 1024);
+            const uint32_t c = chunk(true, 4, i);
+            at[i] = ((lane >> 4) + i * 4) * b_row + c + (c & 128) + shift;
+        } else {
+            at[i] = ((lane >> 3) + i * 8) * b_row + chunk(false, 0, i) + shift;
+        }
+    }
+    // Of the last step by rows, what lies past the rows' end.
+    auto cut = [&](uint32_t (&v)[kLoadsA], bool a) {
+        const int over = p.K * kElem - next.step * kStepBytes;
+        const uint32_t l = opaque(lane);
+#pragma unroll
+        for (int i = 0; i < (kLoadsA > kLoadsB ? kLoadsA : kLoadsB); ++i) {
+            const uint32_t r = (HT == 1 && !a ? w4 * 8 : 0) + i * 8 + (l >> 3);
+            const uint32_t c = ((l & 7) ^ (r >> 1 & 7)) << 4;
+            v[i] = (int)c < over ? at[i] : kNowhere;
         }
     };
+    const bool ragged = !kBT && (p.K * kElem) % kStepBytes != 0;
     auto issue_a = [&]() {
-        const i32x4 buffer =
-            kAT ? make_buffer(next.at, max(0, min(16, next.left)) * (int)a_row, next.col)
-                : make_buffer(next.at, next.left, 0);
-        fetch(std::integral_constant<bool, kAT>{}, std::integral_constant<int, kLoadsA>{}, 256,
-              a_row, buffer, lds_a + (fetched & 1) * kABytes + w4 * kLoadsA * 1024, 0);
+        const i32x4 buffer = make_buffer(
+            next.at, kAT ? max(0, min(16, next.left)) * (int)a_row - next.col : next.left);
+        const uint32_t to = lds_a + (fetched & 1) * kABytes + w4 * kLoadsA * 1024;
+        if (!kAT && ragged && next.step == steps_k - 1) {
+            uint32_t v[kLoadsA];
+            cut(v, true);
+            dma16<4>(v, buffer, to);
+            dma16<4>(v + 4, buffer, to + 4096);
+        } else {
+            dma16<4>(at, buffer, to);
+            dma16<4>(at + 4, buffer, to + 4096);
+        }
         ++fetched;
         advance(kAT, a_row);
     };
     auto issue_b = [&](int half) {
-        i32x4 buffer;
-        if constexpr (kBT) {
-            const int more = half * 128;         // bytes: 64 columns
-            buffer = make_buffer(next.at + more, max(0, min(16, next.left)) * (int)b_row,
-                                 next.col + more);
+        const int more = kBT ? half * 128 : half * HT * 16 * (int)b_row;
+        const i32x4 buffer = make_buffer(
+            next.at + more,
+            kBT ? max(0, min(16, next.left)) * (int)b_row - next.col - more : next.left - more);
+        const uint32_t to =
+            lds_b + ((fetched & 1) * 2 + half) * kBHalf + w4 * kLoadsB * 1024;
+        if (ragged && next.step == steps_k - 1) {
+            uint32_t v[kLoadsA];
+            cut(v, false);
+            dma16<kLoadsB>(v, buffer, to);
         } else {
-            const int more = half * HT * 16 * (int)b_row;
-            buffer = make_buffer(next.at + more, min(next.left - more, HT * 8 * (int)b_row), 0);
+            dma16<kLoadsB>(at, buffer, to);
         }
-        fetch(std::integral_constant<bool, kBT>{}, std::integral_constant<int, kLoadsB>{}, 128,
-              b_row, buffer, lds_b + ((fetched & 1) * 2 + half) * kBHalf + w4 * kLoadsB * 1024,
-              HT == 1 ? (w4 & 1) * 64 : 0);
         if constexpr (FP8) {
             if (half == 0) {
                 dma4((uint32_t)(lane * (p.K / 128) * 4), make_buffer(next.s, next.s_left, 0),
@@ -385,12 +424,11 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>&
                      (int)(uint32_t)(h >> 32)};
     };
     auto lane_columns = [&](int row) {
-        const uint32_t l = opaque(lane), k = (l >> 4) * 8 + (l >> 2 & 3);
+        const uint32_t l = lane, k = (l >> 4) * 8 + (l >> 2 & 3);
         return k * row + (column_turn(k) << 5) + ((l & 3) << 3);
     };
     auto lane_rows = [&]() {
-        const uint32_t l = opaque(lane);
-        return row_place(l & 15, l >> 4);
+        return row_place(lr, lg);
     };
     auto read_a = [&](int buf) {
         const uint8_t* s = lds.a[buf];
@@ -459,6 +497,7 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>&
                     part[i % (kLate + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                         a, b, zero, 0, 0, 0, 127, 0, 127);
                 }
+                __builtin_amdgcn_sched_barrier(0);
                 if (i >= kLate) {
                     const int rt = (i - kLate) / 4, ct = (i - kLate) % 4;
                     const f32x4 t = part[(i - kLate) % (kLate + 1)];
