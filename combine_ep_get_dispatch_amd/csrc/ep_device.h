@@ -107,6 +107,17 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                       pack_bf16x2(f[6], f[7]));
 }
 
+// 1 / (1 + exp(-v)), for results of 16 bits or fewer: v_exp_f32 and v_rcp_f32 are off
+// by a step of fp32 each, and exp multiplies the rounding of v * log2(e) by |v|, so
+// the result is off by at most 1.25 |v| + 5 half steps: 2^-17 of it where exp(-v) is
+// still in range (v > -87.3; 0 below).  (With expf and a division the activation's
+// kernels were bound by these, not by HBM: 32768 x 2048 to E4M3 83 us, 80 with what
+// the product loses made up for.)
+__device__ __forceinline__ float sigmoid(float v) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504f));
+}
+__device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
+
 // Unsigned maximum over the 8 lanes of an aligned group of 8, with three DPP
 // moves (no LDS round trip): swap neighbours (quad_perm 1,0,3,2), swap pairs
 // (quad_perm 2,3,0,1), then mirror each half row of 8 lanes, which pairs the

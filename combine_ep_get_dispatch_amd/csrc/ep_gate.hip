@@ -53,36 +53,60 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(const GateArgs p) {
     const uint64_t held = p.runs.counts ? held_rows(p.runs, r0) : ~0ull;
     if ((held & low_bits(rows)) == 0) return;
     const int per = p.N / 8;             // chunks of 8 channels of a row
-    for (int i = threadIdx.x; i < rows * per; i += kGateThreads) {
-        const int r = i / per, c = i - r * per;
-        if (!(held >> r & 1)) continue;  // whole groups of 16 lanes where codes are written
-        const uint4* a = reinterpret_cast<const uint4*>(p.a + (r0 + r) * 2 * p.N);
-        float g[8], u[8], o[8];
-        unpack8(g, a[c]);
-        unpack8(u, a[per + c]);
-        if constexpr (KIND == kGateBackward) {
-            float d[8], e[8];
-            unpack8(d, reinterpret_cast<const uint4*>(p.gy + (r0 + r) * p.N)[c]);
+    // this thread's chunk, and what lies kGateThreads chunks on
+    int r = threadIdx.x / per, c = threadIdx.x - r * per;
+    const int dr = kGateThreads / per, dc = kGateThreads - dr * per;
+    while (r < rows) {
+        uint4 g[kGateChunks], u[kGateChunks], d[kGateChunks];
+        int row[kGateChunks], at[kGateChunks];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float s = 1.0f / (1.0f + expf(-g[j]));
-                const float si = g[j] * s;
-                o[j] = d[j] * u[j] * __builtin_fmaf(si, 1.0f - s, s);
-                e[j] = d[j] * si;
+        for (int j = 0; j < kGateChunks; ++j) {
+            row[j] = r < rows && (held >> r & 1) ? r : -1;
+            at[j] = c;
+            if (row[j] >= 0) {           // whole groups of 16 lanes where codes are written
+                const uint4* a = reinterpret_cast<const uint4*>(p.a + (r0 + r) * 2 * p.N);
+                g[j] = a[c];
+                u[j] = a[per + c];
+                if constexpr (KIND == kGateBackward)
+                    d[j] = reinterpret_cast<const uint4*>(p.gy + (r0 + r) * p.N)[c];
             }
-            uint4* out = reinterpret_cast<uint4*>(p.y + (r0 + r) * 2 * p.N);
-            out[c] = pack8(o);
-            out[per + c] = pack8(e);
-        } else {
+            r += dr;
+            c += dc;
+            if (c >= per) {
+                c -= per;
+                ++r;
+            }
+        }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = g[j] / (1.0f + expf(-g[j])) * u[j];
-            if constexpr (KIND == kGateBf16) {
-                reinterpret_cast<uint4*>(p.y + (r0 + r) * p.N)[c] = pack8(o);
+        for (int j = 0; j < kGateChunks; ++j) {
+            if (row[j] < 0) continue;
+            float gf[8], uf[8], o[8];
+            unpack8(gf, g[j]);
+            unpack8(uf, u[j]);
+            if constexpr (KIND == kGateBackward) {
+                float df[8], e[8];
+                unpack8(df, d[j]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float s = sigmoid(gf[i]), si = gf[i] * s;
+                    o[i] = df[i] * uf[i] * __builtin_fmaf(si, 1.0f - s, s);
+                    e[i] = df[i] * si;
+                }
+                uint4* out = reinterpret_cast<uint4*>(p.y + (r0 + row[j]) * 2 * p.N);
+                out[at[j]] = pack8(o);
+                out[per + at[j]] = pack8(e);
             } else {
-                float scale;
-                const uint2 q = quantise8(o, scale);
-                reinterpret_cast<uint2*>(p.codes + (r0 + r) * p.N)[c] = q;
-                if ((c & 15) == 0) p.scales[(r0 + r) * (p.N / 128) + c / 16] = scale;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = silu(gf[i]) * uf[i];
+                if constexpr (KIND == kGateBf16) {
+                    reinterpret_cast<uint4*>(p.y + (r0 + row[j]) * p.N)[at[j]] = pack8(o);
+                } else {
+                    float scale;
+                    const uint2 q = quantise8(o, scale);
+                    reinterpret_cast<uint2*>(p.codes + (r0 + row[j]) * p.N)[at[j]] = q;
+                    if ((at[j] & 15) == 0)
+                        p.scales[(r0 + row[j]) * (p.N / 128) + at[j] / 16] = scale;
+                }
             }
         }
     }
@@ -90,8 +114,8 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(const GateArgs p) {
 
 template <int KIND>
 hipError_t launch_gate(GateArgs p, hipStream_t s) {
-    // tiles of about 32 KiB of gate_up rows
-    const int64_t want = (kGateTileBytes / 4) / p.N;
+    // tiles of about one round of chunks
+    const int64_t want = (int64_t)kGateThreads * kGateChunks * 8 / p.N;
     p.tile = (int)(want < 1 ? 1 : want > 64 ? 64 : want);
     const int64_t tiles = (p.rows + p.tile - 1) / p.tile, most = max_launch_tokens(kGateThreads);
     for (int64_t t = 0; t < tiles; t += most) {

@@ -541,7 +541,7 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>&
                 if constexpr (SWIGLU) {
                     const f32x4 u = acc[ct + 2][rt];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = v[i] / (1.0f + expf(-v[i])) * u[i];
+                    for (int i = 0; i < 4; ++i) v[i] = silu(v[i]) * u[i];
                 }
                 if constexpr (F32) {
                     f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(p.y) + at + c);

@@ -321,7 +321,7 @@ hipError_t launch_expert_grad_weight(const uint16_t* gy, const uint16_t* x, cons
 
 // ------------------------------------------------------------------- gate ---
 constexpr int kGateThreads = 256;
-constexpr int kGateTileBytes = 32 * 1024;
+constexpr int kGateChunks = 4;     // chunks of 8 channels that a thread has on their way
 
 // codes null: bf16.  runs.counts null: every row.
 hipError_t launch_expert_swiglu(const uint16_t* a, const RowRuns& runs, int N, uint16_t* y,
@@ -330,6 +330,7 @@ hipError_t launch_expert_swiglu_backward(const uint16_t* gy, const uint16_t* a, 
                                          int N, uint16_t* ga, hipStream_t s);
 
 // ------------------------------------------------------------------- norm ---
+constexpr int kNormThreads = 256;     // of a row with one chunk of 8 channels a thread
 constexpr int kNormMaxParts = 512;
 // Workgroups of the norm's gradient, each with a part of the weight's.
 constexpr int norm_parts(int T) { return T < kNormMaxParts ? T : kNormMaxParts; }

@@ -69,27 +69,23 @@ __device__ __forceinline__ void unpack_weight(float (&f)[8], const Weight8<W32>&
     }
 }
 
-// Sum over a workgroup of NW waves, in wave order, the same in every thread.
-// s holds NW floats; the caller sees to it that no wave still reads it.
-template <int NW>
+// Sum over the workgroup, the same in every thread, in an order fixed by its size.
+// s holds 16 floats; the caller sees to it that no wave still reads it.
 __device__ __forceinline__ float block_sum(float v, float* s) {
     v = seg_sum<64>(v);
-    if constexpr (NW == 1) return v;
+    if (blockDim.x == 64) return v;
     if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
     __syncthreads();
-    float t = s[0];
-#pragma unroll
-    for (int i = 1; i < NW; ++i) t += s[i];
-    return t;
+    const int waves = blockDim.x >> 6, i = threadIdx.x & 15;
+    return seg_sum<16>(i < waves ? s[i] : 0.0f);
 }
 
-// One row per workgroup of NW waves; a thread holds chunks of 8 channels tid,
-// tid + 64 NW, ..., NC of them, so 16 neighbouring lanes hold 128 neighbouring
-// channels, one scale.
-template <int NW, int NC, bool W32>
-__global__ __launch_bounds__(NW * 64) void rms_norm_kernel(const NormArgs p) {
-    constexpr int kThreads = NW * 64;
-    __shared__ float part[NW];
+// One row per workgroup; a thread holds chunks of 8 channels tid, tid + blockDim, ...,
+// NC of them, so 16 neighbouring lanes hold 128 neighbouring channels, one scale.
+template <int NC, bool W32>
+__global__ __launch_bounds__(1024) void rms_norm_kernel(const NormArgs p) {
+    const int kThreads = blockDim.x;
+    __shared__ float part[16];
     const int chunks = p.H / 8;
     const int64_t row = blockIdx.x;
     const uint4* x = reinterpret_cast<const uint4*>(p.x + row * p.H);
@@ -127,7 +123,7 @@ __global__ __launch_bounds__(NW * 64) void rms_norm_kernel(const NormArgs p) {
         for (int j = 0; j < 8; ++j) s = __builtin_fmaf(a[j], a[j], s);
         sum += (int)threadIdx.x + i * kThreads < chunks ? s : 0.0f;
     }
-    sum = block_sum<NW>(sum, part);
+    sum = block_sum(sum, part);
     const float inv = 1.0f / sqrtf(sum / (float)p.H + p.eps);
     if (p.inv && threadIdx.x == 0) p.inv[row] = inv;
 #pragma unroll
@@ -152,10 +148,10 @@ __global__ __launch_bounds__(NW * 64) void rms_norm_kernel(const NormArgs p) {
 // Rows blockIdx.x, blockIdx.x + gridDim.x, ...; a thread's channels as above.
 // It sums its channels' grad_weight over the workgroup's rows in registers;
 // sum_parts_kernel adds the workgroups' sums up in their order.
-template <int NW, int NC, bool W32>
-__global__ __launch_bounds__(NW * 64) void rms_norm_backward_kernel(const NormBackArgs p) {
-    constexpr int kThreads = NW * 64;
-    __shared__ float part[2][NW];
+template <int NC, bool W32>
+__global__ __launch_bounds__(1024) void rms_norm_backward_kernel(const NormBackArgs p) {
+    const int kThreads = blockDim.x;
+    __shared__ float part[2][16];
     const int chunks = p.H / 8;
     float gw[NC][8];
     Weight8<W32> w[NC];
@@ -166,47 +162,66 @@ __global__ __launch_bounds__(NW * 64) void rms_norm_backward_kernel(const NormBa
         for (int j = 0; j < 8; ++j) gw[i][j] = 0.0f;
     }
     const float per = 1.0f / (float)p.H;
-    int turn = 0;
-    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x, turn ^= 1) {
+    // a row's loads are asked for while the row before it is worked on, where the
+    // registers hold both
+    constexpr bool kAhead = NC == 1;
+    uint4 v[NC], g[NC], r[NC];
+    float inv;
+    auto load = [&](int64_t row) {
         const uint4* x = reinterpret_cast<const uint4*>(p.x + row * p.H);
         const uint4* gy = reinterpret_cast<const uint4*>(p.gy + row * p.H);
-        uint4 v[NC], g[NC], r[NC];
+        const uint4* gr = reinterpret_cast<const uint4*>(p.gres + row * p.H);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = min((int)threadIdx.x + i * kThreads, chunks - 1);
             v[i] = x[c];
             g[i] = gy[c];
-            if (p.gres) r[i] = reinterpret_cast<const uint4*>(p.gres + row * p.H)[c];
+            if (p.gres) r[i] = gr[c];
         }
-        const float inv = p.inv[row];
+        inv = p.inv[row];
+    };
+    if (kAhead) load(blockIdx.x);
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x, turn ^= 1) {
+        uint4 nb[NC], gn[NC], rb[NC];     // n and grad_y * weight are made of these again
+        if (!kAhead) load(row);
+        const float inv_row = inv;
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
+            nb[i] = v[i];
+            gn[i] = g[i];
+            rb[i] = r[i];
+        }
+        if (kAhead) load(row + gridDim.x < p.T ? row + gridDim.x : row);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
             float a[8], b[8], f[8], s = 0.0f;
-            unpack8(a, v[i]);
-            unpack8(b, g[i]);
+            unpack8(a, nb[i]);
+            unpack8(b, gn[i]);
             unpack_weight<W32>(f, w[i]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float n = a[j] * inv;
+                const float n = a[j] * inv_row;
                 gw[i][j] = __builtin_fmaf(b[j], n, gw[i][j]);
                 s = __builtin_fmaf(b[j] * f[j], n, s);
             }
             sum += (int)threadIdx.x + i * kThreads < chunks ? s : 0.0f;
         }
-        const float mean = block_sum<NW>(sum, part[turn]) * per;
+        const float mean = block_sum(sum, part[turn]) * per;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = threadIdx.x + i * kThreads;
             if (c >= chunks) break;
             float a[8], b[8], f[8], o[8];
-            unpack8(a, v[i]);
-            unpack8(b, g[i]);
+            unpack8(a, nb[i]);
+            unpack8(b, gn[i]);
             unpack_weight<W32>(f, w[i]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = inv * (b[j] * f[j] - a[j] * inv * mean);
+            for (int j = 0; j < 8; ++j)
+                o[j] = inv_row * (b[j] * f[j] - a[j] * inv_row * mean);
             if (p.gres) {
-                unpack8(f, r[i]);
+                unpack8(f, rb[i]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) o[j] += f[j];
             }
@@ -223,16 +238,17 @@ __global__ __launch_bounds__(NW * 64) void rms_norm_backward_kernel(const NormBa
     }
 }
 
-// out[c] = sum over the parts, four channels a thread; 16 threads share a
-// channel's parts, each every 16th of them, and add up in a fixed order.
-constexpr int kPartThreads = 16;
-__global__ __launch_bounds__(256) void sum_parts_kernel(const float* part, int parts, int H,
-                                                        float* out) {
-    __shared__ float4 s[256];
-    const int c = (blockIdx.x * (256 / kPartThreads) + threadIdx.x % (256 / kPartThreads)) * 4;
+// out[c] = sum over the parts, four channels a thread; 64 threads share a channel's
+// parts, each every 64th of them, and add up in a fixed order.
+constexpr int kSumThreads = 1024, kSumShare = 64, kSumColumns = kSumThreads / kSumShare;
+__global__ __launch_bounds__(kSumThreads) void sum_parts_kernel(const float* part, int parts,
+                                                                int H, float* out) {
+    __shared__ float4 s[kSumThreads];
+    const int col = threadIdx.x % kSumColumns, c = (blockIdx.x * kSumColumns + col) * 4;
     float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (c < H) {
-        for (int i = threadIdx.x / (256 / kPartThreads); i < parts; i += kPartThreads) {
+#pragma unroll 4
+        for (int i = threadIdx.x / kSumColumns; i < parts; i += kSumShare) {
             const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)i * H + c);
             t.x += v.x;
             t.y += v.y;
@@ -241,34 +257,34 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(const float* part, int p
         }
     }
     s[threadIdx.x] = t;
-    __syncthreads();
-    if (threadIdx.x < 256 / kPartThreads && c < H) {
-        for (int i = 1; i < kPartThreads; ++i) {
-            const float4 v = s[threadIdx.x + i * (256 / kPartThreads)];
+    for (int half = kSumThreads / 2; half >= kSumColumns; half /= 2) {
+        __syncthreads();
+        if ((int)threadIdx.x < half) {
+            const float4 v = s[threadIdx.x + half];
             t.x += v.x;
             t.y += v.y;
             t.z += v.z;
             t.w += v.w;
+            s[threadIdx.x] = t;
         }
-        *reinterpret_cast<float4*>(out + c) = t;
     }
+    if ((int)threadIdx.x < kSumColumns && c < H) *reinterpret_cast<float4*>(out + c) = t;
 }
 
-// Waves and chunks per thread for rows of `chunks` chunks.
+// Chunks per thread for rows of `chunks` chunks in workgroups of up to `threads`
+// threads, and the threads that this takes.
 template <typename F>
-void by_width(int chunks, F&& f) {
-    if (chunks <= 64)
-        f(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
-    else if (chunks <= 256)
-        f(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
-    else if (chunks <= 512)
-        f(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
-    else if (chunks <= 1024)
-        f(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
-    else if (chunks <= 2048)
-        f(std::integral_constant<int, 8>{}, std::integral_constant<int, 4>{});
+void by_width(int chunks, int threads, F&& f) {
+    auto run = [&](auto nc) {
+        constexpr int NC = decltype(nc)::value;
+        f(nc, ((chunks + NC - 1) / NC + 63) / 64 * 64);
+    };
+    if (chunks <= threads)
+        run(std::integral_constant<int, 1>{});
+    else if (chunks <= 2 * threads || (chunks <= 2048 && threads < 1024))
+        run(std::integral_constant<int, 2>{});
     else
-        f(std::integral_constant<int, 16>{}, std::integral_constant<int, 4>{});
+        run(std::integral_constant<int, 4>{});
 }
 
 }  // namespace
@@ -276,9 +292,9 @@ void by_width(int chunks, F&& f) {
 hipError_t launch_rms_norm(const uint16_t* x, const uint16_t* res, const void* w, bool w32, int T,
                            int H, float eps, uint16_t* y, uint8_t* codes, float* scales,
                            uint16_t* res_out, float* inv, hipStream_t s) {
-    by_width(H / 8, [&](auto nw, auto nc) {
-        constexpr int NW = decltype(nw)::value, NC = decltype(nc)::value;
-        const int64_t most = max_launch_tokens(NW * 64);
+    by_width(H / 8, kNormThreads, [&](auto nc, int threads) {
+        constexpr int NC = decltype(nc)::value;
+        const int64_t most = max_launch_tokens(threads);
         for (int64_t t = 0; t < T; t += most) {
             const int64_t at = t * H;
             const NormArgs p = {x + at,
@@ -293,9 +309,9 @@ hipError_t launch_rms_norm(const uint16_t* x, const uint16_t* res, const void* w
                                 inv ? inv + t : nullptr};
             const dim3 grid((unsigned)(T - t < most ? T - t : most));
             if (w32)
-                hipLaunchKernelGGL((rms_norm_kernel<NW, NC, true>), grid, dim3(NW * 64), 0, s, p);
+                hipLaunchKernelGGL((rms_norm_kernel<NC, true>), grid, dim3(threads), 0, s, p);
             else
-                hipLaunchKernelGGL((rms_norm_kernel<NW, NC, false>), grid, dim3(NW * 64), 0, s, p);
+                hipLaunchKernelGGL((rms_norm_kernel<NC, false>), grid, dim3(threads), 0, s, p);
         }
     });
     return hipGetLastError();
@@ -307,19 +323,19 @@ hipError_t launch_rms_norm_backward(const uint16_t* gy, const uint16_t* x, const
     const int parts = norm_parts(T);
     if (T > 0) {
         const NormBackArgs p = {gy, x, w, inv, gres, T, H, gx, ws};
-        by_width(H / 8, [&](auto nw, auto nc) {
-            constexpr int NW = decltype(nw)::value, NC = decltype(nc)::value;
+        by_width(H / 8, 1024, [&](auto nc, int threads) {
+            constexpr int NC = decltype(nc)::value;
             if (w32)
-                hipLaunchKernelGGL((rms_norm_backward_kernel<NW, NC, true>), dim3(parts),
-                                   dim3(NW * 64), 0, s, p);
+                hipLaunchKernelGGL((rms_norm_backward_kernel<NC, true>), dim3(parts),
+                                   dim3(threads), 0, s, p);
             else
-                hipLaunchKernelGGL((rms_norm_backward_kernel<NW, NC, false>), dim3(parts),
-                                   dim3(NW * 64), 0, s, p);
+                hipLaunchKernelGGL((rms_norm_backward_kernel<NC, false>), dim3(parts),
+                                   dim3(threads), 0, s, p);
         });
     }
-    const int per = 256 / kPartThreads * 4;
-    hipLaunchKernelGGL(sum_parts_kernel, dim3((H + per - 1) / per), dim3(256), 0, s, ws, parts, H,
-                       gw);
+    const int per = kSumColumns * 4;
+    hipLaunchKernelGGL(sum_parts_kernel, dim3((H + per - 1) / per), dim3(kSumThreads), 0, s, ws,
+                       parts, H, gw);
     return hipGetLastError();
 }
 

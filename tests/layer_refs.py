@@ -41,9 +41,16 @@ def weight_values(codes, scales, N):
     return e4m3_values()[codes.long()] * scales.double()[:, block].repeat_interleave(128, 2)
 
 
-# exp(-v) passes fp32's range below v = -88.7, where silu(v) then becomes 0: it is
-# at most 88.8 * e^-88.7 < 2^-121 there.
-LOST = 2.0 ** -121
+# The sigmoid's result is 0 below v = -87.3, where the reciprocal of 1 + exp(-v) would
+# be subnormal: |silu(v)| is at most 87.4 * e^-87.3 < 2^-119 there.
+LOST = 2.0 ** -119
+
+
+def silu_steps(v):
+    """Half steps of fp32 that silu(v) * u is off by.  v * log2(e) is rounded once,
+    the constant once at 0.22 half steps: exp makes 1.25 |v| half steps of that.
+    exp itself 2, the sum 1, the reciprocal 2, two products 2."""
+    return 1.25 * v.abs() + 8
 
 
 def silu(v):
@@ -67,33 +74,36 @@ def linear(x, w, runs, N, swiglu, cut=0.0):
             g, u, eg, eu = a[:, :N], a[:, N:], err[:, :N], err[:, N:]
             sg = silu(g)
             y[b:b + n] = sg * u
-            # |silu'| <= 1.1; expf, the division and two products: 8 half steps
-            tol[b:b + n] = 1.1 * eg * (u.abs() + eu) + sg.abs() * eu + 8 * U32 * (sg * u).abs() + LOST * u.abs()
+            # |silu'| <= 1.1
+            tol[b:b + n] = (1.1 * eg * (u.abs() + eu) + sg.abs() * eu
+                            + silu_steps(g) * U32 * (sg * u).abs() + LOST * u.abs())
         else:
             y[b:b + n], tol[b:b + n] = a, err
     return y, tol
 
 
 def gate(a, N):
-    """(y, bound ahead of its rounding): expf of 2 half steps, whose argument is
-    exact, an addition, a division, a product: 8 half steps."""
+    """(y, bound ahead of its rounding)."""
     a = a.double()
-    y = silu(a[:, :N]) * a[:, N:]
-    return y, 8 * U32 * y.abs() + LOST * a[:, N:].abs() + TINY
+    g = a[:, :N]
+    y = silu(g) * a[:, N:]
+    return y, silu_steps(g) * U32 * y.abs() + LOST * a[:, N:].abs() + TINY
 
 
 def gate_backward(gy, a, N):
-    """(gradient, bound ahead of its rounding).  s: 4 half steps; 1 - s: U32
-    against s <= 1, so U32 absolute and 4 half steps of s carried over; the rest
-    6 products and additions of terms whose sizes add up to `size`."""
+    """(gradient, bound ahead of its rounding).  s as in silu_steps; 1 - s: U32
+    against s <= 1 and s's own error carried over; the rest 6 products and
+    additions of terms whose sizes add up to `size`."""
     a, gy = a.double(), gy.double()
     g, u = a[:, :N], a[:, N:]
     s = torch.sigmoid(g)
     dg = gy * u * (s + g * s * (1 - s))
     size = (gy * u).abs() * (s + (g * s).abs())
     du = gy * g * s
-    return (torch.cat((dg, du), 1), torch.cat((16 * U32 * size + LOST * (gy * u).abs(), 8 * U32 * du.abs() + LOST * gy.abs()),
-                      1) + TINY)
+    steps = silu_steps(g)
+    return (torch.cat((dg, du), 1),
+            torch.cat((2 * steps * U32 * size + LOST * (gy * u).abs(),
+                       steps * U32 * du.abs() + LOST * gy.abs()), 1) + TINY)
 
 
 def to_e4m3(y, tol):

@@ -113,8 +113,9 @@ def test_linear_bf16(counts, I, N, form, swiglu):
     torch.cuda.synchronize()
     got = y.cpu()
     assert bool((got[~hold] == 77.0).all())
-    if swiglu:                               # silu's own roundings, |up| < 2^15
-        tol = 8 * ref.U32 * want.abs() + 2.0 ** 15 * ref.LOST
+    if swiglu:                               # the sums are exact; silu's own, |up| < 2^15
+        gate, _ = ref.linear(x, w[:, :N], runs, N, False)
+        tol = ref.silu_steps(gate) * ref.U32 * want.abs() + 2.0 ** 15 * ref.LOST
         within(got[hold], want[hold], ref.bf16_tol(want, tol)[hold], "y")
     else:
         assert torch.equal(got[hold].double(), want[hold].bfloat16().double())
@@ -157,7 +158,9 @@ def test_linear_fp8(counts, I, N, form, swiglu):
     got = y.cpu()
     assert bool((got[~hold] == 77.0).all())
     if swiglu:                               # |up| < 2^15
-        tol = 8 * ref.U32 * want.abs() + 2.0 ** 15 * ref.LOST
+        values = ref.weight_values(w, ws, N)[:, :N]
+        gate, _ = ref.linear(ref.fp8_values(x, xs), values, runs, N, False)
+        tol = ref.silu_steps(gate) * ref.U32 * want.abs() + 2.0 ** 15 * ref.LOST
         within(got[hold], want[hold], ref.bf16_tol(want, tol)[hold], "y")
     else:
         assert torch.equal(got[hold].double(), want[hold].bfloat16().double())
