@@ -1020,21 +1020,22 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     if residual is not None:
         _need(residual, torch.bfloat16, "residual", (T, H), device=dev)
     if out is None:
+        f32 = torch.float32
         out = RmsNormed(
-            torch.empty((T, H), dtype=torch.bfloat16, device=dev) if bf16 else None,
-            torch.empty((T, H), dtype=torch.uint8, device=dev) if fp8 else None,
-            torch.empty((T, H // 128), dtype=torch.float32, device=dev) if fp8 else None,
-            torch.empty((T, H), dtype=torch.bfloat16, device=dev) if residual is not None
-            else None,
-            torch.empty(T, dtype=torch.float32, device=dev))
-    if bf16:
-        _need(out.y, torch.bfloat16, "y", (T, H), device=dev)
-    if fp8:
-        _need(out.codes, torch.uint8, "codes", (T, H), device=dev)
-        _need(out.scales, torch.float32, "scales", (T, H // 128), device=dev)
-    if residual is not None:
-        _need(out.residual, torch.bfloat16, "out.residual", (T, H), device=dev)
-    _need(out.inv_rms, torch.float32, "inv_rms", (T,), device=dev)
+            torch.empty_like(x) if bf16 else None,
+            torch.empty_like(x, dtype=torch.uint8) if fp8 else None,
+            x.new_empty((T, H // 128), dtype=f32) if fp8 else None,
+            torch.empty_like(x) if residual is not None else None,
+            x.new_empty(T, dtype=f32))
+    else:
+        if bf16:
+            _need(out.y, torch.bfloat16, "y", (T, H), device=dev)
+        if fp8:
+            _need(out.codes, torch.uint8, "codes", (T, H), device=dev)
+            _need(out.scales, torch.float32, "scales", (T, H // 128), device=dev)
+        if residual is not None:
+            _need(out.residual, torch.bfloat16, "out.residual", (T, H), device=dev)
+        _need(out.inv_rms, torch.float32, "inv_rms", (T,), device=dev)
     _launch("ep_rms_norm", x, _addr(x), _addr(residual), _addr(weight), wdt, T, H, float(eps),
             _addr(out.y) if bf16 else None, _addr(out.codes) if fp8 else None,
             _addr(out.scales) if fp8 else None,
@@ -1062,15 +1063,15 @@ def rms_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.Tenso
     if grad_residual is not None:
         _need(grad_residual, torch.bfloat16, "grad_residual", (T, H), device=dev)
     if out is None:
-        out = (torch.empty((T, H), dtype=torch.bfloat16, device=dev),
-               torch.empty(H, dtype=torch.float32, device=dev))
-    grad_x, grad_weight = out
-    _need(grad_x, torch.bfloat16, "grad_x", (T, H), device=dev)
-    _need(grad_weight, torch.float32, "grad_weight", (H,), device=dev)
+        grad_x, grad_weight = torch.empty_like(grad_y), grad_y.new_empty(H, dtype=torch.float32)
+    else:
+        grad_x, grad_weight = out
+        _need(grad_x, torch.bfloat16, "grad_x", (T, H), device=dev)
+        _need(grad_weight, torch.float32, "grad_weight", (H,), device=dev)
     if workspace is None:
-        workspace = torch.empty(rms_norm_backward_workspace_bytes(T, H), dtype=torch.uint8,
-                                device=dev)
-    _need(workspace, torch.uint8, "workspace", device=dev)
+        workspace = grad_y.new_empty(rms_norm_backward_workspace_bytes(T, H), dtype=torch.uint8)
+    else:
+        _need(workspace, torch.uint8, "workspace", device=dev)
     _launch("ep_rms_norm_backward", grad_y, _addr(grad_y), _addr(x), _addr(weight), wdt,
             _addr(inv_rms), _addr(grad_residual), T, H, _addr(grad_x), _addr(grad_weight),
             _addr(workspace), workspace.numel())
@@ -1080,7 +1081,7 @@ def rms_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.Tenso
 def rms_norm_backward_workspace_bytes(num_tokens: int, hidden: int) -> int:
     """Bytes of rms_norm_backward's workspace (0 for an invalid shape)."""
     _sizes(num_tokens | hidden)
-    return lib().ep_rms_norm_backward_workspace_bytes(num_tokens, hidden)
+    return (_lib or lib()).ep_rms_norm_backward_workspace_bytes(num_tokens, hidden)
 
 
 # ---------------------------------------------------------------------------

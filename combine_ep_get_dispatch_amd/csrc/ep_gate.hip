@@ -65,10 +65,10 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(const GateArgs p) {
             at[j] = c;
             if (row[j] >= 0) {           // whole groups of 16 lanes where codes are written
                 const uint4* a = reinterpret_cast<const uint4*>(p.a + (r0 + r) * 2 * p.N);
-                g[j] = a[c];
-                u[j] = a[per + c];
+                g[j] = load_nt(a + c);
+                u[j] = load_nt(a + per + c);
                 if constexpr (KIND == kGateBackward)
-                    d[j] = reinterpret_cast<const uint4*>(p.gy + (r0 + r) * p.N)[c];
+                    d[j] = load_nt(reinterpret_cast<const uint4*>(p.gy + (r0 + r) * p.N) + c);
             }
             r += dr;
             c += dc;
@@ -93,8 +93,8 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(const GateArgs p) {
                     e[i] = df[i] * si;
                 }
                 uint4* out = reinterpret_cast<uint4*>(p.y + (r0 + row[j]) * 2 * p.N);
-                out[at[j]] = pack8(o);
-                out[per + at[j]] = pack8(e);
+                store_nt(out + at[j], pack8(o));
+                store_nt(out + per + at[j], pack8(e));
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) o[i] = silu(gf[i]) * uf[i];

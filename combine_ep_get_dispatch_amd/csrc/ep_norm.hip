@@ -93,12 +93,12 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(const NormArgs p) {
     Weight8<W32> w[NC];
 #pragma unroll
     for (int i = 0; i < NC; ++i)
-        v[i] = x[min((int)threadIdx.x + i * kThreads, chunks - 1)];
+        v[i] = load_nt(x + min((int)threadIdx.x + i * kThreads, chunks - 1));
     if (p.res) {
         const uint4* res = reinterpret_cast<const uint4*>(p.res + row * p.H);
         uint4 r[NC];
 #pragma unroll
-        for (int i = 0; i < NC; ++i) r[i] = res[min((int)threadIdx.x + i * kThreads, chunks - 1)];
+        for (int i = 0; i < NC; ++i) r[i] = load_nt(res + min((int)threadIdx.x + i * kThreads, chunks - 1));
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             float a[8], b[8];
@@ -174,9 +174,9 @@ __global__ __launch_bounds__(1024) void rms_norm_backward_kernel(const NormBackA
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = min((int)threadIdx.x + i * kThreads, chunks - 1);
-            v[i] = x[c];
-            g[i] = gy[c];
-            if (p.gres) r[i] = gr[c];
+            v[i] = load_nt(x + c);
+            g[i] = load_nt(gy + c);
+            if (p.gres) r[i] = load_nt(gr + c);
         }
         inv = p.inv[row];
     };
