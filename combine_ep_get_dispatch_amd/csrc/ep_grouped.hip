@@ -39,9 +39,18 @@ constexpr int kTileM = 256;
 constexpr int kStepBytes = 128;
 constexpr int kWaves = 8;
 constexpr int kABytes = kTileM * kStepBytes;
-constexpr int kBHalf = kABytes / 2;
+// Of a step's rows a part of up to 128 is read at a time: class 8 has two parts and
+// places for two steps, the others one part and places for three.
+constexpr int kBPart = kABytes / 2;
+template <int RT>
+constexpr int kParts = RT == 8 ? 2 : 1;
+template <int RT>
+constexpr int kStages = RT == 8 ? 2 : 3;
+constexpr int kStageBytes = 3 * (kABytes + kBPart);
+// E4M3 rows' scales, four steps' at a time, in a ring of places.
+constexpr int kScaleSteps = 4, kScalePlaces = 4;
 
-// 16 (or 4) bytes per lane from a bounded buffer to LDS, lane after lane, N loads
+// 16 bytes per lane from a bounded buffer to LDS, lane after lane, N loads
 // one after the other; what lies past the buffer's end arrives as zeros.  A load's
 // place i * 1024 counts in both memories, so `at` holds what is missing from
 // kShift, which the buffer's base makes up for.  Waited for by vmcnt; the compiler
@@ -73,20 +82,14 @@ __device__ __forceinline__ void dma16(const uint32_t* at, const i32x4& buffer, u
                      : "v"(at[0]), "s"(buffer), "s"(lds)
                      : "memory");
 }
-__device__ __forceinline__ void dma4(uint32_t at, const i32x4& buffer, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
-                 :
-                 : "v"(at), "s"(buffer), "s"(lds)
-                 : "memory");
-}
 constexpr uint32_t kNowhere = 0x80000000u;   // past every buffer's end
 
 // `size` bytes (0 or less: none) from `base`, which the loads reach at kShift.
-__device__ __forceinline__ i32x4 make_buffer(uint64_t base, int size, int shift = kShift) {
-    base -= shift;
+__device__ __forceinline__ i32x4 make_buffer(uint64_t base, int size) {
+    base -= kShift;
     return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)base),
                  __builtin_amdgcn_readfirstlane((int)(uint32_t)(base >> 32) & 0xffff),
-                 __builtin_amdgcn_readfirstlane(max(0, size) + shift), 0x00020000};
+                 __builtin_amdgcn_readfirstlane(max(0, size) + kShift), 0x00020000};
 }
 
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
@@ -206,14 +209,20 @@ __device__ __forceinline__ bool find_task(Task& t, const ProductArgs& p, const B
 
 constexpr int kRing = 4;    // tasks that a wave's fetching is ahead of its sums, at most
 
-template <bool FP8>
 struct ProductLds {
-    uint8_t a[2][kABytes];
-    uint8_t b[2][2][kBHalf];      // of a step: each half of the waves' first and second tiles
-    float scales[4][FP8 ? 256 : 1];
+    uint8_t stage[kStageBytes];
     Blocks known;
     int ring[2][kRing][8];
 };
+// The ring of scales lies behind the places of class 8, or after the rest: 4 KiB a
+// place for 256 rows, 2 KiB for 128.
+constexpr int kScaleBytes = kScalePlaces * 128 * kScaleSteps * 4;
+template <bool FP8>
+struct ProductMemory {
+    ProductLds lds;
+    float scales[FP8 ? kScaleBytes / 4 : 1];
+};
+static_assert(sizeof(ProductMemory<true>) <= 160 * 1024, "one workgroup's LDS");
 
 // A value that the compiler recomputes from where it is needed rather than hold
 // in registers all along.
@@ -233,21 +242,30 @@ __device__ __forceinline__ uint32_t row_place(int r, int c) {
 __device__ __forceinline__ int column_turn(int k) { return (k & 3) | (k >> 1 & 4); }
 
 template <Product OP, bool FP8, bool SWIGLU, bool F32, bool ADD, int RT>
-__device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>& lds, int task,
+__device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductMemory<FP8>& mem, int task,
                                           int end, int stride, unsigned nt) {
+    ProductLds& lds = mem.lds;
     constexpr int kTile = SWIGLU ? kTileM / 2 : kTileM;    // result channels
     constexpr bool kAT = OP != kRows;                      // a and b by columns
     constexpr bool kBT = OP == kGradWeight;
     constexpr int kElem = FP8 ? 1 : 2;
     constexpr int kStepK = kStepBytes / kElem;
-    constexpr int HT = RT / 2;                             // row tiles of a half
+    constexpr int kPart = kParts<RT>, kStage = kStages<RT>;
+    constexpr int HT = RT / kPart;                         // row tiles of a part
+    constexpr int kBStage = HT * 4096;                     // bytes of a part
+    constexpr int kScalePlace = 2 * RT * 16 * kScaleSteps * 4;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int group = wave >> 2, w4 = wave & 3;
     const int lg = lane >> 4, lr = lane & 15;
-    const uint32_t lds_a = __builtin_amdgcn_readfirstlane(lds_offset(&lds.a[0][0]));
-    const uint32_t lds_b = __builtin_amdgcn_readfirstlane(lds_offset(&lds.b[0][0][0]));
-    const uint32_t lds_s = FP8 ? __builtin_amdgcn_readfirstlane(lds_offset(&lds.scales[0][0])) : 0;
+    const uint8_t* const stage_a = lds.stage;
+    const uint8_t* const stage_b = lds.stage + kStage * kABytes;
+    const uint8_t* const stage_s =
+        RT == 8 ? lds.stage + kStage * (kABytes + kPart * kBStage)
+                : reinterpret_cast<const uint8_t*>(mem.scales);
+    const uint32_t lds_a = __builtin_amdgcn_readfirstlane(lds_offset(stage_a));
+    const uint32_t lds_b = __builtin_amdgcn_readfirstlane(lds_offset(stage_b));
+    const uint32_t lds_s = FP8 ? __builtin_amdgcn_readfirstlane(lds_offset(stage_s)) : 0;
     const uint32_t a_row = (OP == kRows ? p.K : p.M) * kElem;     // bytes
     const uint32_t b_row = (OP == kGradWeight ? p.B : p.K) * kElem;
     const int steps_k = (p.K + kStepK - 1) / kStepK;
@@ -255,14 +273,16 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>&
     // --- fetching: waves 0..3 a quarter of a's part of a step each, waves 4..7
     // of b's.  A load takes 1 KiB: 8 rows' 128 bytes, 2 steps' 256 or 4 steps' 128
     // columns.
-    constexpr int kLoadsA = 8, kLoadsB = HT;      // of b: a half
+    constexpr int kLoadsA = 8, kLoadsB = HT;      // of b: a part
     struct {
         int task, step, steps;
         uint64_t at, s;
         int left, s_left;       // bytes of the rows, or by columns steps of k
         int col;                // by columns: first byte of the row
     } next;
-    int pushed = 0, fetched = 0;                  // tasks; steps whose fetching has begun
+    int pushed = 0;                               // tasks
+    int fetch_to = 0, scale_to = 0;               // places of the step that is fetched next
+    auto turn_stage = [](int i) { return i + 1 == kStage ? 0 : i + 1; };
     auto seek = [&]() {
         Task t;
         const bool live = find_task<OP, RT>(t, p, lds.known, next.task, end, nt, kTile);
@@ -301,7 +321,7 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>&
             next.at = (uint64_t)(p.b + (t.begin + w4 * 16) * b_row + next.col);
             next.left = t.n - w4 * 16;
         } else {
-            // rows of this wave's part of the first half; those of the second lie 16 HT on
+            // rows of this wave's share of the first part; those of the second lie 16 HT on
             const int r = t.r0 + (w4 >> 1) * RT * 16 + (w4 & 1) * HT * 8;
             next.at = (uint64_t)(p.b + (t.begin + r) * b_row);
             next.left = (int)min((int64_t)max(0, t.n - r) * b_row, (int64_t)0x7fff0000);
@@ -329,8 +349,7 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>&
             const uint32_t pos = l & ((1u << lanes) - 1), k = (l >> lanes) + i * (64 >> lanes);
             return (((pos >> 1) ^ column_turn(k)) << 5) | (pos & 1) << 4;
         }
-        const uint32_t r = (HT == 1 ? w4 * 8 : 0) + i * 8 + (l >> 3);    // of b's part
-        return ((l & 7) ^ (r >> 1 & 7)) << 4;
+        return ((l & 7) ^ ((i * 8 + (l >> 3)) >> 1 & 7)) << 4;
     };
 #pragma unroll
     for (int i = 0; i < kLoadsA; ++i) {
@@ -339,8 +358,7 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>&
             if constexpr (kAT)
                 at[i] = ((lane >> 5) + i * 2) * a_row + chunk(true, 5, i) + shift;
             else
-                at[i] = ((lane >> 3) + i * 8) * a_row +
-                        (((lane & 7) ^ (((lane >> 3) + i * 8) >> 1 & 7)) << 4) + shift;
+                at[i] = ((lane >> 3) + i * 8) * a_row + chunk(false, 0, i) + shift;
         } else if constexpr (kBT) {
             // 128 of 256 columns: the second wave row's lie 128 columns on
             const uint32_t c = chunk(true, 4, i);
@@ -350,13 +368,12 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>&
         }
     }
     // Of the last step by rows, what lies past the rows' end.
-    auto cut = [&](uint32_t (&v)[kLoadsA], bool a) {
+    auto cut = [&](uint32_t (&v)[kLoadsA]) {
         const int over = p.K * kElem - next.step * kStepBytes;
         const uint32_t l = opaque(lane);
 #pragma unroll
-        for (int i = 0; i < (kLoadsA > kLoadsB ? kLoadsA : kLoadsB); ++i) {
-            const uint32_t r = (HT == 1 && !a ? w4 * 8 : 0) + i * 8 + (l >> 3);
-            const uint32_t c = ((l & 7) ^ (r >> 1 & 7)) << 4;
+        for (int i = 0; i < kLoadsA; ++i) {
+            const uint32_t c = ((l & 7) ^ ((i * 8 + (l >> 3)) >> 1 & 7)) << 4;
             v[i] = (int)c < over ? at[i] : kNowhere;
         }
     };
@@ -364,48 +381,53 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>&
     auto issue_a = [&]() {
         const i32x4 buffer = make_buffer(
             next.at, kAT ? max(0, min(16, next.left)) * (int)a_row - next.col : next.left);
-        const uint32_t to = lds_a + (fetched & 1) * kABytes + w4 * kLoadsA * 1024;
+        const uint32_t to = lds_a + fetch_to * kABytes + w4 * kLoadsA * 1024;
         if (!kAT && ragged && next.step == steps_k - 1) {
             uint32_t v[kLoadsA];
-            cut(v, true);
+            cut(v);
             dma16<4>(v, buffer, to);
             dma16<4>(v + 4, buffer, to + 4096);
         } else {
             dma16<4>(at, buffer, to);
             dma16<4>(at + 4, buffer, to + 4096);
         }
-        ++fetched;
+        fetch_to = turn_stage(fetch_to);
         advance(kAT, a_row);
     };
-    auto issue_b = [&](int half) {
-        const int more = kBT ? half * 128 : half * HT * 16 * (int)b_row;
+    auto issue_b = [&](int part) {
+        if constexpr (FP8) {
+            // ahead of the step's rows, so that these are waited for after them
+            if (part == 0 && next.step % kScaleSteps == 0) {
+                if (w4 < (2 * RT * 16 + 63) / 64) {
+                    const uint32_t v = (uint32_t)(lane * (p.K / 128) * 4) + kShift;
+                    dma16<1>(&v, make_buffer(next.s, next.s_left),
+                             lds_s + scale_to * kScalePlace + w4 * 1024);
+                }
+                scale_to = (scale_to + 1) % kScalePlaces;
+                next.s += kScaleSteps * 4;
+                next.s_left -= kScaleSteps * 4;
+            }
+        }
+        const int more = kBT ? part * 128 : part * HT * 16 * (int)b_row;
         const i32x4 buffer = make_buffer(
             next.at + more,
             kBT ? max(0, min(16, next.left)) * (int)b_row - next.col - more : next.left - more);
-        const uint32_t to =
-            lds_b + ((fetched & 1) * 2 + half) * kBHalf + w4 * kLoadsB * 1024;
+        const uint32_t to = lds_b + (fetch_to * kPart + part) * kBStage + w4 * kLoadsB * 1024;
         if (ragged && next.step == steps_k - 1) {
             uint32_t v[kLoadsA];
-            cut(v, false);
+            cut(v);
             dma16<kLoadsB>(v, buffer, to);
         } else {
             dma16<kLoadsB>(at, buffer, to);
         }
-        if constexpr (FP8) {
-            if (half == 0) {
-                dma4((uint32_t)(lane * (p.K / 128) * 4), make_buffer(next.s, next.s_left, 0),
-                     lds_s + (fetched & 3) * 1024 + w4 * 256);
-                next.s += 4;
-                next.s_left = max(0, next.s_left - 4);
-            }
-        }
-        if (half == 1) {
-            ++fetched;
+        if (part == kPart - 1) {
+            fetch_to = turn_stage(fetch_to);
             advance(kBT, b_row);
         }
     };
-    // loads of a step that may be on their way while an older part has to be there
-    constexpr int kAheadA = kLoadsA, kAheadB = 2 * kLoadsB + (FP8 ? 1 : 0);
+    // loads that may be on their way while an older part has to be there (scales not
+    // counted: they come every few steps)
+    constexpr int kAheadA = kLoadsA, kAheadB = kPart * kLoadsB;
 
     // --- this wave's results: 64 channels (4 tiles) by RT tiles of rows ---
     const int wm = w4, wr = group;
@@ -431,7 +453,7 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>&
         return row_place(lr, lg);
     };
     auto read_a = [&](int buf) {
-        const uint8_t* s = lds.a[buf];
+        const uint8_t* s = stage_a + buf * kABytes;
         if constexpr (kAT) {
             const uint32_t at = lane_columns(512);
 #pragma unroll
@@ -451,8 +473,8 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>&
                         (SWIGLU ? (ct >> 1) * 128 + (ct & 1) * 16 : ct * 16) * kStepBytes);
         }
     };
-    auto read_b = [&](int buf, int half, int step) {
-        const uint8_t* s = lds.b[buf][half];
+    auto read_b = [&](int buf, int part, int scales, int step) {
+        const uint8_t* s = stage_b + (buf * kPart + part) * kBStage;
         const uint32_t at = kBT ? lane_columns(256) : lane_rows();
 #pragma unroll
         for (int rt = 0; rt < HT; ++rt)
@@ -467,11 +489,14 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>&
         if constexpr (FP8) {
 #pragma unroll
             for (int rt = 0; rt < HT; ++rt)
-                sx[rt] = lds.scales[step & 3][(wr * RT + half * HT + rt) * 16 + lr];
+                sx[rt] = *reinterpret_cast<const float*>(
+                    stage_s + scales * kScalePlace +
+                    (((wr * RT + part * HT + rt) * 16 + lr) * kScaleSteps + step % kScaleSteps) *
+                        4);
         }
     };
-    auto multiply = [&](auto half_, float s0, float s1) {
-        constexpr int r0 = decltype(half_)::value * HT;
+    auto multiply = [&](auto part_, float s0, float s1) {
+        constexpr int r0 = decltype(part_)::value * HT;
         if constexpr (FP8) {
             const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
             // a tile's 128 channels are scaled into its sums while the next tiles are
@@ -557,14 +582,15 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>&
 
     // --- the steps ---
     // Waves 0..3 and 4..7, one of each on a SIMD, take turns: while one half
-    // multiplies, the other reads its next operands, a's and half of b's tiles,
-    // then the other half of b's.  Phases of step t, four to each half of the
-    // waves, the second half's one later: read a and b's first tiles, multiply,
-    // read b's second tiles, multiply.  What lay in a place is asked for anew once
-    // all waves have read it:
+    // multiplies, the other reads its next operands.  Phases of step t, two for each
+    // part of b, the second half's one later: read a and b's first part, multiply
+    // (read b's second part, multiply).  What lay in a place is asked for anew once
+    // all waves have read it.  In two parts:
     //   a(t + 2)           in the first half's phase 3 of t,  needed six phases later;
     //   b's first (t + 2)  in the second half's phase 3 of t, needed five later;
-    //   b's second (t + 1) in the second half's phase 1 of t, needed five later.
+    //   b's second (t + 1) in the second half's phase 1 of t, needed five later;
+    // in one part, whose phases are as long:
+    //   a(t + 2) and b(t + 2) in the halves' phase 1 of t, needed four and three later.
     next.task = task;
     seek();
     if (group == 0) {
@@ -573,14 +599,14 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>&
         wait_dma<kAheadA>();
     } else {
         issue_b(0);
-        issue_b(1);
+        if (kPart == 2) issue_b(1);
         issue_b(0);
         wait_dma<kAheadB>();
     }
     EP_WAIT_LDS();
     barrier();
     if (group == 1) barrier();
-    int turn = 0;
+    int place = 0, scales = kScalePlaces - 1;     // of the step at hand
 #pragma unroll 1
     for (int taken = 0;; ++taken) {
         const int* q = lds.ring[group][taken & (kRing - 1)];
@@ -605,29 +631,39 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>&
         for (int ct = 0; ct < 4; ++ct)
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) acc[ct][rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        float s0 = FP8 ? as0[0] : 0.0f, s1 = FP8 && SWIGLU ? as1[0] : 0.0f;
 #pragma unroll 1
-        for (int step = 0; step < steps; ++step, ++turn) {
-            const float s0 = FP8 ? as0[step] : 0.0f, s1 = FP8 && SWIGLU ? as1[step] : 0.0f;
-            read_a(turn & 1);
-            read_b(turn & 1, 0, turn);
+        for (int step = 0; step < steps; ++step, place = turn_stage(place)) {
+            if (FP8 && step % kScaleSteps == 0) scales = (scales + 1) % kScalePlaces;
+            read_a(place);
+            read_b(place, 0, scales, step);
             if (group == 1) {
-                issue_b(1);
+                issue_b(kPart == 2 ? 1 : 0);
                 wait_dma<kAheadB>();
-            }
-            EP_WAIT_LDS();
-            barrier();
-            multiply(std::integral_constant<int, 0>{}, s0, s1);
-            barrier();
-            read_b(turn & 1, 1, turn);
-            if (group == 0) {
+            } else if (kPart == 1) {
                 issue_a();
-            } else {
-                issue_b(0);
-                wait_dma<kAheadB>();
             }
             EP_WAIT_LDS();
             barrier();
-            multiply(std::integral_constant<int, 1>{}, s0, s1);
+            const float g = s0, u = s1;
+            if (FP8) {      // the next step's (of the last one: that again)
+                s0 = as0[min(step + 1, steps - 1)];
+                if (SWIGLU) s1 = as1[min(step + 1, steps - 1)];
+            }
+            multiply(std::integral_constant<int, 0>{}, g, u);
+            if constexpr (kPart == 2) {
+                barrier();
+                read_b(place, 1, scales, step);
+                if (group == 0) {
+                    issue_a();
+                } else {
+                    issue_b(0);
+                    wait_dma<kAheadB>();
+                }
+                EP_WAIT_LDS();
+                barrier();
+                multiply(std::integral_constant<int, 1>{}, g, u);
+            }
             if (group == 0) wait_dma<kAheadA>();
             barrier();
         }
@@ -641,7 +677,8 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductLds<FP8>&
 
 template <Product OP, bool FP8, bool SWIGLU, bool F32, bool ADD>
 __global__ __launch_bounds__(kWaves * 64, 2) void product_kernel(const ProductArgs p) {
-    __shared__ __attribute__((aligned(1024))) ProductLds<FP8> lds;
+    __shared__ __attribute__((aligned(1024))) ProductMemory<FP8> mem;
+    ProductLds& lds = mem.lds;
     const int lane = threadIdx.x & 63;
     constexpr int kTile = SWIGLU ? kTileM / 2 : kTileM;
     const unsigned nt = (p.M + kTile - 1) / kTile;
@@ -649,7 +686,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void product_kernel(const ProductAr
     int slot = blockIdx.x / kXcds;
     if constexpr (OP == kGradWeight) {
         const int tasks = p.runs.E * ((p.B + 255) / 256) * nt, per = (tasks + kXcds - 1) / kXcds;
-        run_tasks<OP, FP8, SWIGLU, F32, ADD, 8>(p, lds, xcd * per + slot,
+        run_tasks<OP, FP8, SWIGLU, F32, ADD, 8>(p, mem, xcd * per + slot,
                                                 min(tasks, (xcd + 1) * per), stride, nt);
     } else {
         // Row blocks of the classes; every wave writes the same numbers, and reads
@@ -678,7 +715,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void product_kernel(const ProductAr
             if (sum[c] == 0) return;
             const int tasks = (int)sum[c] * nt, per = (tasks + kXcds - 1) / kXcds;
             run_tasks<OP, FP8, SWIGLU, F32, ADD, decltype(rt)::value>(
-                p, lds, xcd * per + slot, min(tasks, (xcd + 1) * per), stride, nt);
+                p, mem, xcd * per + slot, min(tasks, (xcd + 1) * per), stride, nt);
             slot = (slot + stride - per % stride) % stride;
         };
         run(std::integral_constant<int, 8>{}, 0);
