@@ -109,24 +109,19 @@ __device__ __forceinline__ void barrier() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// Row blocks of an expert with n rows for the class of row tiles RT: whole
-// blocks of 256 rows and what is left over 128 in class 8, up to 128 in class
-// 4, up to 64 in class 2.
-template <int RT>
-__device__ __forceinline__ int row_blocks(int n) {
+// Row blocks of an expert with n rows, by lists: whole blocks of 256 rows and what is
+// left over 128 in list 0, up to 128 in list 1, up to 64 in list 2.
+__device__ __forceinline__ int row_blocks(int list, int n) {
     const int rest = n & 255;
-    if (RT == 8) return (n >> 8) + (rest > 128 ? 1 : 0);
-    if (RT == 4) return rest > 64 && rest <= 128 ? 1 : 0;
-    return rest > 0 && rest <= 64 ? 1 : 0;
+    return list == 0   ? (n >> 8) + (rest > 128 ? 1 : 0)
+           : list == 1 ? (rest > 64 && rest <= 128 ? 1 : 0)
+                       : (rest > 0 && rest <= 64 ? 1 : 0);
 }
 
 constexpr int kKnown = 256;
 struct Blocks {
     int first[kKnown], rows[kKnown], upto[3][kKnown];
 };
-template <int RT>
-constexpr int kClass = RT == 8 ? 0 : RT == 4 ? 1 : 2;
-
 __device__ __forceinline__ int prefix_sum(int v) {
     const int lane = threadIdx.x & 63;
 #pragma unroll
@@ -153,10 +148,18 @@ __device__ __forceinline__ void in_bands(unsigned local, unsigned nb, unsigned n
     mt = band * kBand + rest - rb * width;
 }
 
+// Tasks of a list, which a workgroup takes from `first` on, every stride-th below
+// `end`, in pieces of a block's rows if the list's blocks are larger than its own.
+struct Share {
+    int list, first, end, stride, pieces;
+};
+
 template <Product OP, int RT>
 __device__ __forceinline__ bool find_task(Task& t, const ProductArgs& p, const Blocks& known,
-                                          int task, int end, unsigned nt, int tile) {
-    if (task >= end) return false;
+                                          const Share& s, int task, unsigned nt, int tile) {
+    if (task >= s.end) return false;
+    const int piece = (unsigned)task % (unsigned)s.pieces * (RT * 32);
+    task = (unsigned)task / (unsigned)s.pieces;
     unsigned rb, mt;
     if constexpr (OP == kGradWeight) {
         const unsigned nb = (p.B + 255) / 256, per = nb * nt;
@@ -167,7 +170,7 @@ __device__ __forceinline__ bool find_task(Task& t, const ProductArgs& p, const B
         t.e = __builtin_amdgcn_readfirstlane(t.e);
         t.n = __builtin_amdgcn_readfirstlane(t.n);
         t.begin = __builtin_amdgcn_readfirstlane((int)t.begin);
-        t.r0 = __builtin_amdgcn_readfirstlane(rb * 256);
+        t.r0 = __builtin_amdgcn_readfirstlane(rb * 256 + piece);
         t.m0 = __builtin_amdgcn_readfirstlane(mt * tile);
         return true;
     }
@@ -179,13 +182,13 @@ __device__ __forceinline__ bool find_task(Task& t, const ProductArgs& p, const B
         if (e0 < kKnown) {
             first = known.first[e0 + lane];
             rows = known.rows[e0 + lane];
-            upto = known.upto[kClass<RT>][e0 + lane];
+            upto = known.upto[s.list][e0 + lane];
         } else {
             int64_t b = 0, m = 0;
             if (e0 + lane < p.runs.E) m = p.runs.of(e0 + lane, b);
             first = (int)b;
             rows = m > 0 ? (int)m : 0;
-            upto = prefix_sum(row_blocks<RT>(rows)) + before;
+            upto = prefix_sum(row_blocks(s.list, rows)) + before;
         }
         const uint64_t hit = __ballot(upto * (int)nt > task);
         if (hit) {
@@ -193,10 +196,10 @@ __device__ __forceinline__ bool find_task(Task& t, const ProductArgs& p, const B
             t.e = e0 + at;
             t.n = __builtin_amdgcn_readlane(rows, at);
             t.begin = __builtin_amdgcn_readlane(first, at);
-            const unsigned nb = row_blocks<RT>(t.n);
+            const unsigned nb = row_blocks(s.list, t.n);
             const int local = task - (__builtin_amdgcn_readlane(upto, at) - (int)nb) * (int)nt;
             in_bands(local, nb, nt, rb, mt);
-            t.r0 = RT == 8 ? rb * 256 : t.n & ~255;
+            t.r0 = (s.list == 0 ? rb * 256 : t.n & ~255) + piece;
             t.m0 = mt * tile;
             t.r0 = __builtin_amdgcn_readfirstlane(t.r0);
             t.m0 = __builtin_amdgcn_readfirstlane(t.m0);
@@ -242,8 +245,8 @@ __device__ __forceinline__ uint32_t row_place(int r, int c) {
 __device__ __forceinline__ int column_turn(int k) { return (k & 3) | (k >> 1 & 4); }
 
 template <Product OP, bool FP8, bool SWIGLU, bool F32, bool ADD, int RT>
-__device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductMemory<FP8>& mem, int task,
-                                          int end, int stride, unsigned nt) {
+__device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductMemory<FP8>& mem,
+                                          const Share& share, unsigned nt) {
     ProductLds& lds = mem.lds;
     constexpr int kTile = SWIGLU ? kTileM / 2 : kTileM;    // result channels
     constexpr bool kAT = OP != kRows;                      // a and b by columns
@@ -285,8 +288,8 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductMemory<FP
     auto turn_stage = [](int i) { return i + 1 == kStage ? 0 : i + 1; };
     auto seek = [&]() {
         Task t;
-        const bool live = find_task<OP, RT>(t, p, lds.known, next.task, end, nt, kTile);
-        next.task += stride;
+        const bool live = find_task<OP, RT>(t, p, lds.known, share, next.task, nt, kTile);
+        next.task += share.stride;
         if (lane == 0) {
             int* q = lds.ring[group][pushed & (kRing - 1)];
             q[0] = live ? t.e : -1;
@@ -362,7 +365,7 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductMemory<FP
         } else if constexpr (kBT) {
             // 128 of 256 columns: the second wave row's lie 128 columns on
             const uint32_t c = chunk(true, 4, i);
-            at[i] = ((lane >> 4) + i * 4) * b_row + c + (c & 128) + shift;
+            at[i] = ((lane >> 4) + i * 4) * b_row + c + (kPart == 2 ? c & 128 : 0) + shift;
         } else {
             at[i] = ((lane >> 3) + i * 8) * b_row + chunk(false, 0, i) + shift;
         }
@@ -591,7 +594,7 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductMemory<FP
     //   b's second (t + 1) in the second half's phase 1 of t, needed five later;
     // in one part, whose phases are as long:
     //   a(t + 2) and b(t + 2) in the halves' phase 1 of t, needed four and three later.
-    next.task = task;
+    next.task = share.first;
     seek();
     if (group == 0) {
         issue_a();
@@ -684,43 +687,71 @@ __global__ __launch_bounds__(kWaves * 64, 2) void product_kernel(const ProductAr
     const unsigned nt = (p.M + kTile - 1) / kTile;
     const int stride = gridDim.x / kXcds, xcd = blockIdx.x % kXcds;
     int slot = blockIdx.x / kXcds;
+    // This XCD's part of a list, [begin, begin + count).
+    auto part_of = [&](int64_t blocks, int& begin) {
+        const int tasks = (int)(blocks * nt), per = (tasks + kXcds - 1) / kXcds;
+        begin = xcd * per;
+        return max(0, min(per, tasks - begin));
+    };
+    // Takes `count` of a list's tasks from `begin` on up, in pieces.
+    auto run = [&](auto rt, int list, int begin, int count, int pieces) {
+        if (count == 0) return;
+        run_tasks<OP, FP8, SWIGLU, F32, ADD, decltype(rt)::value>(
+            p, mem,
+            Share{list, begin * pieces + slot, (begin + count) * pieces, stride, pieces}, nt);
+        slot = (slot + stride - count * pieces % stride) % stride;
+    };
+    using Rows256 = std::integral_constant<int, 8>;
+    using Rows128 = std::integral_constant<int, 4>;
+    using Rows64 = std::integral_constant<int, 2>;
+    int begin[3] = {0, 0, 0}, count[3] = {0, 0, 0};
     if constexpr (OP == kGradWeight) {
-        const int tasks = p.runs.E * ((p.B + 255) / 256) * nt, per = (tasks + kXcds - 1) / kXcds;
-        run_tasks<OP, FP8, SWIGLU, F32, ADD, 8>(p, mem, xcd * per + slot,
-                                                min(tasks, (xcd + 1) * per), stride, nt);
+        count[0] = part_of((int64_t)p.runs.E * ((p.B + 255) / 256), begin[0]);
     } else {
-        // Row blocks of the classes; every wave writes the same numbers, and reads
-        // its own.
+        // Row blocks of the lists; every wave writes the same numbers, and reads its
+        // own.
         int64_t sum[3] = {0, 0, 0};
 #pragma unroll 1
         for (int e0 = 0; e0 < p.runs.E; e0 += 64) {
             int64_t b = 0, m = 0;
             if (e0 + lane < p.runs.E) m = p.runs.of(e0 + lane, b);
             const int rows = m > 0 ? (int)m : 0;
-            const int upto[3] = {prefix_sum(row_blocks<8>(rows)), prefix_sum(row_blocks<4>(rows)),
-                                 prefix_sum(row_blocks<2>(rows))};
             if (e0 < kKnown) {
                 lds.known.first[e0 + lane] = (int)b;
                 lds.known.rows[e0 + lane] = rows;
             }
 #pragma unroll
             for (int c = 0; c < 3; ++c) {
-                if (e0 < kKnown) lds.known.upto[c][e0 + lane] = (int)(sum[c] + upto[c]);
-                sum[c] += __builtin_amdgcn_readlane(upto[c], 63);
+                const int upto = prefix_sum(row_blocks(c, rows));
+                if (e0 < kKnown) lds.known.upto[c][e0 + lane] = (int)(sum[c] + upto);
+                sum[c] += __builtin_amdgcn_readlane(upto, 63);
             }
         }
-        // (a y of 2^30 tasks fits no memory: such counts do not belong to these rows)
-        if ((sum[0] + sum[1] + sum[2]) * nt >= 1 << 30) return;
-        auto run = [&](auto rt, int c) {
-            if (sum[c] == 0) return;
-            const int tasks = (int)sum[c] * nt, per = (tasks + kXcds - 1) / kXcds;
-            run_tasks<OP, FP8, SWIGLU, F32, ADD, decltype(rt)::value>(
-                p, mem, xcd * per + slot, min(tasks, (xcd + 1) * per), stride, nt);
-            slot = (slot + stride - per % stride) % stride;
-        };
-        run(std::integral_constant<int, 8>{}, 0);
-        run(std::integral_constant<int, 4>{}, 1);
-        run(std::integral_constant<int, 2>{}, 2);
+        // (a y of 2^28 tasks fits no memory: such counts do not belong to these rows)
+        if ((sum[0] + sum[1] + sum[2]) * nt >= 1 << 28) return;
+#pragma unroll
+        for (int c = 0; c < 3; ++c) count[c] = part_of(sum[c], begin[c]);
+    }
+    // Whole rounds of the largest blocks; what is left of them in pieces, if the
+    // workgroups suffice for one more round of those and of the smaller blocks.
+    const int whole = count[0] / stride * stride, rest = count[0] - whole;
+    const int small = count[1] + count[2];
+    int pieces = 1;
+    if (rest * 2 + small <= stride) pieces = 2;
+    if (OP != kGradWeight && rest * 4 + small <= stride) pieces = 4;
+    const bool halve = pieces == 4 && rest * 4 + count[1] * 2 + count[2] <= stride;
+    run(Rows256{}, 0, begin[0], pieces == 1 ? count[0] : whole, 1);
+#pragma unroll 1
+    for (int i = 0; i < (OP == kGradWeight ? 1 : 2); ++i) {
+        const int n = i == 0 ? (pieces == 2 ? rest : 0) : halve ? 0 : count[1];
+        run(Rows128{}, i, begin[i] + (i == 0 ? whole : 0), n, 2 >> i);
+    }
+    if constexpr (OP != kGradWeight) {
+#pragma unroll 1
+        for (int i = 0; i < 3; ++i) {
+            const int n = i == 0 ? (pieces == 4 ? rest : 0) : i == 1 ? (halve ? count[1] : 0) : count[2];
+            run(Rows64{}, i, begin[i] + (i == 0 ? whole : 0), n, 4 >> i);
+        }
     }
 }
 
