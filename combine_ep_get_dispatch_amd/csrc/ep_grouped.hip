@@ -137,6 +137,14 @@ struct Task {
     int64_t begin;          // first row of the run in the rows' arrays
 };
 
+// Tasks of 256 channels that run as eight times as many of 32 (us, as tasks of 256 / of
+// 32): as many as the workgroups take in one round, or in two where no expert has more
+// than 32 rows.  7168 -> 2 x 2048, E4M3, one expert x 1 row 51 / 15, x 64 rows 52 / 37;
+// 4 experts x 16 rows 52 / 35, x 64 rows (512 tasks of 32) 53 / 71; 2048 -> 7168, bf16,
+// one expert x 1 row 27 / 13, 2 x 16 rows 27 / 23, 2 x 64 rows 29 / 34, 4 x 4 rows (896
+// tasks of 32) 28 / 40.
+constexpr int kFewTasks = 32, kFewTasksOfFewRows = 64;
+
 constexpr int kBand = 8;    // channel tiles whose tasks stand next to each other
 
 // (row block, channel tile) of place `local` in bands of kBand channel tiles.
@@ -678,6 +686,147 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductMemory<FP
     barrier();
 }
 
+// Few tasks of few rows (at most 64 an expert): tiles of 32 channels, whose steps
+// the eight waves share, so that eight times as many workgroups read weights.  Wave w
+// takes steps w, w + 8, ... from global memory straight into operands, DEPTH of its
+// steps ahead (of few rows all of them, where the channels summed are few thousand),
+// and the waves' sums meet in LDS, in wave order.
+template <bool FP8, bool SWIGLU, int RT>
+__device__ __forceinline__ void run_narrow(const ProductArgs& p, ProductMemory<FP8>& mem,
+                                           const Task& t) {
+    constexpr int kElem = FP8 ? 1 : 2;
+    constexpr int CT = 2, DEPTH = RT == 1 ? 7 : RT == 2 ? 5 : 3;
+    const int lane = threadIdx.x & 63, lg = lane >> 4, lr = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t row = p.K * kElem;
+    const int steps = (int)((row + kStepBytes - 1) / kStepBytes);
+    const int KB = p.K / 128, NB = (p.M + 127) / 128;
+
+    // a: 16-channel tiles, with SWIGLU one of either half; b: 16-row tiles
+    __amdgpu_buffer_rsrc_t ab[SWIGLU ? 2 : 1];
+    constexpr int kTile = CT * 16 / (SWIGLU ? 2 : 1);
+#pragma unroll
+    for (int h = 0; h < (SWIGLU ? 2 : 1); ++h) {
+        const int64_t w0 = ((int64_t)t.e * (SWIGLU ? 2 : 1) + h) * p.M + t.m0;
+        ab[h] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.a + w0 * row), 0,
+                                                  min(kTile, p.M - t.m0) * (int)row, 0x00020000);
+    }
+    const __amdgpu_buffer_rsrc_t bb = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(p.b + t.begin * row), 0, min(RT * 16, t.n) * (int)row, 0x00020000);
+    const __amdgpu_buffer_rsrc_t sb = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<float*>(FP8 ? p.bs + t.begin * KB : nullptr), 0,
+        FP8 ? min(RT * 16, t.n) * KB * 4 : 0, 0x00020000);
+    typedef const __attribute__((address_space(4))) float* Scalars;
+    Scalars as0 = nullptr, as1 = nullptr;
+    if constexpr (FP8) {
+        as0 = (Scalars)(uint64_t)(p.as + ((int64_t)t.e * (SWIGLU ? 2 : 1) * NB + t.m0 / 128) * KB);
+        as1 = as0 + (int64_t)NB * KB;
+    }
+    struct Step {
+        i32x4 a[CT][2], b[RT][2];
+        float sx[RT], s0, s1;
+    };
+    auto load = [&](Step& q, int step) {
+        // past the last step: nothing, which arrives as zeros
+        const uint32_t at = step * kStepBytes;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            const uint32_t c = at + (ks * 4 + lg) * 16;
+            const uint32_t v = c < row ? lr * row + c : kNowhere;
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+                q.a[ct][ks] = __builtin_bit_cast(
+                    i32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                               ab[SWIGLU ? ct : 0],
+                               v == kNowhere || SWIGLU ? v : v + ct * 16 * row, 0, 0));
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+                q.b[rt][ks] = __builtin_bit_cast(
+                    i32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                               bb, v == kNowhere ? v : v + rt * 16 * row, 0, 0));
+        }
+        if constexpr (FP8) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+                q.sx[rt] = __builtin_bit_cast(
+                    float, __builtin_amdgcn_raw_buffer_load_b32(
+                               sb, ((rt * 16 + lr) * KB + min(step, KB - 1)) * 4, 0, 0));
+            q.s0 = as0[min(step, KB - 1)];
+            q.s1 = SWIGLU ? as1[min(step, KB - 1)] : q.s0;
+        }
+    };
+    f32x4 acc[CT][RT];
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) acc[ct][rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    auto use = [&](const Step& q) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                if constexpr (FP8) {
+                    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+                    i32x8 a, b;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        a[j] = q.a[ct][j / 4][j % 4];
+                        b[j] = q.b[rt][j / 4][j % 4];
+                    }
+                    const f32x4 v = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        a, b, zero, 0, 0, 0, 127, 0, 127);
+                    const float sc = q.sx[rt] * (SWIGLU && ct >= 1 ? q.s1 : q.s0);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        acc[ct][rt][j] = __builtin_fmaf(v[j], sc, acc[ct][rt][j]);
+                } else {
+#pragma unroll
+                    for (int ks = 0; ks < 2; ++ks)
+                        acc[ct][rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(bf16x8, q.a[ct][ks]),
+                            __builtin_bit_cast(bf16x8, q.b[rt][ks]), acc[ct][rt], 0, 0, 0);
+                }
+            }
+    };
+    Step q[DEPTH];
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) load(q[i], wave + i * kWaves);
+#pragma unroll 1
+    for (int step = wave; step < steps; step += DEPTH * kWaves)
+#pragma unroll
+        for (int i = 0; i < DEPTH; ++i) {
+            use(q[i]);           // (past the last step: zeros)
+            load(q[i], step + (i + DEPTH) * kWaves);
+        }
+
+    f32x4* part = reinterpret_cast<f32x4*>(mem.lds.stage);
+    constexpr int kTiles = CT * RT;
+    static_assert(kWaves * kTiles * 64 * sizeof(f32x4) <= kStageBytes, "the waves' sums");
+    __syncthreads();             // the sums of the task before are done with
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+            part[(wave * kTiles + ct * RT + rt) * 64 + lane] = acc[ct][rt];
+    __syncthreads();
+    for (int o = wave; o < (SWIGLU ? kTiles / 2 : kTiles); o += kWaves) {
+        const int ct = o / RT, rt = o % RT;
+        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f}, u = v;
+        for (int i = 0; i < kWaves; ++i) {
+            v += part[(i * kTiles + o) * 64 + lane];
+            if constexpr (SWIGLU) u += part[(i * kTiles + kTiles / 2 + o) * 64 + lane];
+        }
+        if constexpr (SWIGLU) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = silu(v[i]) * u[i];
+        }
+        const int r = rt * 16 + lr, c = t.m0 + ct * 16 + lg * 4;
+        if (r < t.n && c < p.M)
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + (t.begin + r) * p.M + c) =
+                make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    }
+}
+
 template <Product OP, bool FP8, bool SWIGLU, bool F32, bool ADD>
 __global__ __launch_bounds__(kWaves * 64, 2) void product_kernel(const ProductArgs p) {
     __shared__ __attribute__((aligned(1024))) ProductMemory<FP8> mem;
@@ -711,11 +860,13 @@ __global__ __launch_bounds__(kWaves * 64, 2) void product_kernel(const ProductAr
         // Row blocks of the lists; every wave writes the same numbers, and reads its
         // own.
         int64_t sum[3] = {0, 0, 0};
+        bool few = true;                         // no expert has more than 32 rows
 #pragma unroll 1
         for (int e0 = 0; e0 < p.runs.E; e0 += 64) {
             int64_t b = 0, m = 0;
             if (e0 + lane < p.runs.E) m = p.runs.of(e0 + lane, b);
             const int rows = m > 0 ? (int)m : 0;
+            few = few && __ballot(rows > 32) == 0;
             if (e0 < kKnown) {
                 lds.known.first[e0 + lane] = (int)b;
                 lds.known.rows[e0 + lane] = rows;
@@ -729,6 +880,26 @@ __global__ __launch_bounds__(kWaves * 64, 2) void product_kernel(const ProductAr
         }
         // (a y of 2^28 tasks fits no memory: such counts do not belong to these rows)
         if ((sum[0] + sum[1] + sum[2]) * nt >= 1 << 28) return;
+        if constexpr (OP == kRows) {
+            if (sum[0] + sum[1] == 0 && sum[2] * nt <= (few ? kFewTasksOfFewRows : kFewTasks)) {
+                constexpr int kNarrow = SWIGLU ? 16 : 32;
+                const unsigned tiles = (p.M + kNarrow - 1) / kNarrow;
+                const Share all = {2, 0, (int)sum[2] * (int)tiles, 0, 1};
+                Task t;
+                // neighbouring tiles on neighbouring workgroups: they share the rows
+#pragma unroll 1
+                for (int i = blockIdx.x; find_task<OP, 2>(t, p, lds.known, all, i, tiles, kNarrow);
+                     i += gridDim.x) {
+                    if (t.n <= 16)
+                        run_narrow<FP8, SWIGLU, 1>(p, mem, t);
+                    else if (t.n <= 32)
+                        run_narrow<FP8, SWIGLU, 2>(p, mem, t);
+                    else
+                        run_narrow<FP8, SWIGLU, 4>(p, mem, t);
+                }
+                return;
+            }
+        }
 #pragma unroll
         for (int c = 0; c < 3; ++c) count[c] = part_of(sum[c], begin[c]);
     }
@@ -757,7 +928,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void product_kernel(const ProductAr
 
 template <Product OP, bool FP8, bool SWIGLU, bool F32, bool ADD>
 hipError_t launch(const ProductArgs& p, int64_t tasks, hipStream_t s) {
-    const unsigned grid = (unsigned)((tasks < kCus ? tasks : kCus) + kXcds - 1) / kXcds * kXcds;
+    // tasks run in up to eight pieces
+    const unsigned grid =
+        (unsigned)((tasks * 8 < kCus ? tasks * 8 : kCus) + kXcds - 1) / kXcds * kXcds;
     hipLaunchKernelGGL((product_kernel<OP, FP8, SWIGLU, F32, ADD>), dim3(grid), dim3(kWaves * 64),
                        0, s, p);
     return hipGetLastError();
