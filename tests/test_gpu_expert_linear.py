@@ -88,6 +88,10 @@ SHAPES = [
     ([600], 256, 512, "offsets"),
     ([9, 1, 4] * 100, 128, 128, "offsets"),
     ([3] * 1024, 24, 8, "capacity"),
+    ([200] * 24, 64, 1024, "offsets"),       # what is left of a round, in halves
+    ([200] * 72 + [60], 64, 1032, "offsets"),    # a whole round and a rest, in quarters
+    ([64] * 3, 1160, 520, "capacity"),       # few tasks, more steps than waves
+    ([30, 31], 2056, 264, "offsets"),
 ]
 IDS = ["E%d_%dto%d_%s" % (len(c), i, n, f) for c, i, n, f in SHAPES]
 
@@ -129,6 +133,11 @@ FP8_SHAPES = [
     (EDGES, 128, 128, "capacity"),
     ([300, 5, 700, 64], 512, 512, "aligned"),
     ([9, 1, 4] * 100, 256, 64, "offsets"),
+    ([200] * 24, 128, 1024, "offsets"),
+    ([200] * 72 + [60], 128, 1032, "offsets"),
+    ([64] * 3, 1152, 520, "capacity"),
+    ([30, 31], 1920, 264, "offsets"),
+    ([16], 1408, 200, "offsets"),
 ]
 
 
@@ -311,6 +320,44 @@ def test_rows_past_the_end_and_empty_inputs():
     assert ep.expert_linear(none, w, cnt, expert_offsets=off).shape == (0, N)
     gx, gw = ep.expert_linear_backward(none[:, :N].contiguous(), none, w, cnt, expert_offsets=off)
     assert gx.shape == (0, I) and bool((gw == 0).all())
+
+
+def test_rows_and_weights_past_32_bits():
+    """Rows and experts whose places pass 2^32 bytes, next to rows of nobody."""
+    g = gen(51)
+    R, I, N = 300000, 8192, 16
+    cnt, off = device([3, 100], [5, R - 101, R - 1])
+    x = torch.full((R, I), NAN, dtype=torch.bfloat16, device="cuda")
+    gy = torch.full((R, N), NAN, dtype=torch.bfloat16, device="cuda")
+    w = torch.randint(-1, 2, (2, N, I), generator=g).bfloat16().cuda()
+    gx = torch.full((R, I), 3.0, dtype=torch.bfloat16, device="cuda")
+    runs = [slice(5, 8), slice(R - 101, R - 1)]
+    for r in runs:
+        n = r.stop - r.start
+        x[r] = torch.randint(-1, 2, (n, I), generator=g).bfloat16().cuda()
+        gy[r] = torch.randint(-1, 2, (n, N), generator=g).bfloat16().cuda()
+    y = ep.expert_linear(x, w, cnt, expert_offsets=off)
+    _, gw = ep.expert_linear_backward(gy, x, w, cnt, expert_offsets=off,
+                                      grad_weight_dtype=torch.float32, out=(gx, None))
+    for e, r in enumerate(runs):
+        assert torch.equal(y[r], (x[r].float() @ w[e].float().t().contiguous()).bfloat16())
+        assert torch.equal(gx[r], (gy[r].float() @ w[e].float()).bfloat16())
+        assert torch.equal(gw[e], gy[r].float().t().contiguous() @ x[r].float())
+    assert bool((gx[8:20] == 3.0).all()) and bool((gx[R - 130:R - 101] == 3.0).all())
+    assert bool((gx[R - 1] == 3.0).all())
+    del x, gx, gy, w
+    E, N, I = 520, 2048, 2112                # 4.5 GB of bf16 weights
+    w = torch.empty((E, N, I), dtype=torch.bfloat16, device="cuda")
+    w[E - 1] = torch.randint(-1, 2, (N, I), generator=g).bfloat16().cuda()
+    cnt, off = device([0] * (E - 1) + [70], [0] * E + [70])
+    x = torch.randint(-1, 2, (70, I), generator=g).bfloat16().cuda()
+    gy = torch.randint(-1, 2, (70, N), generator=g).bfloat16().cuda()
+    y = ep.expert_linear(x, w, cnt, expert_offsets=off)
+    assert torch.equal(y, (x.float() @ w[E - 1].float().t().contiguous()).bfloat16())
+    gx, gw = ep.expert_linear_backward(gy, x, w, cnt, expert_offsets=off)
+    assert torch.equal(gx, (gy.float() @ w[E - 1].float()).bfloat16())
+    assert torch.equal(gw[E - 1], (gy.float().t().contiguous() @ x.float()).bfloat16())
+    assert bool((gw[0] == 0).all()) and bool((gw[E - 2] == 0).all())
 
 
 def test_gradient_against_differences():
