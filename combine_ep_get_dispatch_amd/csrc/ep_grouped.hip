@@ -561,8 +561,50 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductMemory<FP
 #pragma unroll
             for (int ct = 0; ct < 4; ++ct) asm volatile("" : "+v"(acc[ct][r0 + rt]));
     };
+    // The largest tiles' results go through LDS, 2 KiB a wave behind the places: 16
+    // rows by 128 bytes, of which eight neighbouring lanes then store a whole line
+    // (stored as they stand, 8 bytes a lane: 1024 x 1024 weights' gradient 42 us, 34
+    // with whole lines; 65521 x 2048 -> 4096 rows' gradient 953, 908).
+    constexpr bool kLines = !FP8 && !SWIGLU && RT == 8;
+    static_assert(!kLines || kStage * (kABytes + kPart * kBStage) + kWaves * 2048 <= kStageBytes);
     auto store = [&](const Task& t) {
         const int rows = OP == kGradWeight ? p.B : t.n;
+        if constexpr (kLines) {
+            constexpr int kOut = F32 ? 4 : 2;           // bytes
+            constexpr int kTiles = F32 ? 2 : 4;         // 16-channel tiles of a line
+            uint8_t* s = lds.stage + kStage * (kABytes + kPart * kBStage) + wave * 2048;
+            const uint32_t turn = (lr >> 1 & 7) << 4;
+            const uint32_t to = lr * 128 + (F32 ? lg * 16 : lg * 8);
+            const int line = lane >> 3;
+            const uint32_t from = line * 128 + (((lane & 7) ^ (line >> 1)) << 4);
+#pragma unroll
+            for (int i = 0; i < RT * 4 / kTiles; ++i) {
+                const int rt = i * kTiles / 4, c0 = i * kTiles % 4;
+#pragma unroll
+                for (int j = 0; j < kTiles; ++j) {
+                    const f32x4 v = acc[c0 + j][rt];
+                    uint8_t* q = s + ((to + j * 16 * kOut) ^ turn);
+                    if constexpr (F32)
+                        *reinterpret_cast<f32x4*>(q) = v;
+                    else
+                        *reinterpret_cast<uint2*>(q) =
+                            make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+                }
+                const int c = t.m0 + wm * 64 + c0 * 16 + (lane & 7) * (16 / kOut);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    f32x4 v = *reinterpret_cast<const f32x4*>(s + (from ^ h * 64) + h * 1024);
+                    const int r = t.r0 + (wr * RT + rt) * 16 + h * 8 + line;
+                    if (r >= rows || c >= p.M) continue;
+                    const int64_t row = OP == kGradWeight ? (int64_t)t.e * p.B + r : t.begin + r;
+                    f32x4* o = reinterpret_cast<f32x4*>(static_cast<uint8_t*>(p.y) +
+                                                        (row * p.M + c) * kOut);
+                    if constexpr (ADD) v += *o;
+                    *o = v;
+                }
+            }
+            return;
+        }
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
             const int r = t.r0 + (wr * RT + rt) * 16 + lr;
