@@ -1,10 +1,44 @@
 // The experts' products over ragged runs of rows, and their gradients, on
 // gfx950:
-//   y[r, n]  = sum_i x[r, i] * w[e, n, i]        e the expert of row r
-//   gx[r, i] = sum_n gy[r, n] * w[e, n, i]
+//   y[r, n]     = sum_i x[r, i] * w[e, n, i]        e the expert of row r
+//   gx[r, i]    = sum_n gy[r, n] * w[e, n, i]
 //   gw[e, n, i] = sum over e's rows r of gy[r, n] * x[r, i]
 // in bf16, or y from E4M3 rows and weights, whose codes' products are summed
 // over 128 channels and then scaled, fp32 throughout and rounded once.
+//
+// What bounds it.  With n rows an expert, a weight of b bytes takes 2n operations: up to
+// about 128 rows (bf16) the weights' way from HBM, beyond that the matrix instructions,
+// and for long sums the card's power: while it multiplies without a pause it lowers its
+// clock, from 2.4 to 1.9 GHz and less, and a library product of the same size does no
+// better than 1.2 times these kernels' rate (65521 x 4096 -> 2048, 8 experts: 852-880 us,
+// one library product of as many rows 715 in short runs and 940 in long ones).
+//
+// Layout.  What gives the results' neighbouring channels (a: weights, or x for gw) is the
+// A operand, what gives their rows (b: rows, or gy for gw) the B operand, so that a lane
+// ends with four neighbouring channels of one row.  A workgroup owns 256 channels by up to
+// 256 rows; both operands' tiles come to LDS by loads that go there directly, in steps of
+// 128 bytes of summed channels, bounded by buffer ranges: what lies past a run's last row,
+// the last channel or the matrix's end arrives as zeros, and neither a short run nor an odd
+// size needs a branch of its own.  (A step by rows that ends inside 128 bytes sends its lanes
+// past the range by itself.)  Where the summed index is the slow one (the weights of gx,
+// both operands of gw) a step's columns lie in LDS as they came, and the reads that
+// transpose make operands of them.  Chunks of 16 or 32 bytes change places with the row
+// (row_place, column_turn), so that no read of an operand meets a bank conflict (counted: 0).
+//
+// Eight waves, four of 64 channels on either half of the rows; a half's row tiles are in
+// registers (128 sums a lane).  The halves take turns at reading and multiplying (see
+// run_tasks).  Rows per block: whole blocks of 256, what is left in blocks of up to 256, 128
+// or 64, so that the last block of an expert costs what its rows need.
+//
+// What it took on MI355X (65521 x 4096 -> 2048 bf16 / 16384 x 7168 -> 2 x 2048 E4M3):
+// 1007 / 1194 us with both halves fetching at once; 1003 / 842 with one half fetching
+// and addresses made where they are used (registers had gone to scratch, whose reads waited
+// for the loads to LDS); 943 / 749 with b in two parts, which lets each place be asked for
+// five phases ahead; 943 / 637 with sums scaled two tiles late; 884 / 605 with four loads an
+// address setting (loads between the matrix instructions instead: 1035 / 697); 861 / 576 with
+// what is left of the largest blocks in pieces; 852 / 565 with whole lines stored.  Tried
+// without gain: 32 x 32 matrix instructions (908), wave priorities, stores that the next
+// step does not wait for.
 #include "ep_internal.h"
 #include "ep_device.h"
 
@@ -54,7 +88,8 @@ constexpr int kScaleSteps = 4, kScalePlaces = 4;
 // one after the other; what lies past the buffer's end arrives as zeros.  A load's
 // place i * 1024 counts in both memories, so `at` holds what is missing from
 // kShift, which the buffer's base makes up for.  Waited for by vmcnt; the compiler
-// does not count it.
+// does not count it (where it waits for loads of its own it waits for more than it
+// knows, never for less).  M0 holds the place in LDS; nothing else here uses it.
 constexpr int kShift = 3072;
 template <int N>
 __device__ __forceinline__ void dma16(const uint32_t* at, const i32x4& buffer, uint32_t lds) {
@@ -103,9 +138,13 @@ __device__ __forceinline__ void wait_dma() {
     asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
 }
 
+// A barrier that, unlike __syncthreads, does not wait for loads to LDS on their way;
+// no access to memory moves across.
 __device__ __forceinline__ void barrier() {
     __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
 }
 

@@ -567,7 +567,11 @@ ep_status_t ep_expert_linear_w4(const void *x, const float *x_scales, ep_dtype_t
  *   two, ahead of the fp32 sums.)
  *   N > 0, N % 8 == 0; x, weight, y 16-byte aligned.  EP_ERR_UNSUPPORTED for
  * E > EP_MAX_EXPERTS, I or W > EP_MAX_LINEAR_CHANNELS.
- *   No workspace, one launch.  Equal arguments give equal bits.
+ *   No workspace, one launch.  Equal arguments give equal bits.  A row's results
+ * are the same bits whatever rows stand beside it, but for one choice: where no
+ * expert has more than 64 rows and there is little to do (up to 32 tiles of 256
+ * weight channels by an expert's rows, 64 if no expert has more than 32 rows), a
+ * sum is taken in eight shares, else channel by channel.
  *   (No page describes the experts themselves; the definitions of this call and
  * the next ones are this library's.)
  */

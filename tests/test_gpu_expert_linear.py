@@ -278,6 +278,41 @@ def test_large_sums_of_integers():
     assert torch.equal(again[:off[-1]], y[:off[-1]])
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_rows_beside_a_row_do_not_change_its_bits(fp8):
+    """The same rows alone in their expert and among many, in blocks of every
+    size, give the same bits (many experts: sums are not taken in shares)."""
+    E, I, N = 80, 640, 264
+    g = gen(61)
+    few, many = [9] * E, [9] * E
+    many[0], many[1], many[2], many[3] = 300, 200, 100, 50
+    w = torch.randn((E, N, I), generator=g)
+    rows = torch.randn((sum(many), I), generator=g)
+    keep, at = [], 0
+    for n in many:
+        keep += list(range(at, at + 9))
+        at += n
+    kw = {}
+    if fp8:
+        q = lambda t: (t * 60).to(torch.float8_e4m3fn).view(torch.uint8)
+        w, rows = q(w), q(rows)
+        xs = torch.rand((rows.shape[0], I // 128), generator=g) * 0.01 + 0.001
+        kw["weight_scales"] = (torch.rand((E, 3, I // 128), generator=g) * 0.01).cuda()
+    else:
+        w, rows = w.bfloat16(), rows.bfloat16()
+    out = []
+    for counts, x in ((few, rows[keep]), (many, rows)):
+        off = [0]
+        for n in counts:
+            off.append(off[-1] + n)
+        cnt, d_off = device(counts, off)
+        if fp8:
+            kw["x_scales"] = (xs[keep] if x.shape[0] < rows.shape[0] else xs).contiguous().cuda()
+        out.append(ep.expert_linear(x.contiguous().cuda(), w.cuda(), cnt, expert_offsets=d_off,
+                                    **kw).cpu())
+    assert torch.equal(out[0], out[1][keep])
+
+
 def test_values_that_are_not_numbers_stay_in_their_row():
     """An infinity or NaN in a row or a weight reaches the results that use it
     and no others."""
