@@ -559,17 +559,10 @@ ep_status_t ep_expert_linear_backward(const void* grad_y, const void* x, const v
     if (st != EP_OK) return st;
     if (I > EP_MAX_LINEAR_CHANNELS || N > EP_MAX_LINEAR_CHANNELS) return EP_ERR_UNSUPPORTED;
     const ep::RowRuns runs = {expert_offsets, num_tokens_per_expert, capacity, E, num_rows};
-    hipStream_t s = static_cast<hipStream_t>(stream);
-    const uint16_t* gy = static_cast<const uint16_t*>(grad_y);
-    if (grad_x) {
-        st = from_hip(ep::launch_expert_grad_rows(gy, runs, I, N,
-                                                  static_cast<const uint16_t*>(weight),
-                                                  static_cast<uint16_t*>(grad_x), s));
-        if (st != EP_OK) return st;
-    }
-    if (!grad_weight) return EP_OK;
-    return from_hip(ep::launch_expert_grad_weight(gy, static_cast<const uint16_t*>(x), runs, I, N,
-                                                  grad_weight, fp32, accumulate != 0, s));
+    return from_hip(ep::launch_expert_gradients(
+        static_cast<const uint16_t*>(grad_y), static_cast<const uint16_t*>(x), runs, I, N,
+        static_cast<const uint16_t*>(weight), static_cast<uint16_t*>(grad_x), grad_weight, fp32,
+        accumulate != 0, static_cast<hipStream_t>(stream)));
 }
 
 ep_status_t ep_expert_swiglu(const void* gate_up, int64_t num_rows, const int32_t* expert_offsets,

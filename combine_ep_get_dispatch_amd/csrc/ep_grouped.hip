@@ -86,30 +86,31 @@ constexpr int kScaleSteps = 4, kScalePlaces = 4;
 
 // 16 bytes per lane from a bounded buffer to LDS, lane after lane, N loads
 // one after the other; what lies past the buffer's end arrives as zeros.  A load's
-// place i * 1024 counts in both memories, so `at` holds what is missing from
+// place i * kLoadBytes counts in both memories, so `at` holds what is missing from
 // kShift, which the buffer's base makes up for.  Waited for by vmcnt; the compiler
 // does not count it (where it waits for loads of its own it waits for more than it
 // knows, never for less).  M0 holds the place in LDS; nothing else here uses it.
-constexpr int kShift = 3072;
+constexpr int kLoadBytes = 1024, kShift = 3 * kLoadBytes;
 template <int N>
 __device__ __forceinline__ void dma16(const uint32_t* at, const i32x4& buffer, uint32_t lds) {
     if constexpr (N == 4)
         asm volatile(
             "s_mov_b32 m0, %5\n\ts_nop 0\n\t"
             "buffer_load_dwordx4 %0, %4, 0 offen lds\n\t"
-            "buffer_load_dwordx4 %1, %4, 0 offen offset:1024 lds\n\t"
-            "buffer_load_dwordx4 %2, %4, 0 offen offset:2048 lds\n\t"
-            "buffer_load_dwordx4 %3, %4, 0 offen offset:3072 lds"
+            "buffer_load_dwordx4 %1, %4, 0 offen offset:%6 lds\n\t"
+            "buffer_load_dwordx4 %2, %4, 0 offen offset:%7 lds\n\t"
+            "buffer_load_dwordx4 %3, %4, 0 offen offset:%8 lds"
             :
-            : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "s"(buffer), "s"(lds)
+            : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "s"(buffer), "s"(lds),
+              "n"(kLoadBytes), "n"(2 * kLoadBytes), "n"(3 * kLoadBytes)
             : "memory");
     else if constexpr (N == 2)
         asm volatile(
             "s_mov_b32 m0, %3\n\ts_nop 0\n\t"
             "buffer_load_dwordx4 %0, %2, 0 offen lds\n\t"
-            "buffer_load_dwordx4 %1, %2, 0 offen offset:1024 lds"
+            "buffer_load_dwordx4 %1, %2, 0 offen offset:%4 lds"
             :
-            : "v"(at[0]), "v"(at[1]), "s"(buffer), "s"(lds)
+            : "v"(at[0]), "v"(at[1]), "s"(buffer), "s"(lds), "n"(kLoadBytes)
             : "memory");
     else
         asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
@@ -908,15 +909,17 @@ __device__ __forceinline__ void run_narrow(const ProductArgs& p, ProductMemory<F
     }
 }
 
+// All tasks of a product.  Every XCD (workgroups i, i + 8, ...) takes one run of each
+// list's tasks, so that its workgroups share rows and weights; a workgroup's `slot` among
+// them moves on, so that those that have had no task of a round come first in the next.
 template <Product OP, bool FP8, bool SWIGLU, bool F32, bool ADD>
-__global__ __launch_bounds__(kWaves * 64, 2) void product_kernel(const ProductArgs p) {
-    __shared__ __attribute__((aligned(1024))) ProductMemory<FP8> mem;
+__device__ __forceinline__ void run_product(const ProductArgs& p, ProductMemory<FP8>& mem,
+                                            int& slot) {
     ProductLds& lds = mem.lds;
     const int lane = threadIdx.x & 63;
     constexpr int kTile = SWIGLU ? kTileM / 2 : kTileM;
     const unsigned nt = (p.M + kTile - 1) / kTile;
     const int stride = gridDim.x / kXcds, xcd = blockIdx.x % kXcds;
-    int slot = blockIdx.x / kXcds;
     // This XCD's part of a list, [begin, begin + count).
     auto part_of = [&](int64_t blocks, int& begin) {
         const int tasks = (int)(blocks * nt), per = (tasks + kXcds - 1) / kXcds;
@@ -1008,12 +1011,33 @@ __global__ __launch_bounds__(kWaves * 64, 2) void product_kernel(const ProductAr
 }
 
 template <Product OP, bool FP8, bool SWIGLU, bool F32, bool ADD>
+__global__ __launch_bounds__(kWaves * 64, 2) void product_kernel(const ProductArgs p) {
+    __shared__ __attribute__((aligned(1024))) ProductMemory<FP8> mem;
+    int slot = blockIdx.x / kXcds;
+    run_product<OP, FP8, SWIGLU, F32, ADD>(p, mem, slot);
+}
+
+// Both gradients in one launch: the weights' tasks start on the workgroups that the last
+// round of the rows' leaves idle (6001 rows of 40 experts, 1032 -> 1000: 83 us as two
+// launches, 77 as one).
+template <bool F32, bool ADD>
+__global__ __launch_bounds__(kWaves * 64, 2) void gradients_kernel(const ProductArgs rows,
+                                                                   const ProductArgs weight) {
+    __shared__ __attribute__((aligned(1024))) ProductMemory<false> mem;
+    int slot = blockIdx.x / kXcds;
+    run_product<kGradRows, false, false, false, false>(rows, mem, slot);
+    run_product<kGradWeight, false, false, F32, ADD>(weight, mem, slot);
+}
+
+// Workgroups for so many tasks, which may run in up to eight pieces each.
+dim3 workgroups(int64_t tasks) {
+    return dim3((unsigned)((tasks * 8 < kCus ? tasks * 8 : kCus) + kXcds - 1) / kXcds * kXcds);
+}
+
+template <Product OP, bool FP8, bool SWIGLU, bool F32, bool ADD>
 hipError_t launch(const ProductArgs& p, int64_t tasks, hipStream_t s) {
-    // tasks run in up to eight pieces
-    const unsigned grid =
-        (unsigned)((tasks * 8 < kCus ? tasks * 8 : kCus) + kXcds - 1) / kXcds * kXcds;
-    hipLaunchKernelGGL((product_kernel<OP, FP8, SWIGLU, F32, ADD>), dim3(grid), dim3(kWaves * 64),
-                       0, s, p);
+    hipLaunchKernelGGL((product_kernel<OP, FP8, SWIGLU, F32, ADD>), workgroups(tasks),
+                       dim3(kWaves * 64), 0, s, p);
     return hipGetLastError();
 }
 
@@ -1040,27 +1064,34 @@ hipError_t launch_expert_linear(const void* x, const float* xs, const RowRuns& r
                   : launch<kRows, false, false, false, false>(p, tasks, s);
 }
 
-hipError_t launch_expert_grad_rows(const uint16_t* gy, const RowRuns& runs, int I, int N,
-                                   const uint16_t* w, uint16_t* gx, hipStream_t s) {
-    if (runs.num_rows == 0) return hipSuccess;
-    const ProductArgs p = {reinterpret_cast<const uint8_t*>(w),
-                           reinterpret_cast<const uint8_t*>(gy),
-                           nullptr, nullptr, runs, N, I, 0, gx};
-    return launch<kGradRows, false, false, false, false>(
-        p, most_blocks(runs) * ((I + kTileM - 1) / kTileM), s);
-}
-
-hipError_t launch_expert_grad_weight(const uint16_t* gy, const uint16_t* x, const RowRuns& runs,
-                                     int I, int N, void* gw, bool fp32, bool accumulate,
-                                     hipStream_t s) {
-    const ProductArgs p = {reinterpret_cast<const uint8_t*>(x),
-                           reinterpret_cast<const uint8_t*>(gy),
-                           nullptr, nullptr, runs, 0, I, N, gw};
-    const int64_t tasks =
-        (int64_t)runs.E * ((N + 255) / 256) * ((I + kTileM - 1) / kTileM);
-    if (!fp32) return launch<kGradWeight, false, false, false, false>(p, tasks, s);
-    return accumulate ? launch<kGradWeight, false, false, true, true>(p, tasks, s)
-                      : launch<kGradWeight, false, false, true, false>(p, tasks, s);
+hipError_t launch_expert_gradients(const uint16_t* gy, const uint16_t* x, const RowRuns& runs,
+                                   int I, int N, const uint16_t* w, uint16_t* gx, void* gw,
+                                   bool fp32, bool accumulate, hipStream_t s) {
+    const uint8_t* g = reinterpret_cast<const uint8_t*>(gy);
+    const ProductArgs rows = {reinterpret_cast<const uint8_t*>(w), g, nullptr, nullptr,
+                              runs, N, I, 0, gx};
+    const ProductArgs weight = {reinterpret_cast<const uint8_t*>(x), g, nullptr, nullptr,
+                                runs, 0, I, N, gw};
+    const int64_t tiles = (I + kTileM - 1) / kTileM;
+    const int64_t row_tasks = gx ? most_blocks(runs) * tiles : 0;
+    const int64_t weight_tasks = gw ? (int64_t)runs.E * ((N + 255) / 256) * tiles : 0;
+    if (!gw) {
+        if (runs.num_rows == 0) return hipSuccess;
+        return launch<kGradRows, false, false, false, false>(rows, row_tasks, s);
+    }
+    if (!gx || runs.num_rows == 0) {
+        if (!fp32) return launch<kGradWeight, false, false, false, false>(weight, weight_tasks, s);
+        return accumulate ? launch<kGradWeight, false, false, true, true>(weight, weight_tasks, s)
+                          : launch<kGradWeight, false, false, true, false>(weight, weight_tasks, s);
+    }
+    const dim3 grid = workgroups(row_tasks + weight_tasks), block(kWaves * 64);
+    if (!fp32)
+        hipLaunchKernelGGL((gradients_kernel<false, false>), grid, block, 0, s, rows, weight);
+    else if (accumulate)
+        hipLaunchKernelGGL((gradients_kernel<true, true>), grid, block, 0, s, rows, weight);
+    else
+        hipLaunchKernelGGL((gradients_kernel<true, false>), grid, block, 0, s, rows, weight);
+    return hipGetLastError();
 }
 
 }  // namespace ep

@@ -313,11 +313,10 @@ struct RowRuns {
 hipError_t launch_expert_linear(const void* x, const float* xs, const RowRuns& runs, int I, int N,
                                 const void* w, const float* ws, bool swiglu, uint16_t* y,
                                 hipStream_t s);
-hipError_t launch_expert_grad_rows(const uint16_t* gy, const RowRuns& runs, int I, int N,
-                                   const uint16_t* w, uint16_t* gx, hipStream_t s);
-hipError_t launch_expert_grad_weight(const uint16_t* gy, const uint16_t* x, const RowRuns& runs,
-                                     int I, int N, void* gw, bool fp32, bool accumulate,
-                                     hipStream_t s);
+// gx null: no rows' gradient (w is then unused); gw null: no weights' gradient (x is).
+hipError_t launch_expert_gradients(const uint16_t* gy, const uint16_t* x, const RowRuns& runs,
+                                   int I, int N, const uint16_t* w, uint16_t* gx, void* gw,
+                                   bool fp32, bool accumulate, hipStream_t s);
 
 // ------------------------------------------------------------------- gate ---
 constexpr int kGateThreads = 256;

@@ -596,7 +596,7 @@ ep_status_t ep_expert_linear(const void *x, const float *x_scales, ep_dtype_t dt
  * only grad_x (x may then be NULL); not both.  Shapes, limits and errors as
  * ep_expert_linear, with N the channels of grad_y bf16 [num_rows*N]; x and
  * grad_x bf16 [num_rows*I], weight and grad_weight [E, N, I]; all 16-byte
- * aligned.  No workspace, a launch for each gradient.
+ * aligned.  No workspace, one launch.
  */
 ep_status_t ep_expert_linear_backward(const void *grad_y, const void *x, const void *weight,
                                       int64_t num_rows, const int32_t *expert_offsets,
