@@ -336,6 +336,53 @@ def test_values_that_are_not_numbers_stay_in_their_row():
             assert torch.equal(~torch.isfinite(y[r]), bad), r
 
 
+@pytest.mark.parametrize("counts", [[40, 200, 9], [5, 20, 3]])
+def test_codes_that_are_not_numbers_stay_in_their_row(counts):
+    """The same in E4M3: a NaN code or an infinite scale of a row, a NaN code of a
+    weight; in blocks and in the few tasks whose sums are taken in shares."""
+    I, N = 256, 136
+    g = gen(23)
+    off, C, R = place(counts, "aligned")
+    runs = ref.ranges(counts, off, C, R)
+    x, w = codes_of(ints((R, I), g)), codes_of(ints((3, N, I), g, 2))
+    xs, ws = torch.ones((R, I // 128)), torch.ones((3, 2, I // 128))
+    x[off[1] + 5, 7] = 0x7F
+    xs[off[0] + 2, 1] = math.inf
+    w[2, 11, 200] = 0xFF
+    x, _ = poison(x, runs, 0x7F)
+    xs, _ = poison(xs, runs, NAN)
+    d_cnt, d_off = device(counts, off)
+    y = ep.expert_linear(x.cuda(), w.cuda(), d_cnt, expert_offsets=d_off, x_scales=xs.cuda(),
+                         weight_scales=ws.cuda()).cpu()
+    for e, (b, n) in enumerate(runs):
+        for r in range(b, b + n):
+            bad = torch.zeros(N, dtype=torch.bool)
+            if r in (off[1] + 5, off[0] + 2):
+                bad[:] = True
+            if e == 2:
+                bad[11] = True
+            assert torch.equal(~torch.isfinite(y[r]), bad), r
+
+
+def test_calls_on_two_streams_at_once():
+    """Products, gradients, norm and activation of two sets of inputs, in flight
+    on two streams at the same time, give what they give alone."""
+    T, H, F, E, K = 300, 256, 128, 8, 2
+    sets = [{k: v.cuda() for k, v in layer_inputs(T, H, F, E, 200 + i).items()} for i in range(2)]
+    alone = [[t.clone() for t in training_step(s, E, K)] for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(3):
+        got = []
+        for s, st in zip(sets, streams):
+            with torch.cuda.stream(st):
+                got.append(training_step(s, E, K))
+        torch.cuda.synchronize()
+        for a, b in zip(got, alone):
+            for u, v in zip(a, b):
+                assert torch.equal(u, v)
+
+
 def test_rows_past_the_end_and_empty_inputs():
     """Runs that reach past num_rows are cut; counts of zero and below are none;
     no rows at all leave gradients of 0."""
