@@ -182,7 +182,8 @@ struct Task {
 // than 32 rows.  7168 -> 2 x 2048, E4M3, one expert x 1 row 51 / 15, x 64 rows 52 / 37;
 // 4 experts x 16 rows 52 / 35, x 64 rows (512 tasks of 32) 53 / 71; 2048 -> 7168, bf16,
 // one expert x 1 row 27 / 13, 2 x 16 rows 27 / 23, 2 x 64 rows 29 / 34, 4 x 4 rows (896
-// tasks of 32) 28 / 40.
+// tasks of 32) 28 / 40.  One expert of more than 64 rows, in runs of 64, would lose: E4M3, 100 rows
+// 53 / 71, 200 rows 53 / 66, 500 rows 53 / 67.
 constexpr int kFewTasks = 32, kFewTasksOfFewRows = 64;
 
 // Channel tiles whose tasks stand next to each other, so that the tasks an XCD has at hand
