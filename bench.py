@@ -199,7 +199,7 @@ def cpu_baseline(wl_case, nbytes, seconds, capacity=None, align=0, dedup=False):
         log("cpu oracle pass %d: %.2f s total" % (passes, t_total))
         if t_total >= seconds:
             break
-    return {"value": round(nbytes * passes / t_total / 1e9, 3), "unit": "GB/s", "cores": 1,
+    return {"value": float("%.6g" % (nbytes * passes / t_total / 1e9)), "unit": "GB/s", "cores": 1,
             "kind": "oracle",
             "sample": "%d full pass(es) of the %s workload (T=%d), %s, "
                       "single-threaded C oracle, %.1f s"
