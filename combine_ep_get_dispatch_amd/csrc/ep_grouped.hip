@@ -89,7 +89,7 @@ constexpr int kScaleSteps = 4, kScalePlaces = 4;
 // place i * kLoadBytes counts in both memories, so `at` holds what is missing from
 // kShift, which the buffer's base makes up for.  Waited for by vmcnt; the compiler
 // does not count it (where it waits for loads of its own it waits for more than it
-// knows, never for less).  M0 holds the place in LDS; nothing else here uses it.
+// knows, never for less).  M0 holds the place in LDS: each block sets it and says so.
 constexpr int kLoadBytes = 1024, kShift = 3 * kLoadBytes;
 template <int N>
 __device__ __forceinline__ void dma16(const uint32_t* at, const i32x4& buffer, uint32_t lds) {
@@ -103,7 +103,7 @@ __device__ __forceinline__ void dma16(const uint32_t* at, const i32x4& buffer, u
             :
             : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "s"(buffer), "s"(lds),
               "n"(kLoadBytes), "n"(2 * kLoadBytes), "n"(3 * kLoadBytes)
-            : "memory");
+            : "memory", "m0");
     else if constexpr (N == 2)
         asm volatile(
             "s_mov_b32 m0, %3\n\ts_nop 0\n\t"
@@ -111,12 +111,12 @@ __device__ __forceinline__ void dma16(const uint32_t* at, const i32x4& buffer, u
             "buffer_load_dwordx4 %1, %2, 0 offen offset:%4 lds"
             :
             : "v"(at[0]), "v"(at[1]), "s"(buffer), "s"(lds), "n"(kLoadBytes)
-            : "memory");
+            : "memory", "m0");
     else
         asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
                      :
                      : "v"(at[0]), "s"(buffer), "s"(lds)
-                     : "memory");
+                     : "memory", "m0");
 }
 constexpr uint32_t kNowhere = 0x80000000u;   // past every buffer's end
 
