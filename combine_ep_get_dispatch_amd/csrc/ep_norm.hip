@@ -13,6 +13,7 @@
 #include "ep_internal.h"
 #include "ep_device.h"
 
+#include <cfloat>
 #include <type_traits>
 
 namespace ep {
@@ -80,12 +81,16 @@ __device__ __forceinline__ float block_sum(float v, float* s) {
     return seg_sum<16>(i < waves ? s[i] : 0.0f);
 }
 
+// Where the mean of the squares (and eps) is at least this, what squares lost below
+// 2^-126, up to 2^-150 each, does not count.
+constexpr float kLeastMean = 0x1p-80f;
+
 // One row per workgroup; a thread holds chunks of 8 channels tid, tid + blockDim, ...,
 // NC of them, so 16 neighbouring lanes hold 128 neighbouring channels, one scale.
 template <int NC, bool W32>
 __global__ __launch_bounds__(1024) void rms_norm_kernel(const NormArgs p) {
     const int kThreads = blockDim.x;
-    __shared__ float part[16];
+    __shared__ float part[2][16];
     const int chunks = p.H / 8;
     const int64_t row = blockIdx.x;
     const uint4* x = reinterpret_cast<const uint4*>(p.x + row * p.H);
@@ -123,9 +128,34 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(const NormArgs p) {
         for (int j = 0; j < 8; ++j) s = __builtin_fmaf(a[j], a[j], s);
         sum += (int)threadIdx.x + i * kThreads < chunks ? s : 0.0f;
     }
-    sum = block_sum(sum, part);
-    const float inv = 1.0f / sqrtf(sum / (float)p.H + p.eps);
-    if (p.inv && threadIdx.x == 0) p.inv[row] = inv;
+    sum = block_sum(sum, part[0]);
+    const float mean = sum / (float)p.H + p.eps;
+    float inv = 1.0f / sqrtf(mean), inv_out = inv;
+    if (!(mean >= kLeastMean && mean <= FLT_MAX)) {      // the same in every thread
+        // Squares that pass fp32's range, or may have lost bits below it: once more, of
+        // channels times a power of two.  2^90 h is exact in bf16 and takes h's place
+        // (1 / rms itself may pass the range); 2^-72 h might not be.
+        const bool up = mean < kLeastMean;
+        const float scale = up ? 0x1p90f : 0x1p-72f;
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            float a[8], s = 0.0f;
+            unpack8(a, v[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                a[j] *= scale;
+                s = __builtin_fmaf(a[j], a[j], s);
+            }
+            if (up) v[i] = pack8(a);
+            sum += (int)threadIdx.x + i * kThreads < chunks ? s : 0.0f;
+        }
+        sum = block_sum(sum, part[1]);
+        inv = 1.0f / sqrtf(sum / (float)p.H + p.eps * scale * scale);
+        inv_out = inv * scale;
+        if (!up) inv = inv_out;
+    }
+    if (p.inv && threadIdx.x == 0) p.inv[row] = inv_out;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int c = threadIdx.x + i * kThreads;

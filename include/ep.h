@@ -645,7 +645,9 @@ ep_status_t ep_expert_swiglu_backward(const void *grad_y, const void *gate_up, i
  *   h[t,i]  = x[t,i], or with a residual bf16(x[t,i] + residual[t,i])
  *   inv[t]  = 1 / sqrt(mean over i of h[t,i]^2 + eps)
  *   y[t,i]  = h[t,i] * inv[t] * weight[i]
- * computed in fp32.  Written are
+ * computed in fp32, for finite h of any size (squares past fp32's range are taken
+ * of scaled channels).  With eps 0 a row whose mean square is below 2^-256 has a y,
+ * but inv_rms +inf, and a row of zeros has a y of NaN.  Written are
  *   y bf16 [T*H] (NULL: not asked for), rounded once;
  *   codes uint8 [T*H] and scales fp32 [T*H/128] (NULL: not asked for;
  *   H % 128 == 0), y in E4M3 by ep_dispatch's rule, from the fp32 results;
