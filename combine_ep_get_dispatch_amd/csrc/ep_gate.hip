@@ -89,7 +89,8 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(const GateArgs p) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float s = sigmoid(gf[i]), si = gf[i] * s;
-                    o[i] = df[i] * uf[i] * __builtin_fmaf(si, 1.0f - s, s);
+                    // grad_y * up may pass fp32's range where the gradient does not
+                    o[i] = df[i] * __builtin_fmaf(si, 1.0f - s, s) * uf[i];
                     e[i] = df[i] * si;
                 }
                 uint4* out = reinterpret_cast<uint4*>(p.y + (r0 + row[j]) * 2 * p.N);
