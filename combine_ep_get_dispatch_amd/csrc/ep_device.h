@@ -107,16 +107,51 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                       pack_bf16x2(f[6], f[7]));
 }
 
-// 1 / (1 + exp(-v)), for results of 16 bits or fewer: v_exp_f32 and v_rcp_f32 are off
-// by a step of fp32 each, and exp multiplies the rounding of v * log2(e) by |v|, so
-// the result is off by at most 1.25 |v| + 5 half steps: 2^-17 of it where exp(-v) is
-// still in range (v > -87.3; 0 below).  (With expf and a division the activation's
-// kernels were bound by these, not by HBM: 32768 x 2048 to E4M3 83 us, 80 with what
-// the product loses made up for.)
-__device__ __forceinline__ float sigmoid(float v) {
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504f));
+// What silu(v) = v / (1 + exp(-v)) and its gradient are made of: q = exp(v / 2) and
+// r = 1 / (1 + q^2), so that 1 / (1 + exp(-v)) = q * (q r) and 1 - that = r.  In halves
+// nothing passes fp32's range where a result does not: exp(-v) would above 88, and its
+// reciprocal be lost where silu(v), let alone silu(v) * u, is a normal number; q is 0
+// only below v = -174.  (Above 17.5 the sigmoid is 1 to half a step.)
+// In half steps of fp32: v_exp_f32 and v_rcp_f32 are off by 2 each, and what v * log2(e)
+// / 2 loses to its rounding, which exp would multiply by |v|, is made up for: q is off by
+// 3, q^2 / (1 + q^2) by 6 and 4 more, silu(v) * u by 13, under 2^-20.
+struct Sigmoid {
+    float q, qr, r;
+};
+__device__ __forceinline__ Sigmoid sigmoid(float v) {
+    constexpr float kHigh = 0x1.715476p-1f, kLow = 0x1.4ae0cp-27f;     // log2(e) / 2
+    const float c = __builtin_amdgcn_fmed3f(v, -200.0f, 17.5f), y = c * kHigh;
+    const float lost = __builtin_fmaf(c, kLow, __builtin_fmaf(c, kHigh, -y));
+    const float e = __builtin_amdgcn_exp2f(y);
+    const float q = __builtin_fmaf(e, lost * 0.693147181f, e);
+    const float r = __builtin_amdgcn_rcpf(__builtin_fmaf(q, q, 1.0f));
+    return {q, q * r, r};
 }
-__device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
+__device__ __forceinline__ float silu_times(float v, float u) {
+    const Sigmoid s = sigmoid(v);
+    return v * s.qr * u * s.q;
+}
+
+// silu(v) * u of eight channels, where instructions count.  From -8 up the plain form is
+// as good: v * log2(e) is off by 1.22 |v| half steps (its rounding and its constant's),
+// the rest by 7, together 17.  (32768 x 2048 to E4M3: 61 us; the above for every element
+// 72; expf and a division 83.)
+__device__ __forceinline__ void silu_times(const float (&v)[8], const float (&u)[8],
+                                           float (&o)[8]) {
+    float low = v[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) low = fminf(low, v[i]);
+    if (low < -8.0f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = silu_times(v[i], u[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float e = __builtin_amdgcn_exp2f(v[i] * -1.44269504f);
+            o[i] = v[i] * __builtin_amdgcn_rcpf(1.0f + e) * u[i];
+        }
+    }
+}
 
 // Unsigned maximum over the 8 lanes of an aligned group of 8, with three DPP
 // moves (no LDS round trip): swap neighbours (quad_perm 1,0,3,2), swap pairs

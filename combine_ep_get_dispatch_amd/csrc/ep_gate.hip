@@ -88,17 +88,18 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(const GateArgs p) {
                 unpack8(df, d[j]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float s = sigmoid(gf[i]), si = gf[i] * s;
-                    // grad_y * up may pass fp32's range where the gradient does not
-                    o[i] = df[i] * __builtin_fmaf(si, 1.0f - s, s) * uf[i];
-                    e[i] = df[i] * si;
+                    // s + g s (1 - s) = s (1 + g r); q last: grad_y * up may pass fp32's
+                    // range where the gradient does not
+                    const Sigmoid s = sigmoid(gf[i]);
+                    const float w = __builtin_fmaf(gf[i] > 17.5f ? 17.5f : gf[i], s.r, 1.0f);
+                    o[i] = df[i] * (s.qr * w) * uf[i] * s.q;
+                    e[i] = df[i] * s.qr * gf[i] * s.q;
                 }
                 uint4* out = reinterpret_cast<uint4*>(p.y + (r0 + row[j]) * 2 * p.N);
                 store_nt(out + at[j], pack8(o));
                 store_nt(out + per + at[j], pack8(e));
             } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = silu(gf[i]) * uf[i];
+                silu_times(gf, uf, o);
                 if constexpr (KIND == kGateBf16) {
                     reinterpret_cast<uint4*>(p.y + (r0 + row[j]) * p.N)[at[j]] = pack8(o);
                 } else {

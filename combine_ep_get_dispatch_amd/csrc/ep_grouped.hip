@@ -662,7 +662,7 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductMemory<FP
                 if constexpr (SWIGLU) {
                     const f32x4 u = acc[ct + 2][rt];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = silu(v[i]) * u[i];
+                    for (int i = 0; i < 4; ++i) v[i] = silu_times(v[i], u[i]);
                 }
                 if constexpr (F32) {
                     f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(p.y) + at + c);
@@ -903,7 +903,7 @@ __device__ __forceinline__ void run_narrow(const ProductArgs& p, ProductMemory<F
         }
         if constexpr (SWIGLU) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = silu(v[i]) * u[i];
+            for (int i = 0; i < 4; ++i) v[i] = silu_times(v[i], u[i]);
         }
         const int r = rt * 16 + lr, c = t.m0 + ct * 16 + lg * 4;
         if (r < t.n && c < p.M)

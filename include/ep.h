@@ -549,7 +549,8 @@ ep_status_t ep_expert_linear_w4(const void *x, const float *x_scales, ep_dtype_t
  *   a[n]    = sum over i of x[r,i] * w[e,n,i]
  *   y[r,n]  = bf16(a[n]),                          n < N        (swiglu == 0)
  *   y[r,n]  = bf16(silu(a[n]) * a[N + n]),         n < N        (swiglu != 0)
- * accumulated in fp32, silu(v) = v / (1 + exp(-v)), rounded once.
+ * accumulated in fp32, silu(v) = v / (1 + exp(-v)) to 2^-20 of its value, rounded
+ * once.
  *   Rows of expert e, num_rows, expert_offsets, num_tokens_per_expert and
  *   capacity: as ep_expert_linear_w4.  Rows of no expert are left untouched in
  *   y, and nothing that they hold reaches another row.
@@ -610,8 +611,9 @@ ep_status_t ep_expert_linear_backward(const void *grad_y, const void *x, const v
  * The gated activation by itself, between two products whose first one's output
  * a training step keeps, or whose second one takes E4M3 rows:
  *   y[r,n] = silu(a[r,n]) * a[r,N+n],   n < N,
- * computed in fp32 from a = gate_up bf16 [num_rows*2N], for the rows of the
- * experts (as ep_expert_linear_w4 describes them), or for all num_rows rows if
+ * computed in fp32, to 17 * 2^-24 of its value (a gate below -174 counts as 0) ahead
+ * of its rounding, from a = gate_up bf16 [num_rows*2N], for the rows of the experts
+ * (as ep_expert_linear_w4 describes them), or for all num_rows rows if
  * num_tokens_per_expert is NULL (the arguments about experts are then ignored).
  * Other rows are left untouched.
  *   out_dtype EP_DTYPE_BF16 (N % 8 == 0): y bf16 [num_rows*N], rounded once.
