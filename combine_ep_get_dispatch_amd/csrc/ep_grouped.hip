@@ -687,6 +687,12 @@ __device__ __forceinline__ void run_tasks(const ProductArgs& p, ProductMemory<FP
     //   b's second (t + 1) in the second half's phase 1 of t, needed five later;
     // in one part, whose phases are as long:
     //   a(t + 2) and b(t + 2) in the halves' phase 1 of t, needed four and three later.
+    // A wait that the compiler counts.  Loads of its own that it holds for under way here
+    // (the narrow form's last ones, which nothing uses) it would wait for inside the steps,
+    // and so for the loads to LDS: as the code around it falls, for those of the step before
+    // or for those just asked for (8 experts x 100 rows, 7168 -> 2 x 2048, E4M3: 67 and 90 us,
+    // 66 with this).
+    __builtin_amdgcn_s_waitcnt(0x0f70);            // vmcnt(0)
     next.task = share.first;
     seek();
     if (group == 0) {
