@@ -177,14 +177,20 @@ struct Task {
     int64_t begin;          // first row of the run in the rows' arrays
 };
 
-// Tasks of 256 channels that run as eight times as many of 32 (us, as tasks of 256 / of
-// 32): as many as the workgroups take in one round, or in two where no expert has more
-// than 32 rows.  7168 -> 2 x 2048, E4M3, one expert x 1 row 51 / 15, x 64 rows 52 / 37;
-// 4 experts x 16 rows 52 / 35, x 64 rows (512 tasks of 32) 53 / 71; 2048 -> 7168, bf16,
-// one expert x 1 row 27 / 13, 2 x 16 rows 27 / 23, 2 x 64 rows 29 / 34, 4 x 4 rows (896
-// tasks of 32) 28 / 40.  One expert of more than 64 rows, in runs of 64, would lose: E4M3, 100 rows
-// 53 / 71, 200 rows 53 / 66, 500 rows 53 / 67.
-constexpr int kFewTasks = 32, kFewTasksOfFewRows = 64;
+// Tasks of 256 channels that run as eight times as many of 32: as many as the workgroups
+// take in one round, or in two where no expert has more than 32 rows and the waves have
+// three steps each or more.  Measured in us, as tasks of 256 / of 32:
+//   one round: 7168 -> 2 x 2048, E4M3, one expert x 1 row 51 / 15, x 64 rows 52 / 37,
+//   4 experts x 16 rows 52 / 35; 2048 -> 7168, bf16, one expert x 1 row 27 / 13, 2 x 16 rows
+//   27 / 23.  Of few steps, 32 tasks x 64 rows: E4M3 128 -> 2 x 4096 (1 step) 8.7 / 6.1, 1024
+//   (8 steps) 14.6 / 15.9, 2048 (16) 21.3 / 18.0; bf16 128 -> 8192 (2) 9.0 / 6.1, 1024 18.4 / 12.7.
+//   two rounds, 64 tasks x 32 rows: E4M3 512 (4 steps) 10.5 / 12.7, 1024 13.9 / 24.9, 2048 20.6 /
+//   27.7, 2560 (20) 24.1 / 25.4, 3584 (28) 30.3 / 28.1, 7168 62 / 55; bf16 512 (8) 12.4 / 17.2, 1024
+//   17.6 / 20.1, 1536 (24) 23.2 / 22.7, 2048 28.1 / 25.6.
+//   more: 4 experts x 64 rows (512 tasks of 32) 53 / 71, 2 x 64 rows bf16 29 / 34, 4 x 4 rows (896)
+//   28 / 40.  One expert of more than 64 rows, in runs of 64, would lose: E4M3, 100 rows
+//   53 / 71, 200 rows 53 / 66, 500 rows 53 / 67.
+constexpr int kFewTasks = 32, kFewTasksOfFewRows = 64, kStepsOfTwoRounds = 3 * kWaves;
 
 // Channel tiles whose tasks stand next to each other, so that the tasks an XCD has at hand
 // share rows as well as channels (65521 x 4096 -> 2048: 4 / 8 / 16 tiles 879 / 859 / 859 us).
@@ -974,6 +980,7 @@ __device__ __forceinline__ void run_product(const ProductArgs& p, ProductMemory<
         // (a y of 2^28 tasks fits no memory: such counts do not belong to these rows)
         if ((sum[0] + sum[1] + sum[2]) * nt >= 1 << 28) return;
         if constexpr (OP == kRows) {
+            few = few && p.K * (FP8 ? 1 : 2) > (kStepsOfTwoRounds - 1) * kStepBytes;
             if (sum[0] + sum[1] == 0 && sum[2] * nt <= (few ? kFewTasksOfFewRows : kFewTasks)) {
                 constexpr int kNarrow = SWIGLU ? 16 : 32;
                 const unsigned tiles = (p.M + kNarrow - 1) / kNarrow;

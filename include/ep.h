@@ -571,8 +571,9 @@ ep_status_t ep_expert_linear_w4(const void *x, const float *x_scales, ep_dtype_t
  *   No workspace, one launch.  Equal arguments give equal bits.  A row's results
  * are the same bits whatever rows stand beside it, but for one choice: where no
  * expert has more than 64 rows and there is little to do (up to 32 tiles of 256
- * weight channels by an expert's rows, 64 if no expert has more than 32 rows), a
- * sum is taken in eight shares, else channel by channel.
+ * weight channels by an expert's rows; 64 if no expert has more than 32 rows and a
+ * row of x more than 23 * 128 bytes), a sum is taken in eight shares, else channel
+ * by channel.
  *   (No page describes the experts themselves; the definitions of this call and
  * the next ones are this library's.)
  */
