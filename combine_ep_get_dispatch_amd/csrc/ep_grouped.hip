@@ -1045,9 +1045,12 @@ __global__ __launch_bounds__(kWaves * 64, 2) void gradients_kernel(const Product
     run_product<kGradWeight, false, false, F32, ADD>(weight, mem, slot);
 }
 
-// Workgroups for so many tasks, which may run in up to eight pieces each.
+// Workgroups for so many tasks: eight a task, which the narrow form's tiles of 32 channels
+// take, and at least four an XCD, for the pieces of its only task (256 rows, 4096 -> 256,
+// bf16: 78 us with one an XCD, 49 with four; E4M3 59 / 32).
 dim3 workgroups(int64_t tasks) {
-    return dim3((unsigned)((tasks * 8 < kCus ? tasks * 8 : kCus) + kXcds - 1) / kXcds * kXcds);
+    const int64_t want = tasks * 8 < 4 * kXcds ? 4 * kXcds : tasks * 8 < kCus ? tasks * 8 : kCus;
+    return dim3((unsigned)(want + kXcds - 1) / kXcds * kXcds);
 }
 
 template <Product OP, bool FP8, bool SWIGLU, bool F32, bool ADD>

@@ -4,7 +4,7 @@ import torch
 
 from combine_ep_get_dispatch_amd import binding as ep
 from parity import announce
-from test_gpu_expert_linear import device, gen
+from test_gpu_expert_linear import device, gen, ints
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +57,30 @@ def test_few_tasks_are_shared_and_near(I, fp8, tiles):
     terms = size * I ** 0.5
     tol = 2 * ((I + 8) * 2 * 2.0 ** -24 + (8 * 2.0 ** -13 if fp8 else 0)) * terms
     assert bool(((a - b).abs() <= tol + 2.0 ** -7 * a.abs()).all())
+
+
+@pytest.mark.parametrize("n", [65, 129, 200, 256, 300, 600])
+@pytest.mark.parametrize("I,N", [(256, 256), (520, 200), (72, 264), (1032, 520)])
+def test_one_to_nine_tasks_in_pieces(n, I, N):
+    """Calls of so few tasks that an XCD has one, whose rows its workgroups share: exact in
+    small integers."""
+    announce("expert_linear and gradients of %d rows %d -> %d" % (n, I, N))
+    g = gen(n + I)
+    x, w, gy = ints((n, I), g), ints((1, N, I), g, 2), ints((n, N), g, 2)
+    cnt, off = device([n], [0, n])
+    xb, wb, gb = (t.bfloat16().cuda() for t in (x, w, gy))
+    y = ep.expert_linear(xb, wb, cnt, expert_offsets=off)
+    assert torch.equal(y.cpu().double(), (x @ w[0].t()).bfloat16().double())
+    gx, gw = ep.expert_linear_backward(gb, xb, wb, cnt, expert_offsets=off,
+                                       grad_weight_dtype=torch.float32)
+    assert torch.equal(gx.cpu().double(), (gy @ w[0]).bfloat16().double())
+    assert torch.equal(gw[0].cpu().double(), gy.t() @ x)
+    only = ep.expert_linear_backward(gb, xb, None, cnt, expert_offsets=off,
+                                     grad_weight_dtype=torch.float32)[1]
+    assert torch.equal(only, gw)
+    if I % 128 == 0:
+        q = lambda t: t.float().to(torch.float8_e4m3fn).view(torch.uint8).cuda()
+        y8 = ep.expert_linear(q(x), q(w), cnt, expert_offsets=off,
+                              x_scales=torch.ones((n, I // 128), device="cuda"),
+                              weight_scales=torch.ones((1, (N + 127) // 128, I // 128), device="cuda"))
+        assert torch.equal(y8, y)
