@@ -38,7 +38,12 @@
 // address setting (loads between the matrix instructions instead: 1035 / 697); 861 / 576 with
 // what is left of the largest blocks in pieces; 852 / 565 with whole lines stored.  Tried
 // without gain: 32 x 32 matrix instructions (908), wave priorities, stores that the next
-// step does not wait for.
+// step does not wait for.  (E4M3, counted: the matrix units busy 41% of the cycles, bf16
+// 62; 5.7 other vector instructions a matrix instruction, four of them the scaling; 10%
+// more matrix instructions than the rows need, for blocks left part empty.)
+//
+// Not split: a sum over an expert's rows (gw).  Few tiles of many rows leave most of the
+// card idle: 65536 rows, 64 x 64 weights 866 us, 8 x 8192 rows, 512 x 512 123.
 #include "ep_internal.h"
 #include "ep_device.h"
 

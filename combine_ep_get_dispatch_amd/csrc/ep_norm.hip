@@ -8,8 +8,13 @@
 //   grad_h = inv * (gn - n * mean(gn * n)) + grad_residual,
 //   grad_weight = sum over tokens of grad_y * n.
 //
-// Both are bound by HBM: a row is read once, kept in registers across its sum,
-// and written once.
+// A row is read once, kept in registers across its sum, and written once, so both are
+// bound by HBM where a row fills its workgroup and fits its registers: 4.9-5.9 TB/s
+// of reads and writes forward from 512 channels on, 4.5-6.0 TB/s of the gradient at 1024
+// to 16384.  Beside that (in us, floor in brackets, with residuals): narrow rows leave most
+// of their workgroup idle, 65536 x 128 forward 26 (11), gradient 80 (11), whose workgroups
+// also take their rows one after the other; and the gradient of more than 16384 channels
+// keeps row and weight's sums in 412-436 bytes of scratch a lane, 1024 x 32768 190 (44).
 #include "ep_internal.h"
 #include "ep_device.h"
 

@@ -563,6 +563,7 @@ ep_status_t ep_expert_linear_w4(const void *x, const float *x_scales, ep_dtype_t
  *   128 x 128: channel n of the first N uses block n/128, channel N + n of the
  *   other half block ceil(N/128) + n/128; S = ceil(N/128), twice that with
  *   swiglu.  The codes' products are summed over 128 channels, then scaled.
+ *   A row's scale times a block's is expected inside fp32's normal range.
  *   (As in ep_expert_linear_w4 the matrix instructions align the products of
  *   neighbouring channels to the largest and cut them at 2^-13 of its power of
  *   two, ahead of the fp32 sums.)
